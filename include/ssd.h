@@ -246,6 +246,61 @@ ssd_status ssd_chunk_scan(const ssd_fwd_desc* desc, const void* X, const float* 
                           const void* B, const void* C, const float* states_in, void* Y,
                           void* stream);
 
+/* ---- Short causal convolution ----
+ *
+ * One filter of `width` taps per channel along the sequence, ahead of the
+ * scan in a layer that uses it.  With x' = x continued to the left by
+ * initial_window (its row width-2 is the step before the first; NULL = zeros):
+ *     pre[b][t][c] = bias[c] + sum_{k<width} weight[c][k] x'[b][t-(width-1)+k][c]
+ *     y = pre * sigmoid(pre) if silu, else pre.
+ * Sums are float32, y is rounded once to the call's dtype.
+ *   x        rows of `channels` consecutive elements; element (b, t, c) is at
+ *            b*x_bstride + t*x_rstride + c, so x may be a slice of wider rows
+ *   weight   [channels][width] float32; bias [channels] float32 or NULL
+ *   windows  [batch][width-1][channels], dtype of the call
+ *   seqlens  [batch] int32 on the device, or NULL: sequence b ends after
+ *            seqlens[b] steps (clamped to 0..seqlen).  Later rows of x (and dy)
+ *            are not read, those of y (and dx) are set to 0, and the final
+ *            window is that after the last step.
+ *   y, dy    npieces (1 to 3) arrays of their own: piece i is
+ *            [batch][seqlen][piece[i]], the piece widths adding up to
+ *            `channels` in order (X, B and C for the chunked scan, say).
+ * x, windows and pieces need the alignment of an element; wide accesses are
+ * used where addresses, strides and widths allow them.  Outputs must not
+ * overlap inputs or each other. */
+typedef struct ssd_conv_desc {
+    int64_t batch, seqlen, channels, width; /* width 2, 3 or 4 */
+    int64_t x_bstride, x_rstride;           /* elements, >= 0 */
+    int64_t piece[3];
+    int32_t npieces;
+    int32_t dtype; /* ssd_dtype */
+    int32_t silu;  /* 1 or 0 */
+    int32_t reserved; /* must be 0 */
+} ssd_conv_desc;
+
+/* final_window may be NULL. */
+ssd_status ssd_short_conv_fwd(const ssd_conv_desc* desc, const void* x, const float* weight,
+                              const float* bias, const void* initial_window, const int32_t* seqlens,
+                              void* const* y, void* final_window, void* stream);
+
+/* Gradients for the upstream dy and (NULL = zero) dfinal_window: dx
+ * [batch][seqlen][channels] dense, dweight and dbias float32 (dbias required
+ * exactly when bias is given), dinitial_window (may be NULL).  Sums over the
+ * batch and the sequence are formed in a fixed order (repeated calls give the
+ * same bits); the workspace holds their parts. */
+ssd_status ssd_short_conv_bwd_workspace_bytes(const ssd_conv_desc* desc, size_t* bytes);
+ssd_status ssd_short_conv_bwd(const ssd_conv_desc* desc, const void* x, const float* weight,
+                              const float* bias, const void* initial_window, const int32_t* seqlens,
+                              const void* const* dy, const void* dfinal_window, void* dx,
+                              float* dweight, float* dbias, void* dinitial_window, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* One token: y from `window` and x (row b at b*x_bstride; seqlen must be 1),
+ * after which the window, updated in place, holds the last width-1 inputs.
+ * y pieces are [batch][piece[i]]. */
+ssd_status ssd_short_conv_step(const ssd_conv_desc* desc, void* window, const void* x,
+                               const float* weight, const float* bias, void* const* y, void* stream);
+
 /* Static description of a status code. */
 const char* ssd_status_str(ssd_status s);
 /* Detail of the calling thread's most recent error ("" if none). */

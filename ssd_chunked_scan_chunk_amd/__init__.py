@@ -1,5 +1,5 @@
-"""MI355X (gfx950) SSD layer: chunked forward, its backward, and the recurrent
-decode step.
+"""MI355X (gfx950) SSD layer: chunked forward, its backward, the recurrent
+decode step, and the operators around them (the short causal convolution).
 
 A thin torch binding over libssd.so's C ABI (include/ssd.h).  This module
 only marshals arguments -- checks every tensor's shape, dtype, device and
@@ -25,7 +25,8 @@ from ._lib import (SSD_ALGO_AUTO, SSD_ALGO_MFMA, SSD_ALGO_VALU, SSD_BF16, SSD_F3
 
 __all__ = ["chunk_scan_fwd", "chunk_scan_fwd_noalloc", "chunk_scan_bwd", "bwd_workspace_bytes", "bwd_da_workspace_bytes", "bwd_da", "step", "stream_rmw", "chunk_cumsum", "chunk_state", "state_passing",
            "chunk_scan", "fwd_plan", "workspace_bytes", "SSDError", "SSD_ALGO_AUTO",
-           "SSD_ALGO_MFMA", "SSD_ALGO_VALU", "library_path"]
+           "SSD_ALGO_MFMA", "SSD_ALGO_VALU", "library_path", "short_conv_fwd", "short_conv_bwd",
+           "short_conv_bwd_workspace_bytes", "short_conv_step"]
 
 
 def library_path() -> str:
@@ -386,3 +387,8 @@ def chunk_scan(X, a, B, C, chunk, states_in=None, seg_chunks=1, Y=None, wg_units
     _lib.check(_L().ssd_chunk_scan(ctypes.byref(d), _ptr(X), _ptr(a), _ptr(B), _ptr(C),
                                    _ptr(states_in), _ptr(Y), _stream(X.device)))
     return Y
+
+
+# the operators around the chunked scan (they use the checks above)
+from .layer import (short_conv_bwd, short_conv_bwd_workspace_bytes,  # noqa: E402
+                    short_conv_fwd, short_conv_step)

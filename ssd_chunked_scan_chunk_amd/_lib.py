@@ -31,7 +31,8 @@ EXPORTS = (
     "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan",
     "ssd_status_str", "ssd_last_error", "ssd_version", "ssd_bwd_workspace_bytes",
     "ssd_chunk_scan_bwd", "ssd_bwd_da_workspace_bytes", "ssd_bwd_da", "ssd_chunk_scan_fwd_noalloc",
-    "ssd_stream_rmw",
+    "ssd_stream_rmw", "ssd_short_conv_fwd", "ssd_short_conv_bwd_workspace_bytes", "ssd_short_conv_bwd",
+    "ssd_short_conv_step",
 )
 SSD_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -50,6 +51,14 @@ class StepDesc(ctypes.Structure):
                 ("headdim", ctypes.c_int64), ("dstate", ctypes.c_int64),
                 ("ngroups", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class ConvDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("x_bstride", ctypes.c_int64), ("x_rstride", ctypes.c_int64),
+                ("piece", ctypes.c_int64 * 3), ("npieces", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("silu", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class SSDError(RuntimeError):
@@ -87,7 +96,13 @@ def load(path: str = LIB_PATH):
     lib.ssd_bwd_da_workspace_bytes.argtypes = [pd, ctypes.POINTER(sz)]
     lib.ssd_bwd_da.argtypes = [pd, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.ssd_stream_rmw.argtypes = [vp, ctypes.c_int64, ctypes.c_float, i32, i32, vp]
-    for f in ("ssd_fwd_workspace_bytes", "ssd_fwd_plan", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_noalloc",
+    pc, pp = ctypes.POINTER(ConvDesc), ctypes.POINTER(vp)
+    lib.ssd_short_conv_fwd.argtypes = [pc, vp, vp, vp, vp, vp, pp, vp, vp]
+    lib.ssd_short_conv_bwd_workspace_bytes.argtypes = [pc, ctypes.POINTER(sz)]
+    lib.ssd_short_conv_bwd.argtypes = [pc, vp, vp, vp, vp, vp, pp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.ssd_short_conv_step.argtypes = [pc, vp, vp, vp, vp, pp, vp]
+    for f in ("ssd_short_conv_fwd", "ssd_short_conv_bwd_workspace_bytes", "ssd_short_conv_bwd", "ssd_short_conv_step",
+              "ssd_fwd_workspace_bytes", "ssd_fwd_plan", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_noalloc",
               "ssd_step",
               "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan",
               "ssd_bwd_workspace_bytes", "ssd_chunk_scan_bwd", "ssd_bwd_da_workspace_bytes", "ssd_bwd_da",

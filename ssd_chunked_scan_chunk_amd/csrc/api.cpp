@@ -947,3 +947,5 @@ ssd_status ssd_bwd_da(const ssd_fwd_desc* desc, const void* X, const float* a, c
 }
 
 }  // extern "C"
+
+#include "api_layer.hpp"

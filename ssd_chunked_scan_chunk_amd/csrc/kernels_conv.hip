@@ -1,0 +1,529 @@
+// kernels_conv.hip -- the short causal convolution on gfx950: forward,
+// backward and the single-token step.
+//
+// One filter of W taps (2..4) per channel along the sequence,
+//     pre[t] = bias + sum_k w[k] x'[t - (W-1) + k],   y = silu(pre) or pre,
+// with x' continued to the left by a window or zeros.  About one flop per byte:
+// bound by HBM.  A thread owns 16 bytes of consecutive channels (or one channel
+// where rows do not allow wide accesses) and walks `rows` steps with the last
+// W-1 inputs in registers, so every input row is read once but for the W-1 rows
+// ahead of each walk; a wavefront's accesses are one contiguous run.
+//
+// Backward, with dpre[t] = dy[t] act'(pre[t]) (0 outside the sequence):
+//     dx[t] = sum_k w[k] dpre[t + W-1 - k],  dw[k] = sum_t dpre[t] x'[t-(W-1)+k],
+//     dbias = sum_t dpre[t].
+// The walk recomputes pre, keeps the last W-1 dpre in registers and runs W-1
+// steps past its rows to finish their dx.  dw and dbias are summed in registers
+// along the walk, over the workgroup's four wavefronts in LDS, and over the
+// workgroups by a second kernel in a fixed order.
+#include "layer_launch.hpp"
+#include "ssd_device.hpp"
+
+namespace ssd {
+
+namespace {
+
+constexpr int kWaves = kConvWaves;   // consecutive in time
+
+struct ConvArgs {
+    int64_t L, C, xb, xr;
+    int64_t end0, end1;      // first channels of the second and third piece
+    int64_t pw[3];
+    int64_t rows;            // steps of one wavefront's walk
+    unsigned cblocks, tblocks;
+};
+
+template <typename T, int V> struct Row {   // V elements of a row, as stored
+    T v[V];
+};
+template <> struct Row<u16, 8> { uint4 v; };
+template <> struct Row<float, 4> { float4 v; };
+
+template <typename T, int V> __device__ __forceinline__ Row<T, V> load_row(const T* p) {
+    Row<T, V> r;
+    if constexpr (V == 1) r.v[0] = *p;
+    else r.v = *reinterpret_cast<const decltype(r.v)*>(p);
+    return r;
+}
+template <typename T, int V> __device__ __forceinline__ Row<T, V> zero_row() {
+    Row<T, V> r;
+    if constexpr (V == 1) r.v[0] = 0;
+    else if constexpr (V == 8) r.v = make_uint4(0, 0, 0, 0);
+    else r.v = make_float4(0.f, 0.f, 0.f, 0.f);
+    return r;
+}
+template <int V> __device__ __forceinline__ void widen(const Row<float, V>& r, float* f) {
+    if constexpr (V == 1) f[0] = r.v[0];
+    else { f[0] = r.v.x; f[1] = r.v.y; f[2] = r.v.z; f[3] = r.v.w; }
+}
+template <int V> __device__ __forceinline__ void widen(const Row<u16, V>& r, float* f) {
+    if constexpr (V == 1) {
+        f[0] = bf_bits_to_f32(r.v[0]);
+    } else {
+        const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+template <int V> __device__ __forceinline__ void store_row(float* p, const float* f) {
+    if constexpr (V == 1) *p = f[0];
+    else *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+template <int V> __device__ __forceinline__ void store_row(u16* p, const float* f) {
+    if constexpr (V == 1) {
+        *p = f32_to_bf_bits(f[0]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (uint32_t)f32_to_bf_bits(f[2 * i]) | ((uint32_t)f32_to_bf_bits(f[2 * i + 1]) << 16);
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+template <typename T, int V> __device__ __forceinline__ void store_raw(T* p, const Row<T, V>& r) {
+    if constexpr (V == 1) *p = r.v[0];
+    else *reinterpret_cast<decltype(r.v)*>(p) = r.v;
+}
+
+// V * W consecutive filter taps and V biases (16-byte aligned when V > 1)
+template <int V, int W>
+__device__ __forceinline__ void load_filter(const float* __restrict__ weight, const float* __restrict__ bias,
+                                            int64_t c, float (&w)[V][W], float (&bs)[V]) {
+    float* wf = &w[0][0];
+    if constexpr (V == 1) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) wf[k] = weight[c * W + k];
+        bs[0] = bias ? bias[c] : 0.f;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * W / 4; ++i) {
+            const float4 q = reinterpret_cast<const float4*>(weight + c * W)[i];
+            wf[4 * i] = q.x; wf[4 * i + 1] = q.y; wf[4 * i + 2] = q.z; wf[4 * i + 3] = q.w;
+        }
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float4 q = bias ? reinterpret_cast<const float4*>(bias + c)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+            bs[4 * i] = q.x; bs[4 * i + 1] = q.y; bs[4 * i + 2] = q.z; bs[4 * i + 3] = q.w;
+        }
+    }
+}
+
+__device__ __forceinline__ float sigmoid(float v) {
+    return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * v));
+}
+
+// the piece that holds channel c, its row width and c's place in it
+template <typename P> struct Pieces { P p[3]; };
+template <typename P>
+__device__ __forceinline__ P piece_of(const ConvArgs& a, const Pieces<P>& y, int64_t c, int64_t* width, int64_t* at) {
+    const bool p1 = c >= a.end0, p2 = c >= a.end1;
+    *width = p2 ? a.pw[2] : p1 ? a.pw[1] : a.pw[0];
+    *at = c - (p2 ? a.end1 : p1 ? a.end0 : 0);
+    return p2 ? y.p[2] : p1 ? y.p[1] : y.p[0];
+}
+
+__device__ __forceinline__ int64_t length_of(const int32_t* lens, int64_t b, int64_t L) {
+    if (!lens) return L;
+    const int64_t n = lens[b];
+    return n < 0 ? 0 : n > L ? L : n;
+}
+
+// x' at step t - (W-1) .. t - 1 as stored: the window (or zeros) left of the
+// sequence; steps at or past n are not read
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_history(const T* xc, int64_t xr, const T* win0, int64_t C, int64_t t, int64_t n,
+                                             Row<T, V> (&h)[W - 1]) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) {
+        const int64_t s = t - (W - 1) + j;
+        h[j] = zero_row<T, V>();
+        if (s >= 0) { if (s < n) h[j] = load_row<T, V>(xc + s * xr); }
+        else if (win0) h[j] = load_row<T, V>(win0 + (s + W - 1) * C);
+    }
+}
+
+template <typename T, int V, int W, bool SILU>
+__global__ __launch_bounds__(64 * kWaves) void k_conv_fwd(ConvArgs a, const T* __restrict__ x,
+                                                          const float* __restrict__ weight,
+                                                          const float* __restrict__ bias,
+                                                          const T* __restrict__ win0,
+                                                          const int32_t* __restrict__ lens, Pieces<T*> y,
+                                                          T* __restrict__ win1)
+{
+    constexpr int U = 8;   // rows in flight
+    const unsigned cb = blockIdx.x % a.cblocks, tb = blockIdx.x / a.cblocks;
+    const int64_t b = blockIdx.y;
+    const int64_t c = ((int64_t)cb * 64 + (threadIdx.x & 63)) * V;
+    const int64_t t0 = ((int64_t)tb * kWaves + (threadIdx.x >> 6)) * a.rows;
+    if (c >= a.C || (t0 >= a.L && t0 > 0)) return;
+    const int64_t t1 = t0 + a.rows < a.L ? t0 + a.rows : a.L;
+    const int64_t n = length_of(lens, b, a.L);
+    const int64_t te = t1 < n ? t1 : n;      // steps t0 .. te are computed, te .. t1 are zero
+    const T* xc = x + b * a.xb + c;
+    const T* w0 = win0 ? win0 + b * (W - 1) * a.C + c : nullptr;
+    int64_t pw, pc;
+    T* yp = piece_of(a, y, c, &pw, &pc);
+    yp += b * a.L * pw + pc;
+
+    float w[V][W], bs[V];
+    load_filter<V, W>(weight, bias, c, w, bs);
+    Row<T, V> hist[W - 1];
+    load_history<T, V, W>(xc, a.xr, w0, a.C, t0, n, hist);
+    float xf[W][V];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) widen<V>(hist[j], xf[j]);
+
+    for (int64_t t = t0; t < te; t += U) {
+        Row<T, V> in[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (t + j < te) in[j] = load_row<T, V>(xc + (t + j) * a.xr);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (t + j < te) {
+                widen<V>(in[j], xf[W - 1]);
+                float o[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float s = bs[v];
+#pragma unroll
+                    for (int k = 0; k < W; ++k) s = fmaf(w[v][k], xf[k][v], s);
+                    o[v] = SILU ? s * sigmoid(s) : s;
+                }
+                store_row<V>(yp + (t + j) * pw, o);
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) xf[k][v] = xf[k + 1][v];
+            }
+        }
+    }
+    const float zero[V] = {};
+    for (int64_t t = te > t0 ? te : t0; t < t1; ++t) store_row<V>(yp + t * pw, zero);
+    // the walk that reaches the sequence's end holds its last W-1 inputs
+    if (win1 && ((te == n && te > t0) || (n == 0 && t0 == 0))) {
+        T* w1 = win1 + b * (W - 1) * a.C + c;
+        // xf[j] is exactly representable: it was widened from T
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) store_row<V>(w1 + j * a.C, xf[j]);
+    }
+}
+
+template <typename T, int V, int W, bool SILU>
+__global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvArgs a, const T* __restrict__ x,
+                                                          const float* __restrict__ weight,
+                                                          const float* __restrict__ bias,
+                                                          const T* __restrict__ win0,
+                                                          const int32_t* __restrict__ lens, Pieces<const T*> dy,
+                                                          const T* __restrict__ dwin1, T* __restrict__ dx,
+                                                          T* __restrict__ dwin0, float* __restrict__ parts)
+{
+    constexpr int U = 4;   // rows in flight
+    constexpr int NA = V * (W + 1);
+    __shared__ float red[(kWaves - 1) * NA * 64];
+    const unsigned cb = blockIdx.x % a.cblocks, tb = blockIdx.x / a.cblocks;
+    const int64_t b = blockIdx.y;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t c = ((int64_t)cb * 64 + lane) * V;
+    const int64_t t0 = ((int64_t)tb * kWaves + wave) * a.rows;
+    float dw[V][W] = {}, db[V] = {};
+    if (c < a.C && (t0 < a.L || t0 == 0)) {
+        const int64_t t1 = t0 + a.rows < a.L ? t0 + a.rows : a.L;
+        const int64_t n = length_of(lens, b, a.L);
+        const T* xc = x + b * a.xb + c;
+        const T* w0 = win0 ? win0 + b * (W - 1) * a.C + c : nullptr;
+        const T* g1 = dwin1 ? dwin1 + b * (W - 1) * a.C + c : nullptr;
+        T* g0 = dwin0 ? dwin0 + b * (W - 1) * a.C + c : nullptr;
+        T* dxc = dx + b * a.L * a.C + c;
+        int64_t pw, pc;
+        const T* dyp = piece_of(a, dy, c, &pw, &pc);
+        dyp += b * a.L * pw + pc;
+
+        float w[V][W], bs[V];
+        load_filter<V, W>(weight, bias, c, w, bs);
+        Row<T, V> hist[W - 1];
+        load_history<T, V, W>(xc, a.xr, w0, a.C, t0, n, hist);
+        float xf[W][V], dp[W][V] = {};
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) widen<V>(hist[j], xf[j]);
+
+        const int64_t tlast = t1 + W - 1;
+        for (int64_t t = t0; t < tlast; t += U) {
+            Row<T, V> in[U], gin[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                in[j] = gin[j] = zero_row<T, V>();
+                if (t + j < n && t + j < tlast) {
+                    in[j] = load_row<T, V>(xc + (t + j) * a.xr);
+                    gin[j] = load_row<T, V>(dyp + (t + j) * pw);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int64_t r = t + j;
+                if (r >= tlast) break;
+                float g[V], o[V];
+                widen<V>(in[j], xf[W - 1]);
+                widen<V>(gin[j], g);
+                const bool own = r < t1;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float d = g[v];
+                    if constexpr (SILU) {
+                        float s = bs[v];
+#pragma unroll
+                        for (int k = 0; k < W; ++k) s = fmaf(w[v][k], xf[k][v], s);
+                        const float sg = sigmoid(s);
+                        d *= sg * fmaf(s, 1.f - sg, 1.f);
+                    }
+                    d = r < n ? d : 0.f;
+                    dp[W - 1][v] = d;
+                    if (own) {
+                        db[v] += d;
+#pragma unroll
+                        for (int k = 0; k < W; ++k) dw[v][k] = fmaf(d, xf[k][v], dw[v][k]);
+                    }
+                    // row r of the sequence with its window ahead: steps r-(W-1) .. r
+                    float s = 0.f;
+#pragma unroll
+                    for (int k = 0; k < W; ++k) s = fmaf(w[v][k], dp[W - 1 - k][v], s);
+                    o[v] = s;
+                }
+                if (g1 && r >= n && r < n + W - 1) {
+                    float e[V];
+                    widen<V>(load_row<T, V>(g1 + (r - n) * a.C), e);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) o[v] += e[v];
+                }
+                if (r >= t0 + W - 1) store_row<V>(dxc + (r - (W - 1)) * a.C, o);
+                else if (t0 == 0 && g0) store_row<V>(g0 + r * a.C, o);
+#pragma unroll
+                for (int k = 0; k < W - 1; ++k)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) { xf[k][v] = xf[k + 1][v]; dp[k][v] = dp[k + 1][v]; }
+            }
+        }
+    }
+    // sum over the workgroup's wavefronts, in their order
+    if (wave > 0) {
+        float* q = red + (wave - 1) * NA * 64 + lane;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) q[(k * V + v) * 64] = dw[v][k];
+            q[(W * V + v) * 64] = db[v];
+        }
+    }
+    __syncthreads();
+    if (wave == 0 && c < a.C) {
+        float* out = parts + ((int64_t)b * a.tblocks + tb) * (W + 1) * a.C + c;
+#pragma unroll
+        for (int k = 0; k <= W; ++k) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float s = k < W ? dw[v][k < W ? k : 0] : db[v];
+#pragma unroll
+                for (int q = 0; q < kWaves - 1; ++q) s += red[(q * NA + k * V + v) * 64 + lane];
+                out[(int64_t)k * a.C + v] = s;
+            }
+        }
+    }
+}
+
+// dweight and dbias from the workgroups' parts [np][W + 1][C]: a workgroup
+// sums 64 columns, its wavefronts every kWaves-th part, in a fixed order
+__global__ __launch_bounds__(64 * kWaves) void k_conv_sum(const float* __restrict__ parts, int64_t np, int64_t C,
+                                                          int W, float* __restrict__ dweight,
+                                                          float* __restrict__ dbias)
+{
+    __shared__ float red[kWaves][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t col = (int64_t)blockIdx.x * 64 + lane, cols = (int64_t)(W + 1) * C;
+    float s = 0.f;
+    if (col < cols) {
+        int64_t p = wave;
+        for (; p + 3 * kWaves < np; p += 4 * kWaves) {
+            const float v0 = parts[p * cols + col], v1 = parts[(p + kWaves) * cols + col];
+            const float v2 = parts[(p + 2 * kWaves) * cols + col], v3 = parts[(p + 3 * kWaves) * cols + col];
+            s += (v0 + v1) + (v2 + v3);
+        }
+        for (; p < np; p += kWaves) s += parts[p * cols + col];
+    }
+    red[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && col < cols) {
+        s = red[0][lane];
+#pragma unroll
+        for (int q = 1; q < kWaves; ++q) s += red[q][lane];
+        const int64_t k = col / C, c = col - k * C;
+        if (k < W) dweight[c * W + k] = s;
+        else if (dbias) dbias[c] = s;
+    }
+}
+
+template <typename T, int V, int W, bool SILU>
+__global__ __launch_bounds__(256) void k_conv_step(ConvArgs a, T* __restrict__ window, const T* __restrict__ x,
+                                                   const float* __restrict__ weight, const float* __restrict__ bias,
+                                                   Pieces<T*> y, int64_t items)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, cv = a.C / V;
+    if (i >= items) return;
+    const int64_t b = i / cv, c = (i - b * cv) * V;
+    T* wp = window + b * (W - 1) * a.C + c;
+    Row<T, V> in[W];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) in[k] = load_row<T, V>(wp + k * a.C);
+    in[W - 1] = load_row<T, V>(x + b * a.xb + c);
+    float w[V][W], o[V];
+    load_filter<V, W>(weight, bias, c, w, o);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        float f[V];
+        widen<V>(in[k], f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = fmaf(w[v][k], f[v], o[v]);
+    }
+    if constexpr (SILU) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] *= sigmoid(o[v]);
+    }
+    int64_t pw, pc;
+    T* yp = piece_of(a, y, c, &pw, &pc);
+    store_row<V>(yp + b * pw + pc, o);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) store_raw<T, V>(wp + k * a.C, in[k + 1]);
+}
+
+ConvArgs args_of(const ConvShape& s, int vec, int64_t rows) {
+    ConvArgs a;
+    a.L = s.L; a.C = s.C; a.xb = s.xb; a.xr = s.xr;
+    a.end0 = s.piece[1] ? s.piece[0] : s.C;
+    a.end1 = s.piece[2] ? s.piece[0] + s.piece[1] : s.C;
+    for (int i = 0; i < 3; ++i) a.pw[i] = s.piece[i];
+    a.rows = rows;
+    a.cblocks = (unsigned)((s.C + 64 * vec - 1) / (64 * vec));
+    a.tblocks = (unsigned)conv_time_blocks(s, rows);
+    return a;
+}
+
+// run f(T, V, W, SILU) for the shape's types and sizes
+template <typename T, int V, typename F> hipError_t by_width(const ConvShape& s, F f) {
+    if (s.silu) {
+        if (s.W == 4) return f.template go<T, V, 4, true>();
+        if (s.W == 3) return f.template go<T, V, 3, true>();
+        return f.template go<T, V, 2, true>();
+    }
+    if (s.W == 4) return f.template go<T, V, 4, false>();
+    if (s.W == 3) return f.template go<T, V, 3, false>();
+    return f.template go<T, V, 2, false>();
+}
+template <typename F> hipError_t by_type(const ConvShape& s, int vec, F f) {
+    if (s.bf16) return vec > 1 ? by_width<u16, 8>(s, f) : by_width<u16, 1>(s, f);
+    return vec > 1 ? by_width<float, 4>(s, f) : by_width<float, 1>(s, f);
+}
+
+template <typename T, typename P> Pieces<T> pieces_of(const ConvShape& s, const P* y) {
+    Pieces<T> p;
+    for (int i = 0; i < 3; ++i) p.p[i] = s.piece[i] ? (T)y[i] : nullptr;
+    return p;
+}
+
+struct FwdCall {
+    const ConvShape& s;
+    ConvArgs a;
+    const void* x;
+    const float *weight, *bias;
+    const void* win0;
+    const int32_t* lens;
+    void* const* y;
+    void* win1;
+    hipStream_t st;
+    template <typename T, int V, int W, bool SILU> hipError_t go() {
+        hipLaunchKernelGGL((k_conv_fwd<T, V, W, SILU>), dim3(a.cblocks * a.tblocks, (unsigned)s.Bz), dim3(64 * kWaves),
+                           0, st, a, (const T*)x, weight, bias, (const T*)win0, lens, (pieces_of<T*>(s, y)), (T*)win1);
+        return hipGetLastError();
+    }
+};
+struct BwdCall {
+    const ConvShape& s;
+    ConvArgs a;
+    const void* x;
+    const float *weight, *bias;
+    const void* win0;
+    const int32_t* lens;
+    const void* const* dy;
+    const void* dwin1;
+    void *dx, *dwin0;
+    float* parts;
+    hipStream_t st;
+    template <typename T, int V, int W, bool SILU> hipError_t go() {
+        hipLaunchKernelGGL((k_conv_bwd<T, V, W, SILU>), dim3(a.cblocks * a.tblocks, (unsigned)s.Bz), dim3(64 * kWaves),
+                           0, st, a, (const T*)x, weight, bias, (const T*)win0, lens, (pieces_of<const T*>(s, dy)),
+                           (const T*)dwin1, (T*)dx, (T*)dwin0, parts);
+        return hipGetLastError();
+    }
+};
+struct StepCall {
+    const ConvShape& s;
+    ConvArgs a;
+    void* window;
+    const void* x;
+    const float *weight, *bias;
+    void* const* y;
+    hipStream_t st;
+    template <typename T, int V, int W, bool SILU> hipError_t go() {
+        const int64_t items = s.Bz * (s.C / V);
+        hipLaunchKernelGGL((k_conv_step<T, V, W, SILU>), dim3((unsigned)((items + 255) / 256)), dim3(256), 0, st, a,
+                           (T*)window, (const T*)x, weight, bias, (pieces_of<T*>(s, y)), items);
+        return hipGetLastError();
+    }
+};
+
+}  // namespace
+
+int conv_vec(const ConvShape& s, const void* x, const void* window, const void* const* y, const void* dx,
+             const void* params, const void* params2)
+{
+    const int vec = s.bf16 ? 8 : 4;
+    auto wide = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    bool ok = wide(x) && wide(window) && wide(dx) && wide(params) && wide(params2) && s.C % vec == 0 &&
+              s.xr % vec == 0 && s.xb % vec == 0;
+    for (int i = 0; i < 3; ++i)
+        if (s.piece[i]) ok = ok && s.piece[i] % vec == 0 && wide(y[i]);
+    return ok ? vec : 1;
+}
+
+hipError_t launch_conv_fwd(const ConvShape& s, const void* x, const float* weight, const float* bias,
+                           const void* win0, const int32_t* lens, void* const* y, void* win1, hipStream_t st)
+{
+    int vec = conv_vec(s, x, win0, y, win1, weight, bias);
+    return by_type(s, vec, FwdCall{s, args_of(s, vec, conv_rows(s, false)), x, weight, bias, win0, lens, y, win1, st});
+}
+
+hipError_t launch_conv_bwd(const ConvShape& s, const void* x, const float* weight, const float* bias,
+                           const void* win0, const int32_t* lens, const void* const* dy, const void* dwin1,
+                           void* dx, float* dweight, float* dbias, void* dwin0, float* parts, hipStream_t st)
+{
+    int vec = conv_vec(s, x, win0, dy, dx, weight, bias);
+    const uintptr_t rest = reinterpret_cast<uintptr_t>(dwin0) | reinterpret_cast<uintptr_t>(dwin1);
+    if (rest % 16 != 0) vec = 1;
+    hipError_t e = by_type(s, vec, BwdCall{s, args_of(s, vec, conv_rows(s, true)), x, weight, bias, win0, lens,
+                                           dy, dwin1, dx, dwin0, parts, st});
+    if (e != hipSuccess) return e;
+    const int64_t cols = (s.W + 1) * s.C;
+    hipLaunchKernelGGL(k_conv_sum, dim3((unsigned)((cols + 63) / 64)), dim3(64 * kWaves), 0, st, parts,
+                       conv_bwd_parts(s), s.C, s.W, dweight, dbias);
+    return hipGetLastError();
+}
+
+hipError_t launch_conv_step(const ConvShape& s, void* window, const void* x, const float* weight,
+                            const float* bias, void* const* y, hipStream_t st)
+{
+    const int vec = conv_vec(s, x, window, y, nullptr, weight, bias);
+    return by_type(s, vec, StepCall{s, args_of(s, vec, 1), window, x, weight, bias, y, st});
+}
+
+}  // namespace ssd

@@ -2,6 +2,7 @@
 // shapes each kernel family takes and how the forward MFMA kernel groups
 // heads into workgroups.  Host code only (no kernels), so the C ABI's
 // planning can also be built and checked without a GPU toolchain.
+#include "layer_launch.hpp"
 #include "ssd_launch.hpp"
 
 namespace ssd {
@@ -36,5 +37,16 @@ int64_t cb_tiles_bytes(const FwdShape& s) {
     const int64_t nI = s.Q / 32;
     return s.Bz * s.nc * s.G * (nI * (nI + 1) / 2) * 1024 * 4;
 }
+
+int64_t conv_rows(const ConvShape& s, bool bwd) {
+    (void)s;
+    (void)bwd;
+    return 32;
+}
+int64_t conv_time_blocks(const ConvShape& s, int64_t rows) {
+    const int64_t n = (s.L + kConvWaves * rows - 1) / (kConvWaves * rows);
+    return n > 0 ? n : 1;
+}
+int64_t conv_bwd_parts(const ConvShape& s) { return s.Bz * conv_time_blocks(s, conv_rows(s, true)); }
 
 }  // namespace ssd

@@ -1,0 +1,182 @@
+"""The operators around the chunked scan: the short causal convolution.
+
+Like the rest of the package these only check arguments, allocate outputs and
+workspace and pass pointers to libssd.so.  Inputs that a layer cuts out of a
+projection's rows (x here) may be views: their rows have to be
+dense, the strides between rows and batches are free.  Parameters, states and
+upstream gradients are contiguous.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _L, _check, _check_bytes, _dtype_code, _lib
+
+_P = ctypes.c_void_p * 3
+
+
+def _rows(name, t, shape, dense, dtype, device):
+    """Check a tensor of ``shape`` whose last ``dense`` dimensions are dense and
+    return the strides of the leading ones."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s is required" % name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype != dtype:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    strides, want = t.stride(), 1
+    for k in range(1, dense + 1):
+        if strides[-k] != want and t.shape[-k] > 1:
+            raise ValueError("the rows of %s must be contiguous" % name)
+        want *= t.shape[-k]
+    return strides[:t.dim() - dense]
+
+
+def _need(name, t):
+    if t is None:
+        raise ValueError("%s is required" % name)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _seqlens(seqlens, Bz, device):
+    if seqlens is not None and not isinstance(seqlens, torch.Tensor):
+        raise TypeError("seqlens must be a torch.Tensor on the GPU")
+    _check("seqlens", seqlens, (Bz,), torch.int32, device)
+
+
+def _enqueue(device, fn, *args):
+    """Call an entry point with the current stream of the tensors' device, that
+    device being the current one."""
+    if device.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        _lib.check(fn(*args, stream))
+    else:
+        with torch.cuda.device(device):
+            _lib.check(fn(*args, stream))
+
+
+# ---- short causal convolution ------------------------------------------------------
+
+def _conv_check(x, weight, bias, silu, pieces, lead):
+    """(desc, pieces) of a convolution of x [*lead, channels]."""
+    if not isinstance(x, torch.Tensor) or x.dim() != lead + 1:
+        raise ValueError("x must be a %d-D tensor [batch, %schannels]" % (lead + 1, "seqlen, " if lead == 2 else ""))
+    code, C = _dtype_code(x), x.shape[-1]
+    strides = _rows("x", x, x.shape, 1, x.dtype, x.device)
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a 2-D tensor [channels, width]")
+    _check("weight", weight, (C, weight.shape[1]), torch.float32, x.device)
+    _check("bias", bias, (C,), torch.float32, x.device)
+    given = (C,) if pieces is None else tuple(int(w) for w in pieces)
+    if not 1 <= len(given) <= 3 or min(given) < 1 or sum(given) != C:
+        raise ValueError("pieces must be one to three widths that add up to the %d channels, got %s" % (C, given))
+    d = _lib.ConvDesc(x.shape[0], x.shape[1] if lead == 2 else 1, C, weight.shape[1], strides[0],
+                      strides[1] if lead == 2 else 0, given + (0,) * (3 - len(given)), len(given), code,
+                      int(bool(silu)), 0)
+    return d, given
+
+
+def _conv_outputs(x, given, pieces, y):
+    """The y pieces to write, as a tuple, and what the caller gets back."""
+    lead = tuple(x.shape[:-1])
+    if y is None:
+        ys = tuple(torch.empty(lead + (w,), dtype=x.dtype, device=x.device) for w in given)
+        return ys, ys[0] if pieces is None else ys
+    ys = (y,) if pieces is None else tuple(y)
+    _conv_given("y", ys, lead, given, x)
+    return ys, y
+
+
+def _conv_given(name, ts, lead, given, x):
+    if len(ts) != len(given):
+        raise ValueError("%s has %d pieces, expected %d" % (name, len(ts), len(given)))
+    for i, (t, w) in enumerate(zip(ts, given)):
+        label = name if len(given) == 1 else "%s[%d]" % (name, i)
+        _need(label, t)
+        _check(label, t, lead + (w,), x.dtype, x.device)
+
+
+def short_conv_fwd(x, weight, bias=None, initial_window=None, seqlens=None, silu=True, pieces=None,
+                   return_final_window=False, y=None, final_window=None):
+    """Causal convolution of every channel along the sequence, then SiLU.
+
+    x [Bz,L,C] (bf16 or f32, rows dense), weight [C,W] f32 with W 2 to 4, bias
+    [C] f32, initial_window [Bz,W-1,C] in x's dtype: the inputs before the first
+    step (None: zeros).  seqlens [Bz] int32 on the GPU: sequence b has that many
+    steps; later rows of x are not read and those of y are 0.  pieces: widths
+    that add up to C; y is then a tuple of contiguous [Bz,L,width] tensors (X,
+    B and C for chunk_scan_fwd, after a view).  Returns (y, final_window or None):
+    the window [Bz,W-1,C] continues the sequence here or in short_conv_step."""
+    d, given = _conv_check(x, weight, bias, silu, pieces, 2)
+    Bz, C, W = x.shape[0], x.shape[2], weight.shape[1]
+    _check("initial_window", initial_window, (Bz, W - 1, C), x.dtype, x.device)
+    _check("final_window", final_window, (Bz, W - 1, C), x.dtype, x.device)
+    _seqlens(seqlens, Bz, x.device)
+    ys, back = _conv_outputs(x, given, pieces, y)
+    if final_window is None and return_final_window:
+        final_window = torch.empty((Bz, max(W - 1, 0), C), dtype=x.dtype, device=x.device)
+    _enqueue(x.device, _L().ssd_short_conv_fwd, d, _at(x), _at(weight), _at(bias), _at(initial_window), _at(seqlens),
+             _P(*map(_at, ys)), _at(final_window))
+    return back, final_window
+
+
+def short_conv_bwd_workspace_bytes(x, weight) -> int:
+    d, _ = _conv_check(x, weight, None, True, None, 2)
+    n = ctypes.c_size_t()
+    _lib.check(_L().ssd_short_conv_bwd_workspace_bytes(d, n))
+    return n.value
+
+
+def short_conv_bwd(x, weight, dy, bias=None, initial_window=None, dfinal_window=None, seqlens=None, silu=True,
+                   return_dinitial_window=False, workspace=None):
+    """Gradients of short_conv_fwd for upstream dy (one contiguous tensor, or a
+    tuple of the forward's pieces) and dfinal_window (None: zero).
+
+    Returns a dict with dx [Bz,L,C] and dinitial_window (x's dtype; None unless
+    requested), dweight and dbias (f32; dbias None without a bias)."""
+    several = isinstance(dy, (tuple, list))
+    if not several:
+        _need("dy", dy)
+    dys = tuple(dy) if several else (dy,)
+    if several and not all(isinstance(t, torch.Tensor) and t.dim() == 3 for t in dys):
+        raise ValueError("the pieces of dy must be 3-D tensors")
+    d, given = _conv_check(x, weight, bias, silu, [t.shape[2] for t in dys] if several else None, 2)
+    Bz, L, C = x.shape
+    W = weight.shape[1]
+    _conv_given("dy", dys, (Bz, L), given, x)
+    _check("initial_window", initial_window, (Bz, W - 1, C), x.dtype, x.device)
+    _check("dfinal_window", dfinal_window, (Bz, W - 1, C), x.dtype, x.device)
+    _seqlens(seqlens, Bz, x.device)
+    n = ctypes.c_size_t()
+    _lib.check(_L().ssd_short_conv_bwd_workspace_bytes(d, n))
+    _check_bytes("workspace", workspace, n.value, x.device)
+    if workspace is None and n.value > 0:
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=x.device)
+    wsz = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    dx = torch.empty((Bz, L, C), dtype=x.dtype, device=x.device)
+    dweight = torch.empty_like(weight)
+    dbias = torch.empty_like(bias) if bias is not None else None
+    dwin = torch.empty((Bz, W - 1, C), dtype=x.dtype, device=x.device) if return_dinitial_window else None
+    _enqueue(x.device, _L().ssd_short_conv_bwd, d, _at(x), _at(weight), _at(bias), _at(initial_window), _at(seqlens),
+             _P(*map(_at, dys)), _at(dfinal_window), _at(dx), _at(dweight), _at(dbias), _at(dwin), _at(workspace), wsz)
+    return {"dx": dx, "dweight": dweight, "dbias": dbias, "dinitial_window": dwin}
+
+
+def short_conv_step(window, x, weight, bias=None, silu=True, pieces=None, y=None):
+    """One token: x [Bz,C] (rows dense) against window [Bz,W-1,C], which is
+    updated in place.  Returns y [Bz,C], or its pieces as a tuple."""
+    d, given = _conv_check(x, weight, bias, silu, pieces, 1)
+    _need("window", window)
+    _check("window", window, (x.shape[0], weight.shape[1] - 1, x.shape[1]), x.dtype, x.device)
+    ys, back = _conv_outputs(x, given, pieces, y)
+    _enqueue(x.device, _L().ssd_short_conv_step, d, _at(window), _at(x), _at(weight), _at(bias), _P(*map(_at, ys)))
+    return back

@@ -3,6 +3,7 @@
 // That build exercises argument validation and planning on the CPU; every
 // call it is given fails validation or is host-only, so none of these should
 // run.  If one does, it reports hipErrorNotSupported instead of launching.
+#include "layer_launch.hpp"
 #include "ssd_launch.hpp"
 
 extern "C" const char* hipGetErrorString(hipError_t) { return "stub launcher (host-only build)"; }
@@ -63,5 +64,12 @@ hipError_t launch_bwd_da(const FwdShape&, const void*, const void*, const float*
 hipError_t launch_cb_tiles(const CbJob&, hipStream_t) { SSD_STUB; }
 hipError_t launch_fill_zero(float*, int64_t, hipStream_t) { SSD_STUB; }
 hipError_t launch_copy_f32(float*, const float*, int64_t, hipStream_t) { SSD_STUB; }
+hipError_t launch_conv_fwd(const ConvShape&, const void*, const float*, const float*, const void*, const int32_t*,
+                           void* const*, void*, hipStream_t) { SSD_STUB; }
+hipError_t launch_conv_bwd(const ConvShape&, const void*, const float*, const float*, const void*, const int32_t*,
+                           const void* const*, const void*, void*, float*, float*, void*, float*,
+                           hipStream_t) { SSD_STUB; }
+hipError_t launch_conv_step(const ConvShape&, void*, const void*, const float*, const float*, void* const*,
+                            hipStream_t) { SSD_STUB; }
 #undef SSD_STUB
 }  // namespace ssd

@@ -1,0 +1,140 @@
+"""Argument checks of the operators around the chunked scan, in the binding and
+behind the C ABI, on the CPU: nothing here launches a kernel."""
+import ctypes
+
+import pytest
+import torch
+
+import ssd_chunked_scan_chunk_amd as ssd
+from ssd_chunked_scan_chunk_amd import _lib
+
+Bz, L, C, W = 2, 10, 24, 4
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def conv_args(**kw):
+    d = dict(x=torch.zeros(Bz, L, C, dtype=BF), weight=torch.zeros(C, W), bias=torch.zeros(C),
+             initial_window=torch.zeros(Bz, W - 1, C, dtype=BF), seqlens=torch.zeros(Bz, dtype=torch.int32))
+    d.update(kw)
+    return d
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(x=torch.zeros(L, C, dtype=BF)), "3-D"),
+    (dict(x=torch.zeros(Bz, C, L, dtype=BF).transpose(1, 2)), "rows of x"),
+    (dict(weight=torch.zeros(C)), "2-D"),
+    (dict(weight=torch.zeros(C - 1, W)), "weight has shape"),
+    (dict(weight=torch.zeros(C, W, dtype=BF)), "weight has dtype"),
+    (dict(bias=torch.zeros(C + 1)), "bias has shape"),
+    (dict(initial_window=torch.zeros(Bz, W, C, dtype=BF)), "initial_window has shape"),
+    (dict(initial_window=torch.zeros(Bz, W - 1, C)), "initial_window has dtype"),
+    (dict(seqlens=torch.zeros(Bz, dtype=torch.int64)), "seqlens has dtype"),
+    (dict(seqlens=torch.zeros(Bz + 1, dtype=torch.int32)), "seqlens has shape"),
+    (dict(pieces=(20, 3)), "pieces must be"),
+    (dict(pieces=(6, 6, 6, 6)), "pieces must be"),
+    (dict(pieces=(24, 0)), "pieces must be"),
+    (dict(y=torch.zeros(Bz, L, C)), "y has dtype"),
+    (dict(pieces=(20, 4), y=(torch.zeros(Bz, L, 20, dtype=BF),)), "y has 1 pieces"),
+    (dict(), "on the GPU"),
+])
+def test_conv_fwd(kw, match):
+    with pytest.raises(ValueError, match=match):
+        ssd.short_conv_fwd(**conv_args(**kw))
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(dy=None), "dy is required"),
+    (dict(dy=torch.zeros(Bz, L, C)), "dy has dtype"),
+    (dict(dy=torch.zeros(Bz, L, C - 1, dtype=BF)), "dy has shape"),
+    (dict(dy=(torch.zeros(Bz, L, C - 1, dtype=BF), torch.zeros(Bz, L, 2, dtype=BF))), "pieces must be"),
+    (dict(dfinal_window=torch.zeros(Bz, W - 1, C)), "dfinal_window has dtype"),
+    (dict(workspace=torch.zeros(8, dtype=torch.uint8)), "workspace holds"),
+])
+def test_conv_bwd(kw, match):
+    d = conv_args()
+    d.setdefault("dy", torch.zeros(Bz, L, C, dtype=BF))
+    d.update(kw)
+    with pytest.raises(ValueError, match=match):
+        ssd.short_conv_bwd(**d)
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(window=None), "window is required"),
+    (dict(window=torch.zeros(Bz, W, C, dtype=BF)), "window has shape"),
+    (dict(x=torch.zeros(Bz, 1, C, dtype=BF)), "2-D"),
+])
+def test_conv_step(kw, match):
+    d = dict(window=torch.zeros(Bz, W - 1, C, dtype=BF), x=torch.zeros(Bz, C, dtype=BF), weight=torch.zeros(C, W))
+    d.update(kw)
+    with pytest.raises(ValueError, match=match):
+        ssd.short_conv_step(**d)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.load()
+
+
+def conv_desc(**kw):
+    d = dict(batch=2, seqlen=100, channels=64, width=4, x_bstride=6400, x_rstride=64, piece=(64, 0, 0), npieces=1,
+             dtype=_lib.SSD_BF16, silu=1, reserved=0)
+    d.update(kw)
+    return _lib.ConvDesc(*[d[k] for k in ("batch", "seqlen", "channels", "width", "x_bstride", "x_rstride", "piece",
+                                          "npieces", "dtype", "silu", "reserved")])
+
+
+P = [ctypes.c_void_p(1 << k) for k in range(20, 44)]   # aligned, far apart, never dereferenced
+
+
+def pieces(*p):
+    return (ctypes.c_void_p * 3)(*p)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=-1), _lib.SSD_ERR_SHAPE), (dict(channels=0), _lib.SSD_ERR_SHAPE),
+    (dict(width=1), _lib.SSD_ERR_UNSUPPORTED), (dict(width=5), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(dtype=3), _lib.SSD_ERR_DTYPE), (dict(silu=2), _lib.SSD_ERR_SHAPE), (dict(reserved=1), _lib.SSD_ERR_SHAPE),
+    (dict(npieces=0), _lib.SSD_ERR_SHAPE), (dict(npieces=4), _lib.SSD_ERR_SHAPE),
+    (dict(piece=(60, 0, 0)), _lib.SSD_ERR_SHAPE), (dict(piece=(60, 4, 0)), _lib.SSD_ERR_SHAPE),
+    (dict(piece=(65, -1, 0), npieces=2), _lib.SSD_ERR_SHAPE),
+    (dict(x_rstride=-64), _lib.SSD_ERR_SHAPE), (dict(x_rstride=1 << 62), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(x_bstride=1 << 62), _lib.SSD_ERR_UNSUPPORTED), (dict(batch=1 << 40), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(seqlen=1 << 50), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(seqlen=1 << 31, channels=1 << 24, piece=(1 << 24, 0, 0)), _lib.SSD_ERR_UNSUPPORTED),
+])
+def test_conv_abi_shapes(lib, kw, code):
+    d, n = conv_desc(**kw), ctypes.c_size_t()
+    assert lib.ssd_short_conv_fwd(d, P[0], P[1], None, None, None, pieces(P[2]), None, None) == code
+    assert lib.ssd_last_error() != b""
+    assert lib.ssd_short_conv_bwd_workspace_bytes(d, n) == code
+
+
+def test_conv_abi_pointers(lib):
+    d, n = conv_desc(), ctypes.c_size_t()
+    fwd = lambda x=P[0], w=P[1], b=None, w0=None, ls=None, y=pieces(P[2]), w1=None, d=d: \
+        lib.ssd_short_conv_fwd(d, x, w, b, w0, ls, y, w1, None)
+    assert fwd(x=None) == fwd(w=None) == fwd(y=pieces()) == _lib.SSD_ERR_NULL
+    assert lib.ssd_short_conv_fwd(None, P[0], P[1], None, None, None, pieces(P[2]), None, None) == _lib.SSD_ERR_NULL
+    odd = ctypes.c_void_p((1 << 20) + 1)
+    assert fwd(x=odd) == fwd(w=odd) == fwd(y=pieces(odd)) == fwd(w0=odd) == fwd(ls=odd) == _lib.SSD_ERR_ALIGN
+    assert fwd(y=pieces(P[0])) == fwd(w1=P[2]) == fwd(w0=P[3], w1=P[3]) == _lib.SSD_ERR_ALIAS
+    two = conv_desc(piece=(32, 32, 0), npieces=2)
+    assert fwd(y=pieces(P[2]), d=two) == _lib.SSD_ERR_NULL
+    assert fwd(y=pieces(P[2], P[2]), d=two) == _lib.SSD_ERR_ALIAS
+    # nothing to do: no launch
+    assert fwd(d=conv_desc(batch=0), x=None) == fwd(d=conv_desc(seqlen=0), x=None) == _lib.SSD_OK
+
+    assert lib.ssd_short_conv_bwd_workspace_bytes(d, n) == 0 and n.value >= 2 * 5 * 64 * 4
+    bwd = lambda dy=pieces(P[2]), b=None, dx=P[3], dw=P[4], db=None, ws=P[5], wsz=n.value, d=d: \
+        lib.ssd_short_conv_bwd(d, P[0], P[1], b, None, None, dy, None, dx, dw, db, None, ws, wsz, None)
+    assert bwd(dy=pieces()) == bwd(dx=None) == bwd(dw=None) == bwd(b=P[6]) == bwd(db=P[6]) == _lib.SSD_ERR_NULL
+    assert bwd(ws=None) == bwd(wsz=n.value - 1) == _lib.SSD_ERR_WORKSPACE
+    assert bwd(ws=ctypes.c_void_p((1 << 25) + 4)) == _lib.SSD_ERR_ALIGN
+    assert bwd(dx=P[0]) == bwd(dw=P[3]) == bwd(ws=P[3]) == _lib.SSD_ERR_ALIAS
+
+    one = conv_desc(seqlen=1)
+    step = lambda w=P[3], y=pieces(P[2]), d=one: lib.ssd_short_conv_step(d, w, P[0], P[1], None, y, None)
+    assert step(d=d) == _lib.SSD_ERR_SHAPE
+    assert step(w=None) == _lib.SSD_ERR_NULL
+    assert step(w=P[0]) == step(y=pieces(P[0])) == _lib.SSD_ERR_ALIAS
+    assert step(d=conv_desc(batch=0, seqlen=1)) == _lib.SSD_OK
