@@ -301,6 +301,52 @@ ssd_status ssd_short_conv_bwd(const ssd_conv_desc* desc, const void* x, const fl
 ssd_status ssd_short_conv_step(const ssd_conv_desc* desc, void* window, const void* x,
                                const float* weight, const float* bias, void* const* y, void* stream);
 
+/* ---- Scan with a decay of its own for every channel and state ----
+ *
+ *     dt = softplus(delta + delta_bias) if softplus, else delta + delta_bias
+ *     h[t][c][n] = exp(dt[t][c] A[c][n]) h[t-1][c][n] + dt[t][c] u[t][c] B[t][g][n]
+ *     y[t][c] = (sum_n h[t][c][n] C[t][g][n] + skip[c] u[t][c]) * silu(gate[t][c])
+ * per batch, with g = c * ngroups / channels (ssd_chunk_scan_fwd's recurrence has one
+ * decay per head).  States, exponents and sums are float32; y is rounded once.
+ *   u, delta, gate   rows of `channels` elements at b*bstride + t*rstride
+ *   B, C             rows of ngroups*dstate elements, likewise strided
+ *   A                [channels][dstate] float32; skip, delta_bias [channels]
+ *                    float32 or NULL (zero); gate NULL: no gating
+ *   states           [batch][channels][dstate] float32
+ *   seqlens          as for the convolution: later rows are not read, y and the
+ *                    gradients' rows there are 0, the final state is the one
+ *                    after the last step
+ *   y, dy            [batch][seqlen][channels] dense
+ * dstate is 1 to 64.  u, delta, gate, B, C, y and the gradients need the
+ * alignment of an element.  Outputs must not overlap inputs, each other or
+ * the workspace. */
+typedef struct ssd_channel_desc {
+    int64_t batch, seqlen, channels, dstate, ngroups;
+    int64_t u_bstride, u_rstride, delta_bstride, delta_rstride, gate_bstride, gate_rstride;
+    int64_t B_bstride, B_rstride, C_bstride, C_rstride; /* elements, >= 0 */
+    int32_t dtype;    /* ssd_dtype of u, delta, gate, B, C, y and their gradients */
+    int32_t softplus; /* 1 or 0 */
+} ssd_channel_desc;
+
+/* initial_state NULL = zero; final_state may be NULL.  Where few channels
+ * leave the GPU idle the sequence is split into segments, whose end states
+ * the workspace holds (0 bytes for a single segment). */
+ssd_status ssd_channel_scan_fwd_workspace_bytes(const ssd_channel_desc* desc, size_t* bytes);
+ssd_status ssd_channel_scan_fwd(const ssd_channel_desc* desc, const void* u, const void* delta,
+                                const float* A, const void* B, const void* C, const float* skip,
+                                const void* gate, const float* delta_bias,
+                                const float* initial_state, const int32_t* seqlens, void* y,
+                                float* final_state, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* One token: state [batch][channels][dstate] is updated in place and y
+ * [batch][channels] written; rows of u, delta, gate, B and C are at
+ * b*bstride (seqlen must be 1). */
+ssd_status ssd_channel_step(const ssd_channel_desc* desc, float* state, const void* u,
+                            const void* delta, const float* A, const void* B, const void* C,
+                            const float* skip, const void* gate, const float* delta_bias, void* y,
+                            void* stream);
+
 /* Static description of a status code. */
 const char* ssd_status_str(ssd_status s);
 /* Detail of the calling thread's most recent error ("" if none). */

@@ -1,5 +1,6 @@
 """MI355X (gfx950) SSD layer: chunked forward, its backward, the recurrent
-decode step, and the operators around them (the short causal convolution).
+decode step, and the operators around them (the short causal convolution and the
+scan with one decay per channel and state).
 
 A thin torch binding over libssd.so's C ABI (include/ssd.h).  This module
 only marshals arguments -- checks every tensor's shape, dtype, device and
@@ -26,7 +27,8 @@ from ._lib import (SSD_ALGO_AUTO, SSD_ALGO_MFMA, SSD_ALGO_VALU, SSD_BF16, SSD_F3
 __all__ = ["chunk_scan_fwd", "chunk_scan_fwd_noalloc", "chunk_scan_bwd", "bwd_workspace_bytes", "bwd_da_workspace_bytes", "bwd_da", "step", "stream_rmw", "chunk_cumsum", "chunk_state", "state_passing",
            "chunk_scan", "fwd_plan", "workspace_bytes", "SSDError", "SSD_ALGO_AUTO",
            "SSD_ALGO_MFMA", "SSD_ALGO_VALU", "library_path", "short_conv_fwd", "short_conv_bwd",
-           "short_conv_bwd_workspace_bytes", "short_conv_step"]
+           "short_conv_bwd_workspace_bytes", "short_conv_step", "channel_scan_fwd",
+           "channel_scan_fwd_workspace_bytes", "channel_step"]
 
 
 def library_path() -> str:
@@ -390,5 +392,6 @@ def chunk_scan(X, a, B, C, chunk, states_in=None, seg_chunks=1, Y=None, wg_units
 
 
 # the operators around the chunked scan (they use the checks above)
-from .layer import (short_conv_bwd, short_conv_bwd_workspace_bytes,  # noqa: E402
-                    short_conv_fwd, short_conv_step)
+from .layer import (channel_scan_fwd, channel_scan_fwd_workspace_bytes,  # noqa: E402
+                    channel_step, short_conv_bwd, short_conv_bwd_workspace_bytes, short_conv_fwd,
+                    short_conv_step)

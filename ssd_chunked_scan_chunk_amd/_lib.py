@@ -32,7 +32,7 @@ EXPORTS = (
     "ssd_status_str", "ssd_last_error", "ssd_version", "ssd_bwd_workspace_bytes",
     "ssd_chunk_scan_bwd", "ssd_bwd_da_workspace_bytes", "ssd_bwd_da", "ssd_chunk_scan_fwd_noalloc",
     "ssd_stream_rmw", "ssd_short_conv_fwd", "ssd_short_conv_bwd_workspace_bytes", "ssd_short_conv_bwd",
-    "ssd_short_conv_step",
+    "ssd_short_conv_step", "ssd_channel_scan_fwd_workspace_bytes", "ssd_channel_scan_fwd", "ssd_channel_step",
 )
 SSD_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -59,6 +59,13 @@ class ConvDesc(ctypes.Structure):
                 ("x_bstride", ctypes.c_int64), ("x_rstride", ctypes.c_int64),
                 ("piece", ctypes.c_int64 * 3), ("npieces", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("silu", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ChannelDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("batch", "seqlen", "channels", "dstate", "ngroups", "u_bstride", "u_rstride", "delta_bstride",
+                 "delta_rstride", "gate_bstride", "gate_rstride", "B_bstride", "B_rstride", "C_bstride",
+                 "C_rstride")] + [("dtype", ctypes.c_int32), ("softplus", ctypes.c_int32)]
 
 
 class SSDError(RuntimeError):
@@ -101,7 +108,11 @@ def load(path: str = LIB_PATH):
     lib.ssd_short_conv_bwd_workspace_bytes.argtypes = [pc, ctypes.POINTER(sz)]
     lib.ssd_short_conv_bwd.argtypes = [pc, vp, vp, vp, vp, vp, pp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.ssd_short_conv_step.argtypes = [pc, vp, vp, vp, vp, pp, vp]
-    for f in ("ssd_short_conv_fwd", "ssd_short_conv_bwd_workspace_bytes", "ssd_short_conv_bwd", "ssd_short_conv_step",
+    ph = ctypes.POINTER(ChannelDesc)
+    lib.ssd_channel_scan_fwd_workspace_bytes.argtypes = [ph, ctypes.POINTER(sz)]
+    lib.ssd_channel_scan_fwd.argtypes = [ph] + [vp] * 13 + [sz, vp]
+    lib.ssd_channel_step.argtypes = [ph] + [vp] * 11
+    for f in ("ssd_channel_scan_fwd_workspace_bytes", "ssd_channel_scan_fwd", "ssd_channel_step", "ssd_short_conv_fwd", "ssd_short_conv_bwd_workspace_bytes", "ssd_short_conv_bwd", "ssd_short_conv_step",
               "ssd_fwd_workspace_bytes", "ssd_fwd_plan", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_noalloc",
               "ssd_step",
               "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan",

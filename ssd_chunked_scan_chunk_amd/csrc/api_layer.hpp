@@ -1,5 +1,5 @@
 // api_layer.hpp -- the C ABI of the operators around the chunked scan: the
-// short causal convolution.  Included once, at the end of api.cpp, whose error
+// short causal convolution and the per-channel scan.  Included once, at the end of api.cpp, whose error
 // state and range checks it shares.
 #include "layer_launch.hpp"
 
@@ -98,6 +98,75 @@ ssd_status check_pieces(const ssd::ConvShape& s, const char* name, const void* c
     return SSD_OK;
 }
 
+ssd_status chan_shape(const ssd_channel_desc* d, ssd::ChanShape* s) {
+    if (!d) return fail(SSD_ERR_NULL, "desc is NULL");
+    if (d->batch < 0 || d->seqlen < 0 || d->channels < 1 || d->dstate < 1 || d->ngroups < 1)
+        return fail(SSD_ERR_SHAPE,
+                    "sizes must be batch>=0, seqlen>=0, channels,dstate,ngroups>=1 (got %lld,%lld,%lld,%lld,%lld)",
+                    (long long)d->batch, (long long)d->seqlen, (long long)d->channels, (long long)d->dstate,
+                    (long long)d->ngroups);
+    if (d->channels % d->ngroups != 0)
+        return fail(SSD_ERR_SHAPE, "channels (%lld) must be a multiple of ngroups (%lld)", (long long)d->channels,
+                    (long long)d->ngroups);
+    if (d->dtype != SSD_F32 && d->dtype != SSD_BF16)
+        return fail(SSD_ERR_DTYPE, "dtype %d is not SSD_F32 or SSD_BF16", (int)d->dtype);
+    if (d->softplus != 0 && d->softplus != 1) return fail(SSD_ERR_SHAPE, "softplus must be 0 or 1");
+    if (d->dstate > 64)
+        return fail(SSD_ERR_UNSUPPORTED, "dstate must be at most 64 (got %lld)", (long long)d->dstate);
+    if (d->batch > 65535 || d->seqlen > ((int64_t)1 << 31) || d->channels > ((int64_t)1 << 20) ||
+        d->batch * d->seqlen > kMaxSize / d->channels)
+        return fail(SSD_ERR_UNSUPPORTED, "sizes beyond the supported range");
+    SSD_CHECK(check_stride("u", d->batch, d->u_bstride, d->seqlen, d->u_rstride));
+    SSD_CHECK(check_stride("delta", d->batch, d->delta_bstride, d->seqlen, d->delta_rstride));
+    SSD_CHECK(check_stride("gate", d->batch, d->gate_bstride, d->seqlen, d->gate_rstride));
+    SSD_CHECK(check_stride("B", d->batch, d->B_bstride, d->seqlen, d->B_rstride));
+    SSD_CHECK(check_stride("C", d->batch, d->C_bstride, d->seqlen, d->C_rstride));
+    // the per-state kernels launch a thread for every (batch, channel, state)
+    if (d->batch * d->channels * 64 >= ((int64_t)1 << 32))
+        return fail(SSD_ERR_UNSUPPORTED, "batch*channels too large for one launch");
+    s->Bz = d->batch; s->L = d->seqlen; s->D = d->channels; s->N = d->dstate; s->G = d->ngroups;
+    s->ub = d->u_bstride; s->ur = d->u_rstride; s->db = d->delta_bstride; s->dr = d->delta_rstride;
+    s->zb = d->gate_bstride; s->zr = d->gate_rstride;
+    s->Bb = d->B_bstride; s->Br = d->B_rstride; s->Cb = d->C_bstride; s->Cr = d->C_rstride;
+    s->bf16 = d->dtype == SSD_BF16; s->softplus = d->softplus == 1;
+    return SSD_OK;
+}
+
+// u .. seqlens: present and aligned; their ranges go to r[0 .. 9]
+constexpr int kChanIn = 10;
+ssd_status check_chan_in(const ssd::ChanShape& s, const ssd::ChanIn& in, Range* r) {
+    const int64_t es = s.bf16 ? 2 : 4;
+    if (!in.A || (s.Bz > 0 && s.L > 0 && (!in.u || !in.delta || !in.B || !in.C)))
+        return fail(SSD_ERR_NULL, "u, delta, A, B and C are required");
+    SSD_CHECK(check_aligned("u", in.u, es));
+    SSD_CHECK(check_aligned("delta", in.delta, es));
+    SSD_CHECK(check_aligned("gate", in.gate, es));
+    SSD_CHECK(check_aligned("B", in.B, es));
+    SSD_CHECK(check_aligned("C", in.C, es));
+    SSD_CHECK(check_aligned("A", in.A, 4));
+    SSD_CHECK(check_aligned("skip", in.skip, 4));
+    SSD_CHECK(check_aligned("delta_bias", in.dbias, 4));
+    SSD_CHECK(check_aligned("initial_state", in.h0, 4));
+    SSD_CHECK(check_aligned("seqlens", in.lens, 4));
+    r[0] = rng("u", in.u, span_bytes(s.Bz, s.L, s.D, s.ub, s.ur, es));
+    r[1] = rng("delta", in.delta, span_bytes(s.Bz, s.L, s.D, s.db, s.dr, es));
+    r[2] = rng("gate", in.gate, span_bytes(s.Bz, s.L, s.D, s.zb, s.zr, es));
+    r[3] = rng("B", in.B, span_bytes(s.Bz, s.L, s.G * s.N, s.Bb, s.Br, es));
+    r[4] = rng("C", in.C, span_bytes(s.Bz, s.L, s.G * s.N, s.Cb, s.Cr, es));
+    r[5] = rng("A", in.A, s.D * s.N * 4);
+    r[6] = rng("skip", in.skip, s.D * 4);
+    r[7] = rng("delta_bias", in.dbias, s.D * 4);
+    r[8] = rng("initial_state", in.h0, s.Bz * s.D * s.N * 4);
+    r[9] = rng("seqlens", in.lens, s.Bz * 4);
+    return SSD_OK;
+}
+
+ssd_status check_workspace(const void* ws, size_t have, size_t need) {
+    if (need > 0 && (!ws || have < need))
+        return fail(SSD_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu%s)", need, have, ws ? "" : ", NULL");
+    return need > 0 ? check_aligned("workspace", ws, 16) : SSD_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -159,10 +228,7 @@ ssd_status ssd_short_conv_bwd(const ssd_conv_desc* desc, const void* x, const fl
     SSD_CHECK(check_aligned("dbias", dbias, 4));
     SSD_CHECK(check_aligned("dinitial_window", dinitial_window, es));
     const size_t need = conv_bwd_bytes(s);
-    if (need > 0 && (!workspace || workspace_bytes < need))
-        return fail(SSD_ERR_WORKSPACE, "workspace needs %zu bytes (got %zu%s)", need, workspace_bytes,
-                    workspace ? "" : ", NULL");
-    SSD_CHECK(check_aligned("workspace", workspace, 16));
+    SSD_CHECK(check_workspace(workspace, workspace_bytes, need));
     Range in[9];
     SSD_CHECK(check_pieces(s, "dy", dy, in));
     in[3] = rng("x", x, span_bytes(s.Bz, s.L, s.C, s.xb, s.xr, es));
@@ -206,6 +272,59 @@ ssd_status ssd_short_conv_step(const ssd_conv_desc* desc, void* window, const vo
     SSD_CHECK(check_disjoint(out, 4, in, 3));
     const hipError_t e = ssd::launch_conv_step(s, window, x, weight, bias, y, reinterpret_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : hip_fail(e, "convolution step launch");
+}
+
+ssd_status ssd_channel_scan_fwd_workspace_bytes(const ssd_channel_desc* desc, size_t* bytes) {
+    if (!bytes) return fail(SSD_ERR_NULL, "bytes is NULL");
+    ssd::ChanShape s;
+    SSD_CHECK(chan_shape(desc, &s));
+    *bytes = ssd::chan_fwd_bytes(s, ssd::chan_fwd_plan(s));
+    return ok();
+}
+
+ssd_status ssd_channel_scan_fwd(const ssd_channel_desc* desc, const void* u, const void* delta, const float* A,
+                                const void* B, const void* C, const float* skip, const void* gate,
+                                const float* delta_bias, const float* initial_state, const int32_t* seqlens, void* y,
+                                float* final_state, void* workspace, size_t workspace_bytes, void* stream) {
+    ssd::ChanShape s;
+    SSD_CHECK(chan_shape(desc, &s));
+    const ssd::ChanIn in{u, delta, B, C, gate, A, skip, delta_bias, initial_state, seqlens};
+    Range r[kChanIn];
+    SSD_CHECK(check_chan_in(s, in, r));
+    const int64_t es = s.bf16 ? 2 : 4;
+    if (!y && s.Bz > 0 && s.L > 0) return fail(SSD_ERR_NULL, "y is required");
+    SSD_CHECK(check_aligned("y", y, es));
+    SSD_CHECK(check_aligned("final_state", final_state, 4));
+    const ssd::ChanPlan p = ssd::chan_fwd_plan(s);
+    const size_t need = ssd::chan_fwd_bytes(s, p);
+    SSD_CHECK(check_workspace(workspace, workspace_bytes, need));
+    const Range out[] = {rng("y", y, s.Bz * s.L * s.D * es), rng("final_state", final_state, s.Bz * s.D * s.N * 4),
+                         rng("workspace", workspace, (int64_t)need)};
+    SSD_CHECK(check_disjoint(out, 3, r, kChanIn));
+    if (s.Bz == 0 || (s.L == 0 && !final_state)) return ok();
+    const hipError_t e = ssd::launch_chan_fwd(s, p, in, y, final_state, need > 0 ? static_cast<float*>(workspace) : nullptr,
+                                              reinterpret_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "per-channel scan launch");
+}
+
+ssd_status ssd_channel_step(const ssd_channel_desc* desc, float* state, const void* u, const void* delta,
+                            const float* A, const void* B, const void* C, const float* skip, const void* gate,
+                            const float* delta_bias, void* y, void* stream) {
+    ssd::ChanShape s;
+    SSD_CHECK(chan_shape(desc, &s));
+    if (s.L != 1) return fail(SSD_ERR_SHAPE, "seqlen must be 1 (got %lld)", (long long)s.L);
+    const ssd::ChanIn in{u, delta, B, C, gate, A, skip, delta_bias, nullptr, nullptr};
+    Range r[kChanIn];
+    SSD_CHECK(check_chan_in(s, in, r));
+    if (s.Bz == 0) return ok();
+    const int64_t es = s.bf16 ? 2 : 4;
+    if (!state || !y) return fail(SSD_ERR_NULL, "state and y are required");
+    SSD_CHECK(check_aligned("state", state, 4));
+    SSD_CHECK(check_aligned("y", y, es));
+    const Range out[] = {rng("y", y, s.Bz * s.D * es), rng("state", state, s.Bz * s.D * s.N * 4)};
+    SSD_CHECK(check_disjoint(out, 2, r, kChanIn));
+    const hipError_t e = ssd::launch_chan_step(s, state, in, y, reinterpret_cast<hipStream_t>(stream));
+    return e == hipSuccess ? ok() : hip_fail(e, "per-channel step launch");
 }
 
 }  // extern "C"

@@ -30,4 +30,28 @@ hipError_t launch_conv_bwd(const ConvShape& s, const void* x, const float* weigh
 hipError_t launch_conv_step(const ConvShape& s, void* window, const void* x, const float* weight,
                             const float* bias, void* const* y, hipStream_t st);
 
+// ---- per-channel scan (kernels_channel.hip) --------------------------------------
+struct ChanShape {
+    int64_t Bz, L, D, N, G;
+    int64_t ub, ur, db, dr, zb, zr, Bb, Br, Cb, Cr;   // batch and step strides in elements
+    bool bf16, softplus;
+};
+struct ChanIn {
+    const void *u, *delta, *B, *C, *gate;
+    const float *A, *skip, *dbias, *h0;
+    const int32_t* lens;
+};
+// How the forward is laid over the GPU (shapes.cpp): R channels per lane (1 or
+// 4; a wavefront covers 16 R channels) and segments of `seg` steps.
+struct ChanPlan {
+    int R;
+    int64_t seg, nseg;
+};
+ChanPlan chan_fwd_plan(const ChanShape& s);
+int64_t chan_tiles(const ChanShape& s, int R);   // wavefronts over the channels of one batch
+size_t chan_fwd_bytes(const ChanShape& s, const ChanPlan& p);
+hipError_t launch_chan_fwd(const ChanShape& s, const ChanPlan& p, const ChanIn& in, void* y, float* hfin,
+                           float* ws, hipStream_t st);
+hipError_t launch_chan_step(const ChanShape& s, float* state, const ChanIn& in, void* y, hipStream_t st);
+
 }  // namespace ssd

@@ -49,4 +49,18 @@ int64_t conv_time_blocks(const ConvShape& s, int64_t rows) {
 }
 int64_t conv_bwd_parts(const ConvShape& s) { return s.Bz * conv_time_blocks(s, conv_rows(s, true)); }
 
+int64_t chan_tiles(const ChanShape& s, int R) {
+    const int64_t per = s.D / s.G, w = 16 * R;
+    return s.G * ((per + w - 1) / w);
+}
+ChanPlan chan_fwd_plan(const ChanShape& s) {
+    return ChanPlan{1, s.L > 0 ? s.L : 1, 1};
+}
+// the segments' end states (slot s becomes the state entering segment s) and
+// their sums of dt
+size_t chan_fwd_bytes(const ChanShape& s, const ChanPlan& p) {
+    if (p.nseg <= 1) return 0;
+    return (size_t)s.Bz * p.nseg * s.D * (s.N + 1) * sizeof(float);
+}
+
 }  // namespace ssd

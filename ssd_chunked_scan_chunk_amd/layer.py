@@ -1,8 +1,9 @@
-"""The operators around the chunked scan: the short causal convolution.
+"""The operators around the chunked scan: the short causal convolution and the
+scan with one decay per channel and state.
 
 Like the rest of the package these only check arguments, allocate outputs and
 workspace and pass pointers to libssd.so.  Inputs that a layer cuts out of a
-projection's rows (x here) may be views: their rows have to be
+projection's rows (x; u, delta, gate, B and C) may be views: their rows have to be
 dense, the strides between rows and batches are free.  Parameters, states and
 upstream gradients are contiguous.
 """
@@ -49,6 +50,13 @@ def _seqlens(seqlens, Bz, device):
     if seqlens is not None and not isinstance(seqlens, torch.Tensor):
         raise TypeError("seqlens must be a torch.Tensor on the GPU")
     _check("seqlens", seqlens, (Bz,), torch.int32, device)
+
+
+def _workspace(workspace, nbytes, device):
+    _check_bytes("workspace", workspace, nbytes, device)
+    if workspace is None and nbytes > 0:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def _enqueue(device, fn, *args):
@@ -158,10 +166,7 @@ def short_conv_bwd(x, weight, dy, bias=None, initial_window=None, dfinal_window=
     _seqlens(seqlens, Bz, x.device)
     n = ctypes.c_size_t()
     _lib.check(_L().ssd_short_conv_bwd_workspace_bytes(d, n))
-    _check_bytes("workspace", workspace, n.value, x.device)
-    if workspace is None and n.value > 0:
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=x.device)
-    wsz = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    workspace, wsz = _workspace(workspace, n.value, x.device)
     dx = torch.empty((Bz, L, C), dtype=x.dtype, device=x.device)
     dweight = torch.empty_like(weight)
     dbias = torch.empty_like(bias) if bias is not None else None
@@ -180,3 +185,79 @@ def short_conv_step(window, x, weight, bias=None, silu=True, pieces=None, y=None
     ys, back = _conv_outputs(x, given, pieces, y)
     _enqueue(x.device, _L().ssd_short_conv_step, d, _at(window), _at(x), _at(weight), _at(bias), _P(*map(_at, ys)))
     return back
+
+
+# ---- scan with one decay per channel and state -----------------------------------------
+
+def _chan_check(u, delta, A, B, C, skip, gate, delta_bias, softplus, lead):
+    """The desc of a scan of u [*lead, channels]; everything but the states checked."""
+    if not isinstance(u, torch.Tensor) or u.dim() != lead + 1:
+        raise ValueError("u must be a %d-D tensor [batch, %schannels]" % (lead + 1, "seqlen, " if lead == 2 else ""))
+    code, dt, dev, D = _dtype_code(u), u.dtype, u.device, u.shape[-1]
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a 2-D tensor [channels, dstate]")
+    _check("A", A, (D, A.shape[1]), torch.float32, dev)
+    if not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
+        raise ValueError("B must be a %d-D tensor [batch, %sngroups, dstate]"
+                         % (lead + 2, "seqlen, " if lead == 2 else ""))
+    G, N, rows = B.shape[-2], A.shape[1], tuple(u.shape[:-1])
+    su = _rows("u", u, u.shape, 1, dt, dev)
+    sd = _rows("delta", delta, u.shape, 1, dt, dev)
+    sz = _rows("gate", gate, u.shape, 1, dt, dev) if gate is not None else (0, 0)
+    sB = _rows("B", B, rows + (G, N), 2, dt, dev)
+    sC = _rows("C", C, rows + (G, N), 2, dt, dev)
+    _check("skip", skip, (D,), torch.float32, dev)
+    _check("delta_bias", delta_bias, (D,), torch.float32, dev)
+    strides = [s[i] if i < lead else 0 for s in (su, sd, sz, sB, sC) for i in (0, 1)]
+    return _lib.ChannelDesc(u.shape[0], u.shape[1] if lead == 2 else 1, D, N, G, *strides, code, int(bool(softplus)))
+
+
+def channel_scan_fwd_workspace_bytes(u, delta, A, B, C) -> int:
+    n = ctypes.c_size_t()
+    _lib.check(_L().ssd_channel_scan_fwd_workspace_bytes(
+        _chan_check(u, delta, A, B, C, None, None, None, True, 2), n))
+    return n.value
+
+
+def channel_scan_fwd(u, delta, A, B, C, skip=None, gate=None, delta_bias=None, softplus=False, initial_state=None,
+                     seqlens=None, return_final_state=False, y=None, final_state=None, workspace=None):
+    """Scan h = exp(dt A) h + dt u B, y = (h C + skip u) silu(gate), with a decay
+    of its own for every channel and state; dt = delta + delta_bias, through a
+    softplus if asked.
+
+    u, delta, gate [Bz,L,D] and B, C [Bz,L,G,N] (bf16 or f32, rows dense; N up to
+    64, channel c reads group c*G//D), A [D,N], skip, delta_bias [D] f32,
+    initial_state [Bz,D,N] f32 (None: zero).  seqlens [Bz] int32 on the GPU:
+    sequence b has that many steps; later rows are not read, y is 0 there and the
+    final state is the one after the last step.  Returns (y, final_state or
+    None); channel_step continues from the state."""
+    d = _chan_check(u, delta, A, B, C, skip, gate, delta_bias, softplus, 2)
+    dev, state = u.device, (u.shape[0], u.shape[2], A.shape[1])
+    _check("initial_state", initial_state, state, torch.float32, dev)
+    _check("final_state", final_state, state, torch.float32, dev)
+    _check("y", y, u.shape, u.dtype, dev)
+    _seqlens(seqlens, u.shape[0], dev)
+    if y is None:
+        y = torch.empty(u.shape, dtype=u.dtype, device=dev)
+    if final_state is None and return_final_state:
+        final_state = torch.empty(state, dtype=torch.float32, device=dev)
+    n = ctypes.c_size_t()
+    _lib.check(_L().ssd_channel_scan_fwd_workspace_bytes(d, n))
+    workspace, wsz = _workspace(workspace, n.value, dev)
+    _enqueue(dev, _L().ssd_channel_scan_fwd, d, _at(u), _at(delta), _at(A), _at(B), _at(C), _at(skip), _at(gate),
+             _at(delta_bias), _at(initial_state), _at(seqlens), _at(y), _at(final_state), _at(workspace), wsz)
+    return y, final_state
+
+
+def channel_step(state, u, delta, A, B, C, skip=None, gate=None, delta_bias=None, softplus=False, y=None):
+    """One token: state [Bz,D,N] f32 is updated in place.  u, delta, gate [Bz,D] and
+    B, C [Bz,G,N] with dense rows.  Returns y [Bz,D]."""
+    d = _chan_check(u, delta, A, B, C, skip, gate, delta_bias, softplus, 1)
+    _need("state", state)
+    _check("state", state, (u.shape[0], u.shape[1], A.shape[1]), torch.float32, u.device)
+    _check("y", y, u.shape, u.dtype, u.device)
+    if y is None:
+        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+    _enqueue(u.device, _L().ssd_channel_step, d, _at(state), _at(u), _at(delta), _at(A), _at(B), _at(C), _at(skip),
+             _at(gate), _at(delta_bias), _at(y))
+    return y

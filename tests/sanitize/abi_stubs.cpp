@@ -71,5 +71,8 @@ hipError_t launch_conv_bwd(const ConvShape&, const void*, const float*, const fl
                            hipStream_t) { SSD_STUB; }
 hipError_t launch_conv_step(const ConvShape&, void*, const void*, const float*, const float*, void* const*,
                             hipStream_t) { SSD_STUB; }
+hipError_t launch_chan_fwd(const ChanShape&, const ChanPlan&, const ChanIn&, void*, float*, float*,
+                           hipStream_t) { SSD_STUB; }
+hipError_t launch_chan_step(const ChanShape&, float*, const ChanIn&, void*, hipStream_t) { SSD_STUB; }
 #undef SSD_STUB
 }  // namespace ssd

@@ -1,0 +1,192 @@
+"""GPU parity of the per-channel scan (forward, single-token step) against the
+plain 64-bit form."""
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as ref
+import ssd_chunked_scan_chunk_amd as ssd
+from gpu_util import log
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+n64 = lambda t: None if t is None else t.detach().double().cpu().numpy()
+
+
+def inputs(Bz, L, D, N, G, dtype, seed=0, wide=0, gate=True, skip=True, bias=True, carry=True, A=None):
+    """wide: elements ahead of u and gate in the rows they are cut from."""
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s, dt=DT[dtype]: torch.randn(s, generator=gen).to(dt).cuda()
+    f = torch.float32
+    both, low = r(Bz, L, wide + 2 * D), r(Bz, L, wide + 2 * G * N)
+    d = dict(u=both[..., wide:wide + D], delta=r(Bz, L, D),
+             A=-(torch.arange(1, N + 1).float() * torch.exp(0.3 * torch.randn(D, N, generator=gen))).cuda()
+             if A is None else A,
+             B=low[..., wide:wide + G * N].unflatten(-1, (G, N)), C=low[..., wide + G * N:].unflatten(-1, (G, N)),
+             skip=r(D, dt=f) if skip else None, gate=both[..., wide + D:] if gate else None,
+             delta_bias=r(D, dt=f) - 3 if bias else None)
+    d["initial_state"] = r(Bz, D, N, dt=f) if carry else None
+    return d
+
+
+def want_of(d, softplus, seqlens, adds=0, **kw):
+    a = {k: n64(v) for k, v in d.items()}
+    return ref.scan(a["u"], a["delta"], a["A"], a["B"], a["C"], a["skip"], a["gate"], a["delta_bias"], softplus,
+                    a["initial_state"], seqlens, adds, **kw)
+
+
+def lens_of(seqlens):
+    return None if seqlens is None else torch.tensor(seqlens, dtype=torch.int32, device="cuda")
+
+
+SHAPES = [
+    # Bz, L, D, N, G, wide, seqlens, softplus, gate, skip, bias, carry
+    (1, 1, 16, 16, 1, 0, None, True, True, True, True, True),
+    (2, 5, 64, 16, 1, 0, None, True, True, True, True, False),
+    (2, 17, 70, 16, 2, 0, None, False, False, False, False, True),      # 35 channels a group
+    (3, 40, 96, 12, 3, 8, [40, 0, 23], True, True, True, True, True),
+    (2, 33, 20, 4, 1, 0, [33, 32], True, True, False, True, True),
+    (1, 50, 33, 1, 1, 3, None, True, False, True, False, True),         # one state, odd rows
+    (1, 21, 130, 7, 2, 0, None, True, True, True, True, False),
+    (2, 19, 24, 32, 1, 0, [19, 1], True, True, True, True, True),
+    (1, 18, 40, 64, 2, 4, None, True, True, True, True, True),
+    (1, 9, 5, 33, 5, 1, None, True, True, True, True, True),            # a channel a group
+    (3, 0, 16, 16, 1, 0, None, True, True, True, True, True),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Bz,L,D,N,G,wide,seqlens,softplus,gate,skip,bias,carry", SHAPES)
+def test_forward(dtype, Bz, L, D, N, G, wide, seqlens, softplus, gate, skip, bias, carry):
+    log("channel scan fwd %s" % ((dtype, Bz, L, D, N, G, wide, seqlens, softplus, gate, skip, bias, carry),))
+    d = inputs(Bz, L, D, N, G, dtype, L + D, wide, gate, skip, bias, carry)
+    if not softplus:   # step sizes have to be positive for the recurrence to decay
+        d["delta"] = d["delta"].abs() * 0.1
+    y, h = ssd.channel_scan_fwd(**d, softplus=softplus, seqlens=lens_of(seqlens), return_final_state=True)
+    torch.cuda.synchronize()
+    want = want_of(d, softplus, seqlens)
+    ref.check("y", y, want, dtype)
+    ref.check("final_state", h, want, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_extreme_step_sizes(dtype):
+    # softplus over its whole range: steps that vanish, and steps so long that
+    # nothing of the state is left
+    log("channel scan extremes %s" % dtype)
+    d = inputs(1, 24, 32, 16, 1, dtype, 3, bias=False)
+    d["delta"] = torch.linspace(-100, 100, 24 * 32).view(1, 24, 32).to(DT[dtype]).cuda()
+    y, h = ssd.channel_scan_fwd(**d, softplus=True, return_final_state=True)
+    torch.cuda.synchronize()
+    want = want_of(d, True, None)
+    ref.check("y", y, want, dtype)
+    ref.check("final_state", h, want, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_behind_the_end_are_not_read(dtype):
+    log("channel scan NaN behind the end %s" % dtype)
+    d = inputs(3, 40, 48, 16, 2, dtype, 4)
+    seqlens = [0, 40, 22]
+    run = lambda lens: ssd.channel_scan_fwd(**d, softplus=True, seqlens=lens_of(lens), return_final_state=True)
+    y0, h0 = run(seqlens)
+    for k in ("u", "delta", "gate", "B", "C"):
+        for b, n in enumerate(seqlens):
+            d[k][b, n:] = float("nan")
+    y1, h1 = run(seqlens)
+    y2, _ = run([-5, 1000, 22])
+    torch.cuda.synchronize()
+    assert torch.equal(y0, y1) and torch.equal(h0, h1) and torch.equal(y0, y2)
+    assert torch.equal(h0[0], d["initial_state"][0])
+    assert not y0[0].any() and not y0[2, 22:].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Bz,D,N,G,wide,gate,skip,bias,softplus", [
+    (1, 1, 1, 1, 0, False, False, False, False), (3, 64, 16, 1, 0, True, True, True, True),
+    (2, 35, 12, 5, 3, True, True, True, True), (5, 20, 64, 2, 0, True, False, True, True),
+    (2, 33, 7, 1, 1, True, True, True, True), (4, 96, 32, 3, 0, False, True, True, True),
+    (2, 40, 8, 1, 4, True, True, True, True), (3, 21, 2, 3, 0, True, True, False, True),
+])
+def test_steps(dtype, Bz, D, N, G, wide, gate, skip, bias, softplus):
+    # a few tokens, each checked from the state the one before left
+    log("channel step %s" % ((dtype, Bz, D, N, G, wide, gate, skip, bias, softplus),))
+    d = inputs(Bz, 4, D, N, G, dtype, D + N, wide, gate, skip, bias, True)
+    if not softplus:
+        d["delta"] = d["delta"].abs() * 0.1
+    state = d.pop("initial_state").clone()
+    for t in range(4):
+        one = {k: v if v is None or k in ("A", "skip", "delta_bias") else v[:, t] for k, v in d.items()}
+        before = state.clone()
+        y = ssd.channel_step(state, **one, softplus=softplus)
+        torch.cuda.synchronize()
+        whole = {k: v if v is None or k in ("A", "skip", "delta_bias") else v[:, None] for k, v in one.items()}
+        want = want_of(dict(whole, initial_state=before), softplus, None)
+        ref.check("y", y[:, None], want, dtype)
+        ref.check("final_state", state, want, "f32")
+
+
+def test_prompt_then_steps():
+    # the convolution and the scan together, a prompt of unequal lengths and then
+    # tokens, against one pass over the whole sequences
+    log("channel prompt then steps")
+    Bz, L, D, N, W, more = 2, 30, 48, 16, 4, 3
+    d = inputs(Bz, L + more, D, N, 1, "f32", 11, carry=False)
+    x = d["u"].contiguous()
+    gen = torch.Generator().manual_seed(5)
+    weight, cb = torch.randn(D, W, generator=gen).cuda(), torch.randn(D, generator=gen).cuda()
+    layer = {k: d[k] for k in ("A", "skip", "delta_bias")}
+    seqlens = [30, 14]
+    lens = lens_of(seqlens)
+    xc, win = ssd.short_conv_fwd(x[:, :L], weight, cb, seqlens=lens, return_final_window=True)
+    rows = {k: d[k][:, :L] for k in ("delta", "B", "C", "gate")}
+    y, state = ssd.channel_scan_fwd(xc, **rows, **layer, softplus=True, seqlens=lens, return_final_state=True)
+    ys = []
+    for t in range(more):
+        xt = ssd.short_conv_step(win, x[:, L + t], weight, cb)
+        ys.append(ssd.channel_step(state, xt, **{k: d[k][:, L + t] for k in rows}, **layer, softplus=True))
+    torch.cuda.synchronize()
+    for b, n in enumerate(seqlens):
+        at = list(range(n)) + list(range(L, L + more))
+        c = ref.conv(n64(x[b:b + 1, at]), n64(weight), n64(cb), None, None, True)
+        a = {k: n64(d[k][b:b + 1, at]) for k in rows}
+        want = ref.scan(c["y"], a["delta"], n64(d["A"]), a["B"], a["C"], n64(d["skip"]), a["gate"],
+                        n64(d["delta_bias"]))
+        got = torch.cat([y[b, :n], torch.stack([v[b] for v in ys])])
+        # the convolution's own error enters through u: at most 40 roundings of
+        # values up to max|u|, against sums of them
+        scale = np.abs(want["y"]).max()
+        assert np.abs(n64(got) - want["y"][0]).max() <= 2e-5 * scale
+        assert np.abs(n64(state[b]) - want["final_state"][0]).max() <= 2e-5 * np.abs(want["final_state"]).max()
+
+
+def test_repeats_streams_and_graphs():
+    log("channel scan streams and graphs")
+    d = inputs(2, 70, 80, 16, 1, "bf16", 6, wide=16)
+    one = {k: v if v is None or k in ("A", "skip", "delta_bias") else v[:, 3] for k, v in d.items()
+           if k != "initial_state"}
+    state = d["initial_state"].clone()
+
+    def run():
+        y, h = ssd.channel_scan_fwd(**d, softplus=True, return_final_state=True)
+        s = state.clone()
+        return y, h, ssd.channel_step(s, **one, softplus=True), s
+
+    want = run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = run()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for _ in range(3):
+        for t in held:
+            t.fill_(7)
+        graph.replay()
+        again = run()
+        torch.cuda.synchronize()
+        for got in (other, held, again):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -138,3 +138,113 @@ def test_conv_abi_pointers(lib):
     assert step(w=None) == _lib.SSD_ERR_NULL
     assert step(w=P[0]) == step(y=pieces(P[0])) == _lib.SSD_ERR_ALIAS
     assert step(d=conv_desc(batch=0, seqlen=1)) == _lib.SSD_OK
+
+
+# ---- per-channel scan ---------------------------------------------------------------
+D, N, G = 24, 16, 2
+
+
+def scan_args(lead=(Bz, L), **kw):
+    d = dict(u=torch.zeros(*lead, D, dtype=BF), delta=torch.zeros(*lead, D, dtype=BF), A=torch.zeros(D, N),
+             B=torch.zeros(*lead, G, N, dtype=BF), C=torch.zeros(*lead, G, N, dtype=BF))
+    d.update(kw)
+    return d
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(u=torch.zeros(L, D, dtype=BF)), "u must be"),
+    (dict(u=torch.zeros(Bz, D, L, dtype=BF).transpose(1, 2)), "rows of u"),
+    (dict(delta=None), "delta is required"),
+    (dict(delta=torch.zeros(Bz, L, D)), "delta has dtype"),
+    (dict(A=torch.zeros(D)), "A must be"),
+    (dict(A=torch.zeros(D + 1, N)), "A has shape"),
+    (dict(A=torch.zeros(D, N, dtype=BF)), "A has dtype"),
+    (dict(B=torch.zeros(Bz, L, N, dtype=BF)), "B must be"),
+    (dict(B=torch.zeros(Bz, L, G, N + 1, dtype=BF)), "B has shape"),
+    (dict(C=torch.zeros(Bz, L, 1, N, dtype=BF)), "C has shape"),
+    (dict(C=torch.zeros(Bz, L, N, G, dtype=BF).transpose(2, 3)), "rows of C"),
+    (dict(gate=torch.zeros(Bz, L, D + 1, dtype=BF)), "gate has shape"),
+    (dict(skip=torch.zeros(D, dtype=BF)), "skip has dtype"),
+    (dict(delta_bias=torch.zeros(D, 1)), "delta_bias has shape"),
+    (dict(initial_state=torch.zeros(Bz, D, N, dtype=BF)), "initial_state has dtype"),
+    (dict(final_state=torch.zeros(Bz, N, D)), "final_state has shape"),
+    (dict(y=torch.zeros(Bz, L, D)), "y has dtype"),
+    (dict(seqlens=torch.zeros(Bz)), "seqlens has dtype"),
+    (dict(), "on the GPU"),
+])
+def test_scan_fwd(kw, match):
+    with pytest.raises(ValueError, match=match):
+        ssd.channel_scan_fwd(**scan_args(**kw))
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(state=None), "state is required"),
+    (dict(state=torch.zeros(Bz, D, N, dtype=BF)), "state has dtype"),
+    (dict(u=torch.zeros(Bz, 1, D, dtype=BF)), "u must be"),
+    (dict(y=torch.zeros(Bz, D)), "y has dtype"),
+])
+def test_channel_step(kw, match):
+    d = scan_args((Bz,), state=torch.zeros(Bz, D, N))
+    d.update(kw)
+    with pytest.raises(ValueError, match=match):
+        ssd.channel_step(**d)
+
+
+def chan_desc(**kw):
+    d = dict(batch=2, seqlen=100, channels=64, dstate=16, ngroups=2, u_bstride=6400, u_rstride=64, delta_bstride=6400,
+             delta_rstride=64, gate_bstride=6400, gate_rstride=64, B_bstride=3200, B_rstride=32, C_bstride=3200,
+             C_rstride=32, dtype=_lib.SSD_BF16, softplus=1)
+    d.update(kw)
+    return _lib.ChannelDesc(*d.values())
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=-1), _lib.SSD_ERR_SHAPE), (dict(seqlen=-1), _lib.SSD_ERR_SHAPE), (dict(channels=0), _lib.SSD_ERR_SHAPE),
+    (dict(dstate=0), _lib.SSD_ERR_SHAPE), (dict(dstate=65), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(ngroups=3), _lib.SSD_ERR_SHAPE), (dict(dtype=2), _lib.SSD_ERR_DTYPE), (dict(softplus=2), _lib.SSD_ERR_SHAPE),
+    (dict(B_rstride=-1), _lib.SSD_ERR_SHAPE), (dict(C_bstride=1 << 60), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(batch=1 << 20), _lib.SSD_ERR_UNSUPPORTED), (dict(channels=1 << 30), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(seqlen=1 << 40), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(batch=1 << 15, channels=1 << 12), _lib.SSD_ERR_UNSUPPORTED),
+])
+def test_scan_abi_shapes(lib, kw, code):
+    d, n = chan_desc(**kw), ctypes.c_size_t()
+    none = [None] * 5
+    assert lib.ssd_channel_scan_fwd(d, *P[:5], *none, P[6], None, None, 0, None) == code
+    assert lib.ssd_last_error() != b""
+    assert lib.ssd_channel_scan_fwd_workspace_bytes(d, n) == code
+
+
+def test_scan_abi_pointers(lib):
+    n, odd = ctypes.c_size_t(), ctypes.c_void_p((1 << 20) + 1)
+    d = chan_desc()
+    assert lib.ssd_channel_scan_fwd_workspace_bytes(d, n) == 0
+    ws = ctypes.c_void_p(1 << 45)
+
+    def fwd(d=d, wsz=n.value, ws=ws, **kw):
+        a = dict(zip(("u", "delta", "A", "B", "C"), P), skip=None, gate=None, bias=None, h0=None, lens=None, y=P[6],
+                 fin=None)
+        a.update(kw)
+        return lib.ssd_channel_scan_fwd(d, *a.values(), ws, wsz, None)
+
+    for k in ("u", "delta", "A", "B", "C", "y"):
+        assert fwd(**{k: None}) == _lib.SSD_ERR_NULL
+        assert fwd(**{k: odd}) == _lib.SSD_ERR_ALIGN
+    for k in ("skip", "gate", "bias", "h0", "lens", "fin"):
+        assert fwd(**{k: odd}) == _lib.SSD_ERR_ALIGN
+    assert fwd(y=P[0]) == fwd(fin=P[2]) == fwd(h0=P[7], fin=P[7]) == fwd(fin=P[6]) == _lib.SSD_ERR_ALIAS
+    assert fwd(d=chan_desc(batch=0), u=None, y=None) == fwd(d=chan_desc(seqlen=0), y=None) == _lib.SSD_OK
+    # a long sequence of few channels is cut into segments, which need a workspace
+    long = chan_desc(batch=1, seqlen=1 << 16, u_bstride=0)
+    assert lib.ssd_channel_scan_fwd_workspace_bytes(long, n) == 0
+    if n.value:
+        assert fwd(d=long, ws=None) == fwd(d=long, wsz=n.value - 1) == _lib.SSD_ERR_WORKSPACE
+        assert fwd(d=long, wsz=n.value, ws=ctypes.c_void_p((1 << 45) + 4)) == _lib.SSD_ERR_ALIGN
+        assert fwd(d=long, wsz=n.value, ws=P[6]) == _lib.SSD_ERR_ALIAS
+
+    one = chan_desc(seqlen=1)
+    step = lambda st=P[8], y=P[6], d=one: lib.ssd_channel_step(d, st, *P[:5], None, None, None, y, None)
+    assert step(d=d) == _lib.SSD_ERR_SHAPE
+    assert step(st=None) == step(y=None) == _lib.SSD_ERR_NULL
+    assert step(st=P[0]) == step(y=P[8]) == _lib.SSD_ERR_ALIAS
+    assert step(d=chan_desc(batch=0, seqlen=1)) == _lib.SSD_OK
