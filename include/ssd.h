@@ -309,6 +309,7 @@ ssd_status ssd_short_conv_step(const ssd_conv_desc* desc, void* window, const vo
  * per batch, with g = c * ngroups / channels (ssd_chunk_scan_fwd's recurrence has one
  * decay per head).  States, exponents and sums are float32; y is rounded once.
  *   u, delta, gate   rows of `channels` elements at b*bstride + t*rstride
+ *                    (rstride at most 2^24 when seqlen > 1)
  *   B, C             rows of ngroups*dstate elements, likewise strided
  *   A                [channels][dstate] float32; skip, delta_bias [channels]
  *                    float32 or NULL (zero); gate NULL: no gating

@@ -6,6 +6,7 @@
 namespace {
 
 constexpr int64_t kMaxSize = (int64_t)1 << 40;
+constexpr int64_t kMaxRow = (int64_t)1 << 24;   // elements between steps of the per-channel scan's inputs
 
 // bytes from the first to past the last element of rows of `n` elements at
 // b * bs + t * rs
@@ -128,6 +129,12 @@ ssd_status chan_shape(const ssd_channel_desc* d, ssd::ChanShape* s) {
     s->ub = d->u_bstride; s->ur = d->u_rstride; s->db = d->delta_bstride; s->dr = d->delta_rstride;
     s->zb = d->gate_bstride; s->zr = d->gate_rstride;
     s->Bb = d->B_bstride; s->Br = d->B_rstride; s->Cb = d->C_bstride; s->Cr = d->C_rstride;
+    // the kernels reach the rows of a batch of steps by 32-bit byte offsets
+    int64_t* rows[] = {&s->ur, &s->dr, &s->zr, &s->Br, &s->Cr};
+    for (int64_t* r : rows) {
+        if (s->L <= 1) *r = 0;
+        if (*r > kMaxRow) return fail(SSD_ERR_UNSUPPORTED, "step strides must be at most 2^24 elements");
+    }
     s->bf16 = d->dtype == SSD_BF16; s->softplus = d->softplus == 1;
     return SSD_OK;
 }

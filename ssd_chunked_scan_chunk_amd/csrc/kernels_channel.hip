@@ -4,174 +4,209 @@
 //     dt = softplus(delta + bias),  h[n] = e^{dt A[n]} h[n] + dt u B[n],
 //     y = (sum_n h[n] C[n] + skip u) silu(gate)
 // for every (batch, channel), n < N states.  Every (step, channel, state) costs
-// a multiplication, an exponential, another multiplication and two fused
-// multiply-adds, none of which the matrix units can take (no operand is shared
-// between channels), so the forward is bound by vector issue, not by HBM: it is
-// written to spend as little as possible beside those.  The layout is described
-// in chan_util.hpp.  The recurrence itself runs sequentially in registers, which
-// needs the fewest operations; the sequence is cut into segments only where the
-// channels alone leave the GPU idle (a first pass then finds each segment's end
-// state from zero and its sum of dt, a scan over segments the states entering
-// them; the decay over a segment is e^{A sum dt}).
+// two multiplications, an exponential and two fused multiply-adds, none of which
+// the matrix units can take (no operand is shared between channels): 24 cycles of
+// a SIMD for 64 of them, so the forward is bound by vector issue and the kernel
+// is laid out to spend little beside those.
+//
+// A workgroup owns 64 consecutive channels of a group (32 where that balances the
+// GPU better), a lane one of them and a quarter (an eighth) of its states, in
+// registers.  Steps are taken in batches of eight: dt and dt u are formed once,
+// spread over the workgroup, and passed through LDS with the batch's B and C (the
+// same for all channels: broadcast reads), the parts of every step's y are summed
+// through LDS, and one barrier per batch orders all of it; inputs are in flight
+// two batches ahead.  The recurrence itself runs sequentially, which needs the
+// fewest operations; the sequence is cut into segments only where the channels
+// alone leave the GPU idle (a first pass then finds each segment's end state from
+// zero and its sum of dt, a scan over segments the states entering them; the
+// decay over a segment is e^{A sum dt}).
+#include <type_traits>
+
 #include "chan_util.hpp"
 
 namespace ssd {
 
 namespace {
 
+template <int V> using Int = std::integral_constant<int, V>;
+
+// CW: channels of a workgroup (64, or 32 with half the states in each half of a
+// wavefront); NR: states of a lane, 256 / CW parts of a channel's states.
 // FULL: outputs from the states entering each segment; otherwise each segment's
-// end state from zero (S) and its sums of dt.
-template <typename T, int R, int NR, bool FULL>
+// end state from zero (S) and its sum of dt.
+template <typename T, int NR, int CW, bool FULL>
 __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
 {
-    constexpr int S = 4 / R, TB = 4 * S, NP = 4 * NR;
-    constexpr int NB = (TB * NP + 63) / 64;
-    __shared__ float4 s_dt[4][64], s_du[4][64];
-    __shared__ float s_B[4][TB * NP], s_C[4][FULL ? TB * NP : 1];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
-    const int tile = blockIdx.x * 4 + wave;
-    if (tile >= a.tiles) return;   // wavefronts share nothing
-    const int g = tile / a.tpg, cg = (tile - g * a.tpg) * 16 * R + c * R;   // channel within the group
-    const int live = a.per - cg < 0 ? 0 : a.per - cg > R ? R : a.per - cg;
-    const int64_t ch = (int64_t)g * a.per + cg, b = blockIdx.z, seg = blockIdx.y;
-    const bool wide = a.wide;
+    constexpr int ES = sizeof(T), NPART = 256 / CW, NP = NPART * NR;
+    constexpr int TB = 8, TP = TB * CW / 256;       // steps of a batch; (step, channel) pairs of a thread
+    constexpr int NBC = TB * NP * (FULL ? 2 : 1);   // elements of B and C in a batch
+    constexpr int NE = (NBC + 255) / 256;           // of these, passed on by a thread
+    constexpr bool EXACT = ES == 4;
+    __shared__ float2 s_dt[2][TB][CW];
+    __shared__ __align__(16) float s_bc[2][NBC];    // [step][B, C][state]
+    __shared__ float s_y[FULL ? 2 : 1][FULL ? TB : 1][NPART][CW];
+    const int tid = threadIdx.x, c = tid & (CW - 1), part = tid / CW, n0 = part * NR;
+    const int g = blockIdx.x / a.tpg, cg = (blockIdx.x - g * a.tpg) * CW + c;
+    const bool live = cg < a.per;
+    // threads past the group repeat its last channel and store nothing
+    const int cl = live ? cg : a.per - 1;
+    const uint32_t col = (uint32_t)cl * ES;
+    const int64_t gch = (int64_t)g * a.per, ch = gch + cl, b = blockIdx.z, seg = blockIdx.y;
     const int64_t ts = seg * a.seg, t1 = ts + a.seg < a.L ? ts + a.seg : a.L;
-    const int64_t n = chan_length(a.in.lens, b, a.L), te = n < t1 ? n : t1;
+    const int64_t len = chan_length(a.in.lens, b, a.L);
+    const int te = (int)(len < ts ? 0 : (len < t1 ? len : t1) - ts);   // steps to compute from ts on
+    const bool gated = a.in.gate != nullptr;
 
-    float A2[R][NR], h[R][NR], bias[R], skip[R], sdt[R] = {};
+    float A2[NR], h[NR], sdt = 0.f;
+    const float bias = a.in.dbias ? a.in.dbias[ch] : 0.f, skip = a.in.skip ? a.in.skip[ch] : 0.f;
+    const float* h0 = !FULL ? nullptr
+                      : seg > 0 ? a.S + ((b * a.nseg + seg) * a.D + ch) * a.N
+                      : a.in.h0 ? a.in.h0 + (b * a.D + ch) * a.N : nullptr;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        bias[r] = a.in.dbias && r < live ? a.in.dbias[ch + r] : 0.f;
-        skip[r] = a.in.skip && r < live ? a.in.skip[ch + r] : 0.f;
-        const float* h0 = !FULL ? nullptr
-                          : seg > 0 ? a.S + ((b * a.nseg + seg) * a.D + ch + r) * a.N
-                          : a.in.h0 ? a.in.h0 + (b * a.D + ch + r) * a.N : nullptr;
-#pragma unroll
-        for (int i = 0; i < NR; ++i) {
-            const int k = q * NR + i;
-            const bool in = r < live && k < a.N;
-            A2[r][i] = in ? a.in.A[(ch + r) * a.N + k] * kLog2e : 0.f;
-            h[r][i] = in && h0 ? h0[k] : 0.f;
-        }
+    for (int i = 0; i < NR; ++i) {
+        const bool in = n0 + i < a.N;   // states past N: A = B = C = 0
+        A2[i] = in ? a.in.A[ch * a.N + n0 + i] * kLog2e : 0.f;
+        h[i] = in && h0 ? h0[n0 + i] : 0.f;
     }
-    const T* up = (const T*)a.in.u + b * a.ub + ch;
-    const T* dp = (const T*)a.in.delta + b * a.db + ch;
-    const T* zp = a.in.gate ? (const T*)a.in.gate + b * a.zb + ch : nullptr;
-    const T* Bp = (const T*)a.in.B + b * a.Bb + (int64_t)g * a.N;
-    const T* Cp = (const T*)a.in.C + b * a.Cb + (int64_t)g * a.N;
-    T* yp = (T*)a.y + b * a.L * a.D + ch;
+    // rows of the batch being fetched, and of the one being written
+    RowIn up = row_in(a.in.u, (b * a.ub + gch) * ES + ts * a.ur);
+    RowIn dp = row_in(a.in.delta, (b * a.db + gch) * ES + ts * a.dr);
+    RowIn zp = row_in(gated ? a.in.gate : a.in.u, (b * a.zb + gch) * ES + ts * a.zr);
+    RowIn Bp = row_in(a.in.B, (b * a.Bb + (int64_t)g * a.N) * ES + ts * a.Br);
+    RowIn Cp = row_in(a.in.C, (b * a.Cb + (int64_t)g * a.N) * ES + ts * a.Cr);
+    const uint32_t yr = (uint32_t)a.D * ES;
+    RowOut yp = row_out(a.y, ((b * a.L + ts) * a.D + gch) * ES);
 
-    Elems<T, R> ru[S], rd[S], rz[S];
-    T rB[NB], rC[NB];
-    auto fetch = [&](int64_t t) {
+    // This thread's pairs of a batch are the steps part + k NPART of channel c, its
+    // elements of B and C those at e 256 + tid; offsets in the batch's rows.  Steps
+    // past `last` repeat that one.
+    uint32_t ou[TP], od[TP], oz[TP], obc[NE];
+    auto offsets = [&](int last) {
 #pragma unroll
-        for (int k = 0; k < S; ++k) {
-            const int64_t s = t + q * S + k;
-            const int lv = s < te ? live : 0;
-            ru[k] = load_elems<T, R>(up + s * a.ur, lv, wide);
-            rd[k] = load_elems<T, R>(dp + s * a.dr, lv, wide);
-            if (FULL && zp) rz[k] = load_elems<T, R>(zp + s * a.zr, lv, wide);
+        for (int k = 0; k < TP; ++k) {
+            const int s = part + k * NPART;
+            const uint32_t r = s < last ? s : last;
+            ou[k] = r * a.ur + col;
+            od[k] = r * a.dr + col;
+            oz[k] = r * a.zr + col;
         }
 #pragma unroll
-        for (int e = 0; e < NB; ++e) {
-            const int idx = e * 64 + lane, k = idx & (NP - 1);
-            const int64_t s = t + idx / NP;
-            const bool in = k < a.N && s < te && idx < TB * NP;
-            rB[e] = in ? Bp[s * a.Br + k] : T(0);
-            if (FULL) rC[e] = in ? Cp[s * a.Cr + k] : T(0);
+        for (int e = 0; e < NE; ++e) {
+            const int i = e * 256 + tid, s = i / (FULL ? 2 * NP : NP), n = i & (NP - 1);
+            const uint32_t r = s < last ? s : last;
+            obc[e] = r * (FULL && (i & NP) ? a.Cr : a.Br) + (uint32_t)(n < a.N ? n : a.N - 1) * ES;
         }
     };
-
-    fetch(ts);
-    for (int64_t t = ts; t < te; t += TB) {
-        // this row's unit: dt and dt u, once per (step, channel)
-        float u[S][R], gz[S][R], d4[4], w4[4];
+    // two batches in flight
+    T ru[2][TP], rd[2][TP], rz[2][TP], rbc[2][NE];
+    auto fetch = [&](auto slot, int last) {
+        constexpr int P = decltype(slot)::value;
+        if (last < TB - 1) offsets(last);
 #pragma unroll
-        for (int k = 0; k < S; ++k)
+        for (int k = 0; k < TP; ++k) {
+            ru[P][k] = load_at<T>(up, ou[k]);
+            rd[P][k] = load_at<T>(dp, od[k]);
+            if (FULL) rz[P][k] = load_at<T>(zp, oz[k]);
+        }
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const float x = as_f32(rd[k].v[r]) + bias[r];
-                float dt = a.softplus ? softplus_of(x) : x;
-                dt = t + q * S + k < te ? dt : 0.f;   // a step past the end changes nothing
-                u[k][r] = as_f32(ru[k].v[r]);
-                d4[k * R + r] = dt;
-                w4[k * R + r] = dt * u[k][r];
-                sdt[r] += dt;
-                if (FULL && zp) {
-                    const float z = as_f32(rz[k].v[r]);
-                    gz[k][r] = z * sigmoid_of(z);
-                }
+        for (int e = 0; e < NE; ++e)
+            rbc[P][e] = FULL && ((e * 256 + tid) & NP) ? load_at<T>(Cp, obc[e]) : load_at<T>(Bp, obc[e]);
+        up += TB * (uint64_t)a.ur;
+        dp += TB * (uint64_t)a.dr;
+        zp += TB * (uint64_t)a.zr;
+        Bp += TB * (uint64_t)a.Br;
+        Cp += TB * (uint64_t)a.Cr;
+    };
+    float u[TP], z[TP];
+    auto prepare = [&](int t, auto slot) {
+        constexpr int P = decltype(slot)::value;
+#pragma unroll
+        for (int k = 0; k < TP; ++k) {
+            const int s = part + k * NPART;
+            const float x = as_f32(rd[P][k]) + bias, sp = softplus_of<EXACT>(x);
+            float dt = a.softplus ? sp : x;
+            dt = t + s < te ? dt : 0.f;   // a step past the end changes nothing
+            u[k] = as_f32(ru[P][k]);
+            z[k] = as_f32(rz[P][k]);
+            sdt += dt;
+            s_dt[P][s][c] = make_float2(dt, dt * u[k]);
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const int i = e * 256 + tid;
+            if (NBC % 256 == 0 || i < NBC) s_bc[P][i] = (i & (NP - 1)) < a.N ? as_f32(rbc[P][e]) : 0.f;
+        }
+    };
+    // The batch at t, whose values lie in slot P; the inputs of the one after the
+    // next are fetched into that slot, those of the next prepared.
+    auto batch = [&](int t, auto slot) {
+        constexpr int P = decltype(slot)::value;
+        if (t + 2 * TB < te) fetch(slot, te - 1 - t - 2 * TB);
+        if (t == 0 || !FULL) lds_barrier();   // otherwise the one below has ordered slot P
+#pragma unroll
+        for (int k = 0; k < TB; ++k) {
+            const float2 d = s_dt[P][k][c];
+            const float* bc = s_bc[P] + k * (NBC / TB) + n0;
+            float y = 0.f;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const float e = fast_exp2(d.x * A2[i]);
+                h[i] = fmaf(e, h[i], d.y * bc[i]);
+                if (FULL) y = i == 0 ? h[i] * bc[NP + i] : fmaf(h[i], bc[NP + i], y);
             }
-        wave_lds_fence();
-        s_dt[wave][q * 16 + c] = make_float4(d4[0], d4[1], d4[2], d4[3]);
-        s_du[wave][q * 16 + c] = make_float4(w4[0], w4[1], w4[2], w4[3]);
+            if (FULL) s_y[P][k][part][c] = y;
+        }
+        float pu[TP], pz[TP];
 #pragma unroll
-        for (int e = 0; e < NB; ++e)
-            if (TB * NP >= 64 || lane < TB * NP) {
-                s_B[wave][e * 64 + lane] = as_f32(rB[e]);
-                if (FULL) s_C[wave][e * 64 + lane] = as_f32(rC[e]);
-            }
-        wave_lds_fence();
-        if (t + TB < te) fetch(t + TB);
-
-        float v[4][4];
+        for (int k = 0; k < TP; ++k) { pu[k] = u[k]; pz[k] = z[k]; }
+        if (t + TB < te) prepare(t + TB, Int<P ^ 1>());
+        if constexpr (FULL) {
+            lds_barrier();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float4 dv = s_dt[wave][j * 16 + c], wv = s_du[wave][j * 16 + c];
-            const float dd[4] = {dv.x, dv.y, dv.z, dv.w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
+            for (int k = 0; k < TP; ++k) {
+                const int s = part + k * NPART;
+                float y = 0.f;
 #pragma unroll
-            for (int k = 0; k < S; ++k) {
-                float Bv[NR], Cv[NR];
-#pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    Bv[i] = s_B[wave][(j * S + k) * NP + q * NR + i];
-                    if (FULL) Cv[i] = s_C[wave][(j * S + k) * NP + q * NR + i];
-                }
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    float s = 0.f;
-#pragma unroll
-                    for (int i = 0; i < NR; ++i) {
-                        const float e = fast_exp2(dd[k * R + r] * A2[r][i]);
-                        h[r][i] = fmaf(e, h[r][i], ww[k * R + r] * Bv[i]);
-                        if (FULL) s = fmaf(h[r][i], Cv[i], s);
-                    }
-                    v[j][k * R + r] = s;
-                }
+                for (int q = 0; q < NPART; q += 2) y += s_y[P][s][q][c] + s_y[P][s][q + 1][c];
+                y = fmaf(skip, pu[k], y);
+                const float sz = pz[k] * sigmoid_of(pz[k]);
+                y *= gated ? sz : 1.f;
+                if (live && t + s < te) store_at(yp, s * yr + col, y, T());
             }
         }
-        if constexpr (FULL) {
-#pragma unroll
-            for (int k = 0; k < S; ++k) {
-                float o[R];
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int m = k * R + r;
-                    o[r] = fmaf(skip[r], u[k][r], sum_to_rows(v[0][m], v[1][m], v[2][m], v[3][m]));
-                    if (zp) o[r] *= gz[k][r];
-                }
-                const int64_t s = t + q * S + k;
-                if (s < te) store_elems<T, R>(yp + s * a.D, o, live, wide);
-            }
+        yp += TB * (uint64_t)yr;
+    };
+    if (te > 0) {
+        offsets(TB - 1);
+        fetch(Int<0>(), te - 1);
+        if (TB < te) fetch(Int<1>(), te - 1 - TB);
+        prepare(0, Int<0>());
+        for (int t = 0; t < te; t += 2 * TB) {
+            batch(t, Int<0>());
+            if (t + TB < te) batch(t + TB, Int<1>());
         }
     }
 
     if constexpr (FULL) {
-        const float zero[R] = {};
-        for (int64_t s = (te > ts ? te : ts) + q; s < t1; s += 4) store_elems<T, R>(yp + s * a.D, zero, live, wide);
+        const RowOut yz = row_out(a.y, ((b * a.L + ts) * a.D + gch) * ES);
+        for (int64_t s = te + part; s < t1 - ts; s += NPART)
+            if (live) store_at(yz + s * (uint64_t)yr, col, 0.f, T());
     }
     float* out = FULL ? (seg == a.nseg - 1 ? a.hfin : nullptr) : a.S;
     if (out) {
         const int64_t row = FULL ? b : b * a.nseg + seg + 1;   // slot s + 1: what enters the next segment
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+        for (int i = 0; i < NR; ++i)
+            if (live && n0 + i < a.N) out[(row * a.D + ch) * a.N + n0 + i] = h[i];
+        if constexpr (!FULL) {   // each thread summed its own share of the steps
+            __syncthreads();
+            float* sum = &s_dt[0][0][0].x;
+            sum[tid] = sdt;
+            __syncthreads();
+            sdt = 0.f;
 #pragma unroll
-            for (int i = 0; i < NR; ++i)
-                if (r < live && q * NR + i < a.N) out[(row * a.D + ch + r) * a.N + q * NR + i] = h[r][i];
-            if (!FULL) {
-                const float sum = sum_rows(sdt[r]);
-                if (r < live && q == 0) a.sumdt[row * a.D + ch + r] = sum;
-            }
+            for (int q = 0; q < NPART; ++q) sdt += sum[q * CW + c];
+            if (live && part == 0) a.sumdt[row * a.D + ch] = sdt;
         }
     }
 }
@@ -188,9 +223,18 @@ __global__ __launch_bounds__(256) void k_chan_pass(ChanArgs a, int64_t items)
     float h = a.in.h0 ? a.in.h0[i] : 0.f;
     float* S = a.S + b * a.nseg * DN + dn;
     const float* sd = a.sumdt + b * a.nseg * a.D + ch;
-    for (int64_t s = 1; s < a.nseg; ++s) {
-        h = fmaf(fast_exp2(A2 * sd[s * a.D]), h, S[s * DN]);
-        S[s * DN] = h;
+    constexpr int U = 8;   // segments in flight
+    for (int64_t s = 1; s < a.nseg; s += U) {
+        float v[U], d[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (s + k < a.nseg) { v[k] = S[(s + k) * DN]; d[k] = sd[(s + k) * a.D]; }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (s + k < a.nseg) {
+                h = fmaf(fast_exp2(A2 * d[k]), h, v[k]);
+                S[(s + k) * DN] = h;
+            }
     }
 }
 
@@ -212,11 +256,11 @@ __global__ __launch_bounds__(256) void k_chan_step(ChanArgs a, float* __restrict
     const bool quad = on && a.wide && n0 < a.N;   // N a multiple of 4, 16-byte rows
     if (quad) {
         const f32x4 hv = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(hp));
-        const float4 av = *reinterpret_cast<const float4*>(Ap);
-        const Elems<T, 4> bv = load_elems<T, 4>(Bp, 4, true), cv = load_elems<T, 4>(Cp, 4, true);
-        A[0] = av.x; A[1] = av.y; A[2] = av.z; A[3] = av.w;
+        load_quad(Ap, A);
+        load_quad(Bp, Bv);
+        load_quad(Cp, Cv);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) { h[k] = hv[k]; Bv[k] = as_f32(bv.v[k]); Cv[k] = as_f32(cv.v[k]); }
+        for (int k = 0; k < 4; ++k) h[k] = hv[k];
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -232,7 +276,7 @@ __global__ __launch_bounds__(256) void k_chan_step(ChanArgs a, float* __restrict
     if (on && a.in.dbias) dt += a.in.dbias[ch];
     const float z = on && a.in.gate ? as_f32(((const T*)a.in.gate)[b * a.zb + ch]) : 0.f;
     const float skip = on && a.in.skip ? a.in.skip[ch] : 0.f;
-    if (a.softplus) dt = softplus_of(dt);
+    if (a.softplus) dt = softplus_of<sizeof(T) == 4>(dt);
     const float du = dt * u;
     float y = 0.f;
 #pragma unroll
@@ -255,38 +299,44 @@ __global__ __launch_bounds__(256) void k_chan_step(ChanArgs a, float* __restrict
     if (on && n0 == 0) Elem<T>::store((T*)a.y + b * a.D + ch, y);
 }
 
-ChanArgs args_of(const ChanShape& s, const ChanIn& in, int R) {
+ChanArgs args_of(const ChanShape& s, const ChanIn& in) {
     ChanArgs a = {};
     a.in = in;
     a.L = s.L; a.D = s.D; a.N = (int)s.N;
-    a.ub = s.ub; a.ur = s.ur; a.db = s.db; a.dr = s.dr; a.zb = s.zb; a.zr = s.zr;
-    a.Bb = s.Bb; a.Br = s.Br; a.Cb = s.Cb; a.Cr = s.Cr;
+    a.ub = s.ub; a.db = s.db; a.Bb = s.Bb; a.Cb = s.Cb;
+    a.zb = in.gate ? s.zb : s.ub;   // without a gate the kernels load u in its place
+    const uint32_t es = s.bf16 ? 2 : 4;
+    a.ur = (uint32_t)s.ur * es; a.dr = (uint32_t)s.dr * es; a.zr = (uint32_t)(in.gate ? s.zr : s.ur) * es;
+    a.Br = (uint32_t)s.Br * es; a.Cr = (uint32_t)s.Cr * es;
     a.per = (int)(s.D / s.G);
-    a.tiles = (int)chan_tiles(s, R);
-    a.tpg = (int)(a.tiles / s.G);
     a.softplus = s.softplus;
     return a;
 }
 
-bool on16(const void* p, int64_t es, int64_t n) { return reinterpret_cast<uintptr_t>(p) % (es * n) == 0; }
+bool on_bytes(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-template <typename T, int R, int NR> hipError_t run_fwd(const ChanArgs& a, const ChanShape& s, hipStream_t st) {
-    const dim3 blk(256), grid((unsigned)((a.tiles + 3) / 4), (unsigned)a.nseg, (unsigned)s.Bz);
+template <typename T, int NR, int CW> hipError_t run_fwd(const ChanArgs& a, const ChanShape& s, hipStream_t st) {
+    const dim3 blk(256), grid((unsigned)chan_tiles(s, CW), (unsigned)a.nseg, (unsigned)s.Bz);
     if (a.nseg > 1) {
         // the last segment's end state enters nothing
-        hipLaunchKernelGGL((k_chan_fwd<T, R, NR, false>), dim3(grid.x, grid.y - 1, grid.z), blk, 0, st, a);
+        hipLaunchKernelGGL((k_chan_fwd<T, NR, CW, false>), dim3(grid.x, grid.y - 1, grid.z), blk, 0, st, a);
         const int64_t items = s.Bz * s.D * s.N;
         hipLaunchKernelGGL(k_chan_pass, dim3((unsigned)((items + 255) / 256)), blk, 0, st, a, items);
     }
-    hipLaunchKernelGGL((k_chan_fwd<T, R, NR, true>), grid, blk, 0, st, a);
+    hipLaunchKernelGGL((k_chan_fwd<T, NR, CW, true>), grid, blk, 0, st, a);
     return hipGetLastError();
 }
-template <typename T, int R> hipError_t run_fwd_n(const ChanArgs& a, const ChanShape& s, hipStream_t st) {
-    if (s.N <= 4) return run_fwd<T, R, 1>(a, s, st);
-    if (s.N <= 8) return run_fwd<T, R, 2>(a, s, st);
-    if (s.N <= 16) return run_fwd<T, R, 4>(a, s, st);
-    if (s.N <= 32) return run_fwd<T, R, 8>(a, s, st);
-    return run_fwd<T, R, 16>(a, s, st);
+template <typename T> hipError_t run_fwd_t(const ChanArgs& a, const ChanShape& s, int cw, hipStream_t st) {
+    if (cw == 32) {
+        if (s.N <= 8) return run_fwd<T, 1, 32>(a, s, st);
+        if (s.N <= 16) return run_fwd<T, 2, 32>(a, s, st);
+        if (s.N <= 32) return run_fwd<T, 4, 32>(a, s, st);
+        return run_fwd<T, 8, 32>(a, s, st);
+    }
+    if (s.N <= 8) return run_fwd<T, 2, 64>(a, s, st);
+    if (s.N <= 16) return run_fwd<T, 4, 64>(a, s, st);
+    if (s.N <= 32) return run_fwd<T, 8, 64>(a, s, st);
+    return run_fwd<T, 16, 64>(a, s, st);
 }
 
 template <typename T> hipError_t run_step(const ChanArgs& a, const ChanShape& s, float* state, hipStream_t st) {
@@ -306,25 +356,22 @@ template <typename T> hipError_t run_step(const ChanArgs& a, const ChanShape& s,
 hipError_t launch_chan_fwd(const ChanShape& s, const ChanPlan& p, const ChanIn& in, void* y, float* hfin,
                            float* ws, hipStream_t st)
 {
-    ChanArgs a = args_of(s, in, p.R);
+    ChanArgs a = args_of(s, in);
     a.seg = p.seg; a.nseg = p.nseg;
+    a.tpg = (int)(chan_tiles(s, p.cw) / s.G);
     a.y = y; a.hfin = hfin;
     a.S = ws;
     a.sumdt = ws ? ws + s.Bz * p.nseg * s.D * s.N : nullptr;
-    const int64_t es = s.bf16 ? 2 : 4;
-    a.wide = a.per % 4 == 0 && on16(in.u, es, 4) && on16(in.delta, es, 4) && on16(in.gate, es, 4) && on16(y, es, 4) &&
-             (s.ub | s.ur | s.db | s.dr) % 4 == 0 && (!in.gate || (s.zb | s.zr) % 4 == 0);
-    if (s.bf16) return p.R == 4 ? run_fwd_n<u16, 4>(a, s, st) : run_fwd_n<u16, 1>(a, s, st);
-    return p.R == 4 ? run_fwd_n<float, 4>(a, s, st) : run_fwd_n<float, 1>(a, s, st);
+    return s.bf16 ? run_fwd_t<u16>(a, s, p.cw, st) : run_fwd_t<float>(a, s, p.cw, st);
 }
 
 hipError_t launch_chan_step(const ChanShape& s, float* state, const ChanIn& in, void* y, hipStream_t st)
 {
-    ChanArgs a = args_of(s, in, 1);
+    ChanArgs a = args_of(s, in);
     a.y = y;
-    const int64_t es = s.bf16 ? 2 : 4;
-    a.wide = s.N % 4 == 0 && on16(state, 4, 4) && on16(in.A, 4, 4) && on16(in.B, es, 4) && on16(in.C, es, 4) &&
-             (s.Bb | s.Cb) % 4 == 0;
+    const uintptr_t quad = s.bf16 ? 8 : 16;
+    a.wide = s.N % 4 == 0 && on_bytes(state, 16) && on_bytes(in.A, 16) && on_bytes(in.B, quad) &&
+             on_bytes(in.C, quad) && (s.Bb | s.Cb) % 4 == 0;
     return s.bf16 ? run_step<u16>(a, s, state, st) : run_step<float>(a, s, state, st);
 }
 

@@ -41,14 +41,14 @@ struct ChanIn {
     const float *A, *skip, *dbias, *h0;
     const int32_t* lens;
 };
-// How the forward is laid over the GPU (shapes.cpp): R channels per lane (1 or
-// 4; a wavefront covers 16 R channels) and segments of `seg` steps.
+// How the forward is laid over the GPU (shapes.cpp): channels of a workgroup (64
+// or 32), and segments of `seg` steps the sequence is cut into.
 struct ChanPlan {
-    int R;
+    int cw;
     int64_t seg, nseg;
 };
 ChanPlan chan_fwd_plan(const ChanShape& s);
-int64_t chan_tiles(const ChanShape& s, int R);   // wavefronts over the channels of one batch
+int64_t chan_tiles(const ChanShape& s, int cw);   // workgroups over the channels of one batch
 size_t chan_fwd_bytes(const ChanShape& s, const ChanPlan& p);
 hipError_t launch_chan_fwd(const ChanShape& s, const ChanPlan& p, const ChanIn& in, void* y, float* hfin,
                            float* ws, hipStream_t st);

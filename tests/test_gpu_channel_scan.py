@@ -71,6 +71,23 @@ def test_forward(dtype, Bz, L, D, N, G, wide, seqlens, softplus, gate, skip, bia
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Bz,L,D,N,G,seqlens", [
+    (1, 1000, 40, 16, 1, None),               # few channels: cut into segments
+    (3, 900, 24, 5, 3, [900, 0, 411]),        # sequences that end inside, before and at a segment's end
+    (2, 512, 64, 40, 1, [256, 512]),
+])
+def test_segments(dtype, Bz, L, D, N, G, seqlens):
+    log("channel scan segments %s" % ((dtype, Bz, L, D, N, G, seqlens),))
+    d = inputs(Bz, L, D, N, G, dtype, L, wide=2)
+    assert ssd.channel_scan_fwd_workspace_bytes(d["u"], d["delta"], d["A"], d["B"], d["C"]) > 0
+    y, h = ssd.channel_scan_fwd(**d, softplus=True, seqlens=lens_of(seqlens), return_final_state=True)
+    torch.cuda.synchronize()
+    want = want_of(d, True, seqlens, adds=L / 16)   # segments have at least 16 steps, and a sum of dt no more than L / 2
+    ref.check("y", y, want, dtype)
+    ref.check("final_state", h, want, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_extreme_step_sizes(dtype):
     # softplus over its whole range: steps that vanish, and steps so long that
     # nothing of the state is left
