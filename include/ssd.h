@@ -340,6 +340,31 @@ ssd_status ssd_channel_scan_fwd(const ssd_channel_desc* desc, const void* u, con
                                 float* final_state, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/* Gradients for the upstream dy and (NULL = zero) dfinal_state.  du, ddelta,
+ * dB, dC and dgate (required exactly when gate is given) are dense in the
+ * call's dtype; dA, dskip, ddelta_bias (the latter two required exactly when
+ * their input is given) and dinitial_state (may be NULL) float32.  dB and dC
+ * are summed over their group's channels in float32 and rounded once.  The
+ * sums' order is fixed: repeated calls give the same bits. */
+typedef struct ssd_channel_grads {
+    void* du;
+    void* ddelta;
+    void* dgate;
+    void* dB;
+    void* dC;
+    float* dA;
+    float* dskip;
+    float* ddelta_bias;
+    float* dinitial_state;
+} ssd_channel_grads;
+ssd_status ssd_channel_scan_bwd_workspace_bytes(const ssd_channel_desc* desc, size_t* bytes);
+ssd_status ssd_channel_scan_bwd(const ssd_channel_desc* desc, const void* u, const void* delta,
+                                const float* A, const void* B, const void* C, const float* skip,
+                                const void* gate, const float* delta_bias,
+                                const float* initial_state, const int32_t* seqlens, const void* dy,
+                                const float* dfinal_state, const ssd_channel_grads* grads,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* One token: state [batch][channels][dstate] is updated in place and y
  * [batch][channels] written; rows of u, delta, gate, B and C are at
  * b*bstride (seqlen must be 1). */

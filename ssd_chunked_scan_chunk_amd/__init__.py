@@ -28,7 +28,8 @@ __all__ = ["chunk_scan_fwd", "chunk_scan_fwd_noalloc", "chunk_scan_bwd", "bwd_wo
            "chunk_scan", "fwd_plan", "workspace_bytes", "SSDError", "SSD_ALGO_AUTO",
            "SSD_ALGO_MFMA", "SSD_ALGO_VALU", "library_path", "short_conv_fwd", "short_conv_bwd",
            "short_conv_bwd_workspace_bytes", "short_conv_step", "channel_scan_fwd",
-           "channel_scan_fwd_workspace_bytes", "channel_step"]
+           "channel_scan_fwd_workspace_bytes", "channel_scan_bwd", "channel_scan_bwd_workspace_bytes",
+           "channel_step"]
 
 
 def library_path() -> str:
@@ -392,6 +393,6 @@ def chunk_scan(X, a, B, C, chunk, states_in=None, seg_chunks=1, Y=None, wg_units
 
 
 # the operators around the chunked scan (they use the checks above)
-from .layer import (channel_scan_fwd, channel_scan_fwd_workspace_bytes,  # noqa: E402
-                    channel_step, short_conv_bwd, short_conv_bwd_workspace_bytes, short_conv_fwd,
-                    short_conv_step)
+from .layer import (channel_scan_bwd, channel_scan_bwd_workspace_bytes,  # noqa: E402
+                    channel_scan_fwd, channel_scan_fwd_workspace_bytes, channel_step, short_conv_bwd,
+                    short_conv_bwd_workspace_bytes, short_conv_fwd, short_conv_step)

@@ -33,6 +33,7 @@ EXPORTS = (
     "ssd_chunk_scan_bwd", "ssd_bwd_da_workspace_bytes", "ssd_bwd_da", "ssd_chunk_scan_fwd_noalloc",
     "ssd_stream_rmw", "ssd_short_conv_fwd", "ssd_short_conv_bwd_workspace_bytes", "ssd_short_conv_bwd",
     "ssd_short_conv_step", "ssd_channel_scan_fwd_workspace_bytes", "ssd_channel_scan_fwd", "ssd_channel_step",
+    "ssd_channel_scan_bwd_workspace_bytes", "ssd_channel_scan_bwd",
 )
 SSD_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -66,6 +67,11 @@ class ChannelDesc(ctypes.Structure):
                 ("batch", "seqlen", "channels", "dstate", "ngroups", "u_bstride", "u_rstride", "delta_bstride",
                  "delta_rstride", "gate_bstride", "gate_rstride", "B_bstride", "B_rstride", "C_bstride",
                  "C_rstride")] + [("dtype", ctypes.c_int32), ("softplus", ctypes.c_int32)]
+
+
+class ChannelGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("du", "ddelta", "dgate", "dB", "dC", "dA", "dskip", "ddelta_bias",
+                                               "dinitial_state")]
 
 
 class SSDError(RuntimeError):
@@ -111,8 +117,10 @@ def load(path: str = LIB_PATH):
     ph = ctypes.POINTER(ChannelDesc)
     lib.ssd_channel_scan_fwd_workspace_bytes.argtypes = [ph, ctypes.POINTER(sz)]
     lib.ssd_channel_scan_fwd.argtypes = [ph] + [vp] * 13 + [sz, vp]
+    lib.ssd_channel_scan_bwd_workspace_bytes.argtypes = [ph, ctypes.POINTER(sz)]
+    lib.ssd_channel_scan_bwd.argtypes = [ph] + [vp] * 12 + [ctypes.POINTER(ChannelGrads), vp, sz, vp]
     lib.ssd_channel_step.argtypes = [ph] + [vp] * 11
-    for f in ("ssd_channel_scan_fwd_workspace_bytes", "ssd_channel_scan_fwd", "ssd_channel_step", "ssd_short_conv_fwd", "ssd_short_conv_bwd_workspace_bytes", "ssd_short_conv_bwd", "ssd_short_conv_step",
+    for f in ("ssd_channel_scan_bwd_workspace_bytes", "ssd_channel_scan_bwd", "ssd_channel_scan_fwd_workspace_bytes", "ssd_channel_scan_fwd", "ssd_channel_step", "ssd_short_conv_fwd", "ssd_short_conv_bwd_workspace_bytes", "ssd_short_conv_bwd", "ssd_short_conv_step",
               "ssd_fwd_workspace_bytes", "ssd_fwd_plan", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_noalloc",
               "ssd_step",
               "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan",

@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libssd.so")
 SOURCES = ["api.cpp", "shapes.cpp", "kernels_scan.hip", "kernels_mfma.hip", "kernels_fwd.hip", "kernels_step.hip",
            "kernels_bwd.hip", "noalloc.hip", "kernels_conv.hip",
-           "kernels_channel.hip"]
+           "kernels_channel.hip", "kernels_channel_bwd.hip"]
 
 
 def hipcc() -> str:

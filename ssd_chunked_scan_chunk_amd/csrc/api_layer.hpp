@@ -122,8 +122,10 @@ ssd_status chan_shape(const ssd_channel_desc* d, ssd::ChanShape* s) {
     SSD_CHECK(check_stride("gate", d->batch, d->gate_bstride, d->seqlen, d->gate_rstride));
     SSD_CHECK(check_stride("B", d->batch, d->B_bstride, d->seqlen, d->B_rstride));
     SSD_CHECK(check_stride("C", d->batch, d->C_bstride, d->seqlen, d->C_rstride));
-    // the per-state kernels launch a thread for every (batch, channel, state)
-    if (d->batch * d->channels * 64 >= ((int64_t)1 << 32))
+    // the per-state kernels launch a thread for every (batch, channel, state), of
+    // channels rounded up to 64 for every group
+    const int64_t padded = d->ngroups * ((d->channels / d->ngroups + 63) / 64 * 64);
+    if (d->batch * padded * 64 >= ((int64_t)1 << 32))
         return fail(SSD_ERR_UNSUPPORTED, "batch*channels too large for one launch");
     s->Bz = d->batch; s->L = d->seqlen; s->D = d->channels; s->N = d->dstate; s->G = d->ngroups;
     s->ub = d->u_bstride; s->ur = d->u_rstride; s->db = d->delta_bstride; s->dr = d->delta_rstride;
@@ -165,6 +167,14 @@ ssd_status check_chan_in(const ssd::ChanShape& s, const ssd::ChanIn& in, Range* 
     r[7] = rng("delta_bias", in.dbias, s.D * 4);
     r[8] = rng("initial_state", in.h0, s.Bz * s.D * s.N * 4);
     r[9] = rng("seqlens", in.lens, s.Bz * 4);
+    return SSD_OK;
+}
+
+// The sums of dB and dC launch a thread for every (batch, step, group, B or C,
+// padded state).
+ssd_status check_chan_bwd(const ssd::ChanShape& s) {
+    if (s.Bz * s.L > ((int64_t)1 << 31) / (s.G * 128))
+        return fail(SSD_ERR_UNSUPPORTED, "batch*seqlen*ngroups too large for one launch of the backward");
     return SSD_OK;
 }
 
@@ -312,6 +322,65 @@ ssd_status ssd_channel_scan_fwd(const ssd_channel_desc* desc, const void* u, con
     const hipError_t e = ssd::launch_chan_fwd(s, p, in, y, final_state, need > 0 ? static_cast<float*>(workspace) : nullptr,
                                               reinterpret_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : hip_fail(e, "per-channel scan launch");
+}
+
+ssd_status ssd_channel_scan_bwd_workspace_bytes(const ssd_channel_desc* desc, size_t* bytes) {
+    if (!bytes) return fail(SSD_ERR_NULL, "bytes is NULL");
+    ssd::ChanShape s;
+    SSD_CHECK(chan_shape(desc, &s));
+    SSD_CHECK(check_chan_bwd(s));
+    *bytes = ssd::chan_bwd_plan(s).off[9];
+    return ok();
+}
+
+ssd_status ssd_channel_scan_bwd(const ssd_channel_desc* desc, const void* u, const void* delta, const float* A,
+                                const void* B, const void* C, const float* skip, const void* gate,
+                                const float* delta_bias, const float* initial_state, const int32_t* seqlens,
+                                const void* dy, const float* dfinal_state, const ssd_channel_grads* grads,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    ssd::ChanShape s;
+    SSD_CHECK(chan_shape(desc, &s));
+    SSD_CHECK(check_chan_bwd(s));
+    if (!grads) return fail(SSD_ERR_NULL, "grads is NULL");
+    const ssd_channel_grads& o = *grads;
+    const ssd::ChanIn in{u, delta, B, C, gate, A, skip, delta_bias, initial_state, seqlens};
+    Range r[kChanIn + 2];
+    SSD_CHECK(check_chan_in(s, in, r));
+    const int64_t es = s.bf16 ? 2 : 4, nx = s.Bz * s.L * s.D * es, nbc = s.Bz * s.L * s.G * s.N * es;
+    const int64_t nh = s.Bz * s.D * s.N * 4;
+    if (!o.dA || (s.Bz > 0 && s.L > 0 && (!dy || !o.du || !o.ddelta || !o.dB || !o.dC)))
+        return fail(SSD_ERR_NULL, "dy, du, ddelta, dA, dB and dC are required");
+    if ((s.Bz > 0 && s.L > 0 && !gate != !o.dgate) || !skip != !o.dskip || !delta_bias != !o.ddelta_bias)
+        return fail(SSD_ERR_NULL, "dgate, dskip and ddelta_bias are required exactly when their input is given");
+    struct { const char* name; const void* p; size_t n; int64_t bytes; } const outs[] = {
+        {"du", o.du, (size_t)es, nx}, {"ddelta", o.ddelta, (size_t)es, nx}, {"dgate", o.dgate, (size_t)es, nx},
+        {"dB", o.dB, (size_t)es, nbc}, {"dC", o.dC, (size_t)es, nbc}, {"dA", o.dA, 4, s.D * s.N * 4},
+        {"dskip", o.dskip, 4, s.D * 4}, {"ddelta_bias", o.ddelta_bias, 4, s.D * 4},
+        {"dinitial_state", o.dinitial_state, 4, nh}};
+    Range out[10];
+    for (int i = 0; i < 9; ++i) {
+        SSD_CHECK(check_aligned(outs[i].name, outs[i].p, outs[i].n));
+        out[i] = rng(outs[i].name, outs[i].p, outs[i].bytes);
+    }
+    SSD_CHECK(check_aligned("dy", dy, es));
+    SSD_CHECK(check_aligned("dfinal_state", dfinal_state, 4));
+    r[kChanIn] = rng("dy", dy, nx);
+    r[kChanIn + 1] = rng("dfinal_state", dfinal_state, nh);
+    const ssd::ChanBwdPlan p = ssd::chan_bwd_plan(s);
+    SSD_CHECK(check_workspace(workspace, workspace_bytes, p.off[9]));
+    out[9] = rng("workspace", workspace, (int64_t)p.off[9]);
+    SSD_CHECK(check_disjoint(out, 10, r, kChanIn + 2));
+    hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+    hipError_t e;
+    if (s.Bz == 0) {   // no rows: the parameters' gradients are zero
+        e = ssd::launch_fill_zero(o.dA, s.D * s.N, hs);
+        if (e == hipSuccess && o.dskip) e = ssd::launch_fill_zero(o.dskip, s.D, hs);
+        if (e == hipSuccess && o.ddelta_bias) e = ssd::launch_fill_zero(o.ddelta_bias, s.D, hs);
+        return e == hipSuccess ? ok() : hip_fail(e, "empty scan gradient");
+    }
+    const ssd::ChanGrads gr{o.du, o.ddelta, o.dgate, o.dB, o.dC, o.dA, o.dskip, o.ddelta_bias, o.dinitial_state};
+    e = ssd::launch_chan_bwd(s, p, in, dy, dfinal_state, gr, workspace, hs);
+    return e == hipSuccess ? ok() : hip_fail(e, "per-channel scan backward launch");
 }
 
 ssd_status ssd_channel_step(const ssd_channel_desc* desc, float* state, const void* u, const void* delta,

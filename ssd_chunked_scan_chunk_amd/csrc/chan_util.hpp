@@ -79,4 +79,18 @@ __device__ __forceinline__ int64_t chan_length(const int32_t* lens, int64_t b, i
     return n < 0 ? 0 : n > L ? L : n;
 }
 
+inline ChanArgs chan_args(const ChanShape& s, const ChanIn& in) {
+    ChanArgs a = {};
+    a.in = in;
+    a.L = s.L; a.D = s.D; a.N = (int)s.N;
+    a.ub = s.ub; a.db = s.db; a.Bb = s.Bb; a.Cb = s.Cb;
+    a.zb = in.gate ? s.zb : s.ub;   // without a gate the kernels load u in its place
+    const uint32_t es = s.bf16 ? 2 : 4;
+    a.ur = (uint32_t)s.ur * es; a.dr = (uint32_t)s.dr * es; a.zr = (uint32_t)(in.gate ? s.zr : s.ur) * es;
+    a.Br = (uint32_t)s.Br * es; a.Cr = (uint32_t)s.Cr * es;
+    a.per = (int)(s.D / s.G);
+    a.softplus = s.softplus;
+    return a;
+}
+
 }  // namespace ssd

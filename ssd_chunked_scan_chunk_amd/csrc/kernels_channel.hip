@@ -299,20 +299,6 @@ __global__ __launch_bounds__(256) void k_chan_step(ChanArgs a, float* __restrict
     if (on && n0 == 0) Elem<T>::store((T*)a.y + b * a.D + ch, y);
 }
 
-ChanArgs args_of(const ChanShape& s, const ChanIn& in) {
-    ChanArgs a = {};
-    a.in = in;
-    a.L = s.L; a.D = s.D; a.N = (int)s.N;
-    a.ub = s.ub; a.db = s.db; a.Bb = s.Bb; a.Cb = s.Cb;
-    a.zb = in.gate ? s.zb : s.ub;   // without a gate the kernels load u in its place
-    const uint32_t es = s.bf16 ? 2 : 4;
-    a.ur = (uint32_t)s.ur * es; a.dr = (uint32_t)s.dr * es; a.zr = (uint32_t)(in.gate ? s.zr : s.ur) * es;
-    a.Br = (uint32_t)s.Br * es; a.Cr = (uint32_t)s.Cr * es;
-    a.per = (int)(s.D / s.G);
-    a.softplus = s.softplus;
-    return a;
-}
-
 bool on_bytes(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 template <typename T, int NR, int CW> hipError_t run_fwd(const ChanArgs& a, const ChanShape& s, hipStream_t st) {
@@ -356,7 +342,7 @@ template <typename T> hipError_t run_step(const ChanArgs& a, const ChanShape& s,
 hipError_t launch_chan_fwd(const ChanShape& s, const ChanPlan& p, const ChanIn& in, void* y, float* hfin,
                            float* ws, hipStream_t st)
 {
-    ChanArgs a = args_of(s, in);
+    ChanArgs a = chan_args(s, in);
     a.seg = p.seg; a.nseg = p.nseg;
     a.tpg = (int)(chan_tiles(s, p.cw) / s.G);
     a.y = y; a.hfin = hfin;
@@ -367,7 +353,7 @@ hipError_t launch_chan_fwd(const ChanShape& s, const ChanPlan& p, const ChanIn& 
 
 hipError_t launch_chan_step(const ChanShape& s, float* state, const ChanIn& in, void* y, hipStream_t st)
 {
-    ChanArgs a = args_of(s, in);
+    ChanArgs a = chan_args(s, in);
     a.y = y;
     const uintptr_t quad = s.bf16 ? 8 : 16;
     a.wide = s.N % 4 == 0 && on_bytes(state, 16) && on_bytes(in.A, 16) && on_bytes(in.B, quad) &&

@@ -1,0 +1,643 @@
+// kernels_channel_bwd.hip -- gradients of the scan with one decay per channel
+// and state (kernels_channel.hip) on gfx950.
+//
+// With e = e^{dt A}, d = dy silu(gate) and the adjoint g[t] of h[t],
+//     g[t] = d[t] C[t] + e[t+1] g[t+1],       m[t] = e[t] g[t] h[t-1],
+//     dB = sum_c g dt u,  dC = sum_c h d,  dA = sum_t m dt,
+//     du = dt sum_n g B + skip d,  d(dt) = u sum_n g B + sum_n m A,
+//     dgate = dy (sum_n h C + skip u) silu'(gate),
+// and ddelta = d(dt) softplus'(delta + bias).  The states are not kept by the
+// forward: a first pass writes them at every eighth step (a quarter of the
+// inputs' own bytes per state), and the main pass walks the batches of eight steps
+// backwards, runs each forward again with its states and decays in registers and
+// then takes the eight steps in reverse, the adjoint staying in registers
+// throughout.  About 18 vector instructions per (step, channel, state), against
+// some 60 bytes per (step, channel): bound by vector issue.
+//
+// The layout is the forward's: a workgroup owns CW channels of a group, a thread
+// NR of a channel's states; dt, dt u and d are formed once per (step, channel) and
+// the sums over states finished through LDS.  The sums over channels of dB and
+// dC take the CW lanes of a wavefront together, halving the number of values a
+// lane holds with the number of lanes that hold parts of one; each workgroup
+// writes its sums, and a last kernel adds the workgroups' in a fixed order.
+// Few channels: the sequence is cut into segments, whose end states and adjoints
+// from zero the first pass also finds (the adjoint in forward order, weighted by
+// the decay since the segment's start).
+#include <type_traits>
+
+#include "chan_util.hpp"
+
+namespace ssd {
+
+namespace {
+
+template <int V> using Int = std::integral_constant<int, V>;
+
+constexpr int TB = 8;   // steps of a batch
+
+struct BwdArgs {
+    ChanArgs f;
+    const void* dy;
+    const float* dh;              // dfinal_state
+    void *du, *ddelta, *dgate;
+    float* dh0;                   // dinitial_state
+    // workspace: states at the start of every batch [b][batch][tile][thread][NR]
+    // and, with several segments, the sums of dt before them [b][batch][tile][CW]
+    float *ck, *cdt;
+    // per segment [b][seg][tile][thread][NR]: state and adjoint from zero, then
+    // (k_chan_link) those that enter it; its sum of dt [b][seg][tile][CW]
+    float *hs, *gs, *sumdt;
+    float* pbc;                   // [b][t][tile][B, C][NP]: sums over a workgroup's channels
+    float *pA, *pskip, *pbias;    // [b][seg][channel]([state])
+    int tiles, nb;                // workgroups along the channels, batches of a segment
+};
+
+// A wavefront's reduction of NV values over W neighbouring lanes (64 or 32): lane l
+// is left with values index(l) .. of sum over the lanes.  Each level pairs
+// lanes, which hand over one half of their values each.
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+template <int NV, int W> struct LaneSum {
+    static constexpr int kLeft = NV > W ? NV / W : 1;
+    // first value of lane l; lanes that share one (NV < W) hold the same sum
+    __device__ static int index(int l) {
+        int at = 0, m = NV;
+#pragma unroll
+        for (int d = W / 2; d >= 1; d >>= 1)
+            if (m > 1) {
+                m /= 2;
+                if (l & d) at += m;
+            }
+        return at;
+    }
+    template <int D, int M> __device__ static void level(float (&v)[NV], int l) {
+        if constexpr (D >= 1) {
+            if constexpr (M > 1) {
+#pragma unroll
+                for (int j = 0; j < M / 2; ++j) {
+                    const float a = v[j], b = v[j + M / 2];
+                    if constexpr (D >= 16) {
+                        const unsigned x = __float_as_uint(a), y = __float_as_uint(b);
+                        const auto r = D == 32 ? __builtin_amdgcn_permlane32_swap(x, y, false, false)
+                                               : __builtin_amdgcn_permlane16_swap(x, y, false, false);
+                        v[j] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+                    } else {
+                        const float keep = (l & D) ? b : a, give = (l & D) ? a : b;
+                        v[j] = keep + across<D>(give);
+                    }
+                }
+                level<D / 2, M / 2>(v, l);
+            } else {
+                if constexpr (D >= 16) v[0] += __shfl_xor(v[0], D, 64);
+                else v[0] += across<D>(v[0]);
+                level<D / 2, 1>(v, l);
+            }
+        }
+    }
+    // the partner's value: row rotation by 8, mirror of 8, quad exchanges (each
+    // pairs a lane with one of the other half of its group)
+    template <int D> __device__ static float across(float v) {
+        if constexpr (D == 8) return dpp<0x128>(v);
+        else if constexpr (D == 4) return dpp<0x141>(v);
+        else if constexpr (D == 2) return dpp<0x4E>(v);
+        else return dpp<0xB1>(v);
+    }
+    __device__ static void run(float (&v)[NV], int l) { level<W / 2, NV>(v, l); }
+};
+
+// The states at the start of every batch.  SEGS: from zero, with the segment's
+// adjoint, state and sum of dt; otherwise from the initial state.
+template <typename T, int NR, int CW, bool SEGS>
+__global__ __launch_bounds__(256) void k_chan_states(BwdArgs a)
+{
+    constexpr int ES = sizeof(T), NPART = 256 / CW, NP = NPART * NR;
+    constexpr int TP = TB * CW / 256;
+    constexpr int NBC = TB * NP * (SEGS ? 2 : 1), NE = (NBC + 255) / 256;
+    constexpr bool EXACT = ES == 4;
+    const ChanArgs& f = a.f;
+    __shared__ float2 s_dt[2][TB][CW];
+    __shared__ float s_d[SEGS ? 2 : 1][SEGS ? TB : 1][CW];
+    __shared__ __align__(16) float s_bc[2][NBC];
+    const int tid = threadIdx.x, c = tid & (CW - 1), part = tid / CW, n0 = part * NR;
+    const int tile = blockIdx.x, g = tile / f.tpg, cg = (tile - g * f.tpg) * CW + c;
+    const int cl = cg < f.per ? cg : f.per - 1;   // threads past the group repeat its last channel
+    const uint32_t col = (uint32_t)cl * ES;
+    const int64_t gch = (int64_t)g * f.per, ch = gch + cl, b = blockIdx.z, seg = blockIdx.y;
+    const int64_t ts = seg * f.seg, t1 = ts + f.seg < f.L ? ts + f.seg : f.L;
+    const int64_t len = chan_length(f.in.lens, b, f.L);
+    const int te = (int)(len < ts ? 0 : (len < t1 ? len : t1) - ts);
+    const bool gated = f.in.gate != nullptr;
+
+    float A2[NR], h[NR], G[NR] = {}, P[NR], sum = 0.f;
+    const float bias = f.in.dbias ? f.in.dbias[ch] : 0.f;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const bool in = n0 + i < f.N;
+        A2[i] = in ? f.in.A[ch * f.N + n0 + i] * kLog2e : 0.f;
+        h[i] = !SEGS && in && f.in.h0 ? f.in.h0[(b * f.D + ch) * f.N + n0 + i] : 0.f;
+        P[i] = 1.f;
+    }
+    RowIn up = row_in(f.in.u, (b * f.ub + gch) * ES + ts * f.ur);
+    RowIn dp = row_in(f.in.delta, (b * f.db + gch) * ES + ts * f.dr);
+    RowIn zp = row_in(gated ? f.in.gate : f.in.u, (b * f.zb + gch) * ES + ts * f.zr);
+    RowIn Bp = row_in(f.in.B, (b * f.Bb + (int64_t)g * f.N) * ES + ts * f.Br);
+    RowIn Cp = row_in(f.in.C, (b * f.Cb + (int64_t)g * f.N) * ES + ts * f.Cr);
+    const uint32_t yr = (uint32_t)f.D * ES;
+    RowIn gp = row_in(a.dy, ((b * f.L + ts) * f.D + gch) * ES);
+
+    uint32_t ou[TP], od[TP], oz[TP], og[TP], obc[NE];
+    auto offsets = [&](int last) {
+#pragma unroll
+        for (int k = 0; k < TP; ++k) {
+            const int s = part + k * NPART;
+            const uint32_t r = s < last ? s : last;
+            ou[k] = r * f.ur + col;
+            od[k] = r * f.dr + col;
+            oz[k] = r * f.zr + col;
+            og[k] = r * yr + col;
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const int i = e * 256 + tid, s = i / (SEGS ? 2 * NP : NP), n = i & (NP - 1);
+            const uint32_t r = s < last ? s : last;
+            obc[e] = r * (SEGS && (i & NP) ? f.Cr : f.Br) + (uint32_t)(n < f.N ? n : f.N - 1) * ES;
+        }
+    };
+    T ru[2][TP], rd[2][TP], rz[2][TP], rg[2][TP], rbc[2][NE];
+    auto fetch = [&](auto slot, int last) {
+        constexpr int Q = decltype(slot)::value;
+        if (last < TB - 1) offsets(last);
+#pragma unroll
+        for (int k = 0; k < TP; ++k) {
+            ru[Q][k] = load_at<T>(up, ou[k]);
+            rd[Q][k] = load_at<T>(dp, od[k]);
+            if (SEGS) {
+                rz[Q][k] = load_at<T>(zp, oz[k]);
+                rg[Q][k] = load_at<T>(gp, og[k]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+            rbc[Q][e] = SEGS && ((e * 256 + tid) & NP) ? load_at<T>(Cp, obc[e]) : load_at<T>(Bp, obc[e]);
+        up += TB * (uint64_t)f.ur;
+        dp += TB * (uint64_t)f.dr;
+        zp += TB * (uint64_t)f.zr;
+        gp += TB * (uint64_t)yr;
+        Bp += TB * (uint64_t)f.Br;
+        Cp += TB * (uint64_t)f.Cr;
+    };
+    auto prepare = [&](int t, auto slot) {
+        constexpr int Q = decltype(slot)::value;
+#pragma unroll
+        for (int k = 0; k < TP; ++k) {
+            const int s = part + k * NPART;
+            const bool on = t + s < te;
+            const float x = as_f32(rd[Q][k]) + bias, sp = softplus_of<EXACT>(x);
+            float dt = f.softplus ? sp : x;
+            dt = on ? dt : 0.f;
+            s_dt[Q][s][c] = make_float2(dt, dt * as_f32(ru[Q][k]));
+            if (SEGS) {
+                const float z = as_f32(rz[Q][k]), sz = z * sigmoid_of(z);
+                const float d = as_f32(rg[Q][k]) * (gated ? sz : 1.f);
+                s_d[Q][s][c] = on ? d : 0.f;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const int i = e * 256 + tid;
+            if (NBC % 256 == 0 || i < NBC) s_bc[Q][i] = (i & (NP - 1)) < f.N ? as_f32(rbc[Q][e]) : 0.f;
+        }
+    };
+    int64_t at = (b * f.nseg + seg) * a.nb * a.tiles + tile;   // (batch, tile)
+    auto batch = [&](int t, auto slot) {
+        constexpr int Q = decltype(slot)::value;
+        if (t + 2 * TB < te) fetch(slot, te - 1 - t - 2 * TB);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) a.ck[(at * 256 + tid) * NR + i] = h[i];
+        if (SEGS && part == 0) a.cdt[at * CW + c] = sum;
+        at += a.tiles;
+        lds_barrier();
+#pragma unroll
+        for (int k = 0; k < TB; ++k) {
+            const float2 d = s_dt[Q][k][c];
+            const float* bc = s_bc[Q] + k * (NBC / TB) + n0;
+            if (SEGS) sum += d.x;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const float e = fast_exp2(d.x * A2[i]);
+                h[i] = fmaf(e, h[i], d.y * bc[i]);
+                if constexpr (SEGS) {
+                    P[i] *= e;
+                    G[i] = fmaf(P[i], s_d[Q][k][c] * bc[NP + i], G[i]);
+                }
+            }
+        }
+        if (t + TB < te) prepare(t + TB, Int<Q ^ 1>());
+    };
+    if (te > 0) {
+        offsets(TB - 1);
+        fetch(Int<0>(), te - 1);
+        if (TB < te) fetch(Int<1>(), te - 1 - TB);
+        prepare(0, Int<0>());
+        for (int t = 0; t < te; t += 2 * TB) {
+            batch(t, Int<0>());
+            if (t + TB < te) batch(t + TB, Int<1>());
+        }
+    }
+    if constexpr (SEGS) {
+        const int64_t s = (b * f.nseg + seg) * a.tiles + tile;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            a.hs[(s * 256 + tid) * NR + i] = h[i];
+            a.gs[(s * 256 + tid) * NR + i] = G[i];
+        }
+        if (part == 0) a.sumdt[s * CW + c] = sum;
+    }
+}
+
+// Segments joined: hs[seg] becomes the state that enters it, gs[seg] the adjoint
+// that enters it from behind.  One thread per (batch, tile, thread, state).
+template <int NR, int CW>
+__global__ __launch_bounds__(256) void k_chan_link(BwdArgs a, int64_t items)
+{
+    const ChanArgs& f = a.f;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= items) return;
+    const int64_t per_b = (int64_t)a.tiles * 256 * NR, b = i / per_b, k = i - b * per_b;
+    const int tile = (int)(k / (256 * NR)), rest = (int)(k - (int64_t)tile * 256 * NR), tid = rest / NR;
+    const int c = tid & (CW - 1), n = tid / CW * NR + rest % NR;
+    const int g = tile / f.tpg, cg = (tile - g * f.tpg) * CW + c;
+    const int64_t ch = (int64_t)g * f.per + (cg < f.per ? cg : f.per - 1), at = (b * f.D + ch) * f.N + n;
+    const bool in = n < f.N;
+    const float A2 = in ? f.in.A[ch * f.N + n] * kLog2e : 0.f;
+    float h = in && f.in.h0 ? f.in.h0[at] : 0.f, gr = in && a.dh ? a.dh[at] : 0.f;
+    float* S = a.hs + b * f.nseg * per_b + k;
+    float* G = a.gs + b * f.nseg * per_b + k;
+    const int64_t per_s = (int64_t)a.tiles * CW;
+    const float* sd = a.sumdt + b * f.nseg * per_s + (int64_t)tile * CW + c;
+    constexpr int U = 8;   // segments in flight
+    for (int64_t s = 0; s < f.nseg; s += U) {
+        float v[U], w[U], d[U], x[U];
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+            if (s + q < f.nseg) {
+                const int64_t r = f.nseg - 1 - s - q;
+                v[q] = S[(s + q) * per_b]; d[q] = sd[(s + q) * per_s];
+                w[q] = G[r * per_b]; x[q] = sd[r * per_s];
+            }
+#pragma unroll
+        for (int q = 0; q < U; ++q)
+            if (s + q < f.nseg) {
+                S[(s + q) * per_b] = h;
+                h = fmaf(fast_exp2(A2 * d[q]), h, v[q]);
+                G[(f.nseg - 1 - s - q) * per_b] = gr;
+                gr = fmaf(fast_exp2(A2 * x[q]), gr, w[q]);
+            }
+    }
+}
+
+template <typename T, int NR, int CW, bool SEGS>
+__global__ __launch_bounds__(256) void k_chan_bwd(BwdArgs a)
+{
+    constexpr int ES = sizeof(T), NPART = 256 / CW, NP = NPART * NR;
+    constexpr int TP = TB * CW / 256, NBC = TB * NP * 2, NE = (NBC + 255) / 256;
+    constexpr bool EXACT = ES == 4;
+    const ChanArgs& f = a.f;
+    __shared__ float2 s_dt[TB][CW];
+    __shared__ float s_d[TB][CW];
+    __shared__ __align__(16) float s_bc[NBC];          // [step][B, C][state]
+    __shared__ float s_part[3][TB][NPART][CW];         // parts of h C, g B and m A
+    const int tid = threadIdx.x, c = tid & (CW - 1), part = tid / CW, n0 = part * NR, lane = tid & 63;
+    const int tile = blockIdx.x, g = tile / f.tpg, cg = (tile - g * f.tpg) * CW + c;
+    const bool live = cg < f.per;
+    // threads past the group repeat its last channel, store nothing and add nothing
+    // to sums over channels
+    const int cl = live ? cg : f.per - 1;
+    const uint32_t col = (uint32_t)cl * ES;
+    const int64_t gch = (int64_t)g * f.per, ch = gch + cl, b = blockIdx.z, seg = blockIdx.y;
+    const int64_t ts = seg * f.seg, t1 = ts + f.seg < f.L ? ts + f.seg : f.L;
+    const int64_t len = chan_length(f.in.lens, b, f.L);
+    const int te = (int)(len < ts ? 0 : (len < t1 ? len : t1) - ts);
+    const bool gated = f.in.gate != nullptr;
+    const int nb = (te + TB - 1) / TB;                 // batches of this segment
+
+    float A2[NR], dA[NR] = {}, carry[NR], hin[NR];
+    const float bias = f.in.dbias ? f.in.dbias[ch] : 0.f, skip = f.in.skip ? f.in.skip[ch] : 0.f;
+    const int64_t sat = (((b * f.nseg + seg) * a.tiles + tile) * 256 + tid) * NR;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const bool in = n0 + i < f.N;
+        A2[i] = in ? f.in.A[ch * f.N + n0 + i] * kLog2e : 0.f;
+        carry[i] = SEGS ? a.gs[sat + i] : in && a.dh ? a.dh[(b * f.D + ch) * f.N + n0 + i] : 0.f;
+        hin[i] = SEGS ? a.hs[sat + i] : 0.f;
+    }
+    const RowIn up = row_in(f.in.u, (b * f.ub + gch) * ES + ts * f.ur);
+    const RowIn dp = row_in(f.in.delta, (b * f.db + gch) * ES + ts * f.dr);
+    const RowIn zp = row_in(gated ? f.in.gate : f.in.u, (b * f.zb + gch) * ES + ts * f.zr);
+    const RowIn Bp = row_in(f.in.B, (b * f.Bb + (int64_t)g * f.N) * ES + ts * f.Br);
+    const RowIn Cp = row_in(f.in.C, (b * f.Cb + (int64_t)g * f.N) * ES + ts * f.Cr);
+    const uint32_t yr = (uint32_t)f.D * ES;
+    const int64_t dense = ((b * f.L + ts) * f.D + gch) * ES;
+    const RowIn gp = row_in(a.dy, dense);
+    const RowOut dup = row_out(a.du, dense), ddp = row_out(a.ddelta, dense), dzp = row_out(a.dgate, dense);
+
+    // the share of batch j of this thread, as in the forward; offsets of whole batches
+    uint32_t ou[TP], od[TP], oz[TP], og[TP], obc[NE];
+    auto offsets = [&](int last) {
+#pragma unroll
+        for (int k = 0; k < TP; ++k) {
+            const int s = part + k * NPART;
+            const uint32_t r = s < last ? s : last;
+            ou[k] = r * f.ur + col;
+            od[k] = r * f.dr + col;
+            oz[k] = r * f.zr + col;
+            og[k] = r * yr + col;
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const int i = e * 256 + tid, s = i / (2 * NP), n = i & (NP - 1);
+            const uint32_t r = s < last ? s : last;
+            obc[e] = r * (i & NP ? f.Cr : f.Br) + (uint32_t)(n < f.N ? n : f.N - 1) * ES;
+        }
+    };
+    T ru[TP], rd[TP], rz[TP], rg[TP], rbc[NE];
+    float rck[NR], rcdt = 0.f;
+    auto fetch = [&](int j) {
+        const uint64_t t = (uint64_t)j * TB;
+#pragma unroll
+        for (int k = 0; k < TP; ++k) {
+            ru[k] = load_at<T>(up + t * f.ur, ou[k]);
+            rd[k] = load_at<T>(dp + t * f.dr, od[k]);
+            rz[k] = load_at<T>(zp + t * f.zr, oz[k]);
+            rg[k] = load_at<T>(gp + t * yr, og[k]);
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+            rbc[e] = (e * 256 + tid) & NP ? load_at<T>(Cp + t * f.Cr, obc[e]) : load_at<T>(Bp + t * f.Br, obc[e]);
+        const int64_t at = ((b * f.nseg + seg) * a.nb + j) * a.tiles + tile;
+#pragma unroll
+        for (int i = 0; i < NR; ++i) rck[i] = a.ck[(at * 256 + tid) * NR + i];
+        if (SEGS) rcdt = a.cdt[at * CW + c];
+    };
+    float u[TP], x[TP], z[TP], dyv[TP], dtv[TP], d[TP], h[NR], sskip = 0.f, sbias = 0.f;
+    auto prepare = [&](int j) {
+#pragma unroll
+        for (int k = 0; k < TP; ++k) {
+            const int s = part + k * NPART;
+            const bool on = j * TB + s < te;   // a step past the end changes nothing
+            x[k] = as_f32(rd[k]) + bias;
+            const float sp = softplus_of<EXACT>(x[k]);
+            dtv[k] = on ? (f.softplus ? sp : x[k]) : 0.f;
+            u[k] = as_f32(ru[k]);
+            z[k] = as_f32(rz[k]);
+            dyv[k] = on ? as_f32(rg[k]) : 0.f;
+            const float sz = z[k] * sigmoid_of(z[k]);
+            d[k] = on ? dyv[k] * (gated ? sz : 1.f) : 0.f;
+            s_dt[s][c] = make_float2(dtv[k], dtv[k] * u[k]);
+            s_d[s][c] = d[k];
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const int i = e * 256 + tid;
+            if (NBC % 256 == 0 || i < NBC) s_bc[i] = (i & (NP - 1)) < f.N ? as_f32(rbc[e]) : 0.f;
+        }
+        // the state entering the batch
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+            h[i] = SEGS ? fmaf(fast_exp2(A2[i] * rcdt), hin[i], rck[i]) : rck[i];
+    };
+
+    if (nb > 0) {
+        offsets(te - 1 - (nb - 1) * TB < TB - 1 ? te - 1 - (nb - 1) * TB : TB - 1);
+        fetch(nb - 1);
+        if (nb > 1) offsets(TB - 1);
+        prepare(nb - 1);
+    }
+    using Sum = LaneSum<TB * 2 * NR, CW>;
+    const int vi = Sum::index(lane);
+    for (int j = nb - 1; j >= 0; --j) {
+        if (j > 0) fetch(j - 1);
+        lds_barrier();
+        // forward: states and decays of the batch
+        float H[TB][NR], E[TB][NR], hfirst[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) hfirst[i] = h[i];
+#pragma unroll
+        for (int k = 0; k < TB; ++k) {
+            const float2 dt = s_dt[k][c];
+            const float* bc = s_bc + k * 2 * NP + n0;
+            float y = 0.f;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                E[k][i] = fast_exp2(dt.x * A2[i]);
+                h[i] = fmaf(E[k][i], h[i], dt.y * bc[i]);
+                H[k][i] = h[i];
+                y = i == 0 ? h[i] * bc[NP + i] : fmaf(h[i], bc[NP + i], y);
+            }
+            s_part[0][k][part][c] = y;
+        }
+        // reverse: E[k] and H[k] give way to the terms of dB and dC
+        float v[TB * 2 * NR];
+#pragma unroll
+        for (int k = TB - 1; k >= 0; --k) {
+            const float2 dt = s_dt[k][c];
+            const float dk = s_d[k][c];
+            const float* bc = s_bc + k * 2 * NP + n0;
+            float fed = 0.f, ma = 0.f;
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const float gr = fmaf(dk, bc[NP + i], carry[i]);
+                fed = i == 0 ? gr * bc[i] : fmaf(gr, bc[i], fed);
+                v[(k * 2) * NR + i] = live ? gr * dt.y : 0.f;
+                v[(k * 2 + 1) * NR + i] = live ? H[k][i] * dk : 0.f;
+                carry[i] = gr * E[k][i];
+                const float m = carry[i] * (k > 0 ? H[k > 0 ? k - 1 : 0][i] : hfirst[i]);
+                dA[i] = fmaf(m, dt.x, dA[i]);
+                ma = i == 0 ? m * A2[i] : fmaf(m, A2[i], ma);
+            }
+            s_part[1][k][part][c] = fed;
+            s_part[2][k][part][c] = ma;
+        }
+        Sum::run(v, lane);
+#pragma unroll
+        for (int e = 0; e < Sum::kLeft; ++e) {
+            // value vi + e: state (part's n0 +) i of B or C at step k
+            const int m = vi + e, k = m / (2 * NR), which = m / NR & 1, i = m % NR;
+            const int64_t t = ts + (int64_t)j * TB + k;
+            // lanes that share a value store it more than once, the same bits
+            if (j * TB + k < te) a.pbc[(((b * f.L + t) * a.tiles + tile) * 2 + which) * NP + n0 + i] = v[e];
+        }
+        lds_barrier();
+        // this thread's pairs of the batch
+#pragma unroll
+        for (int k = 0; k < TP; ++k) {
+            const int s = part + k * NPART;
+            float y = 0.f, fed = 0.f, ma = 0.f;
+#pragma unroll
+            for (int q = 0; q < NPART; ++q) {
+                y += s_part[0][s][q][c];
+                fed += s_part[1][s][q][c];
+                ma += s_part[2][s][q][c];
+            }
+            // A2 = A log2(e)
+            const float ddt = fmaf(fed, u[k], ma * 0.69314718f);
+            const float e = exp_neg_abs<EXACT>(x[k]), r = __builtin_amdgcn_rcpf(1.f + e);
+            const float dd = f.softplus ? ddt * (x[k] >= 0.f ? r : e * r) : ddt;
+            const uint32_t at = s * yr + col;
+            const bool on = live && j * TB + s < te;
+            const RowOut row_u = dup + (uint64_t)j * TB * yr, row_d = ddp + (uint64_t)j * TB * yr;
+            if (on) {
+                sskip = fmaf(d[k], u[k], sskip);
+                sbias += dd;
+                store_at(row_u, at, fmaf(fed, dtv[k], skip * d[k]), T());
+                store_at(row_d, at, dd, T());
+                if (gated) {
+                    const float sg = sigmoid_of(z[k]);
+                    store_at(dzp + (uint64_t)j * TB * yr, at,
+                             dyv[k] * fmaf(skip, u[k], y) * (sg * fmaf(z[k], 1.f - sg, 1.f)), T());
+                }
+            }
+        }
+        if (j > 0) prepare(j - 1);
+    }
+
+    for (int64_t s = te + part; s < t1 - ts; s += NPART)
+        if (live) {
+            store_at(dup + s * (uint64_t)yr, col, 0.f, T());
+            store_at(ddp + s * (uint64_t)yr, col, 0.f, T());
+            if (gated) store_at(dzp + s * (uint64_t)yr, col, 0.f, T());
+        }
+    const int64_t row = b * f.nseg + seg;
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+        if (live && n0 + i < f.N) {
+            a.pA[(row * f.D + ch) * f.N + n0 + i] = dA[i];
+            if (a.dh0 && seg == 0) a.dh0[(b * f.D + ch) * f.N + n0 + i] = carry[i];
+        }
+    __syncthreads();
+    float* sum = &s_part[0][0][0][0];
+    sum[tid] = sskip;
+    sum[256 + tid] = sbias;
+    __syncthreads();
+    if (live && part == 0) {
+        sskip = sbias = 0.f;
+#pragma unroll
+        for (int q = 0; q < NPART; ++q) {
+            sskip += sum[q * CW + c];
+            sbias += sum[256 + q * CW + c];
+        }
+        if (a.pskip) a.pskip[row * f.D + ch] = sskip;
+        if (a.pbias) a.pbias[row * f.D + ch] = sbias;
+    }
+}
+
+// dB and dC: the workgroups' sums of a step added, one thread per (batch, step,
+// group, B or C, state); zeros past a sequence's end.
+template <typename T>
+__global__ __launch_bounds__(256) void k_chan_sum_bc(BwdArgs a, int NP, T* __restrict__ dB, T* __restrict__ dC,
+                                                     int64_t items)
+{
+    const ChanArgs& f = a.f;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= items) return;
+    const int G = a.tiles / f.tpg;
+    const int n = (int)(i & (2 * NP - 1));              // [B, C][state]
+    const int64_t r = i / (2 * NP), g = r % G, bt = r / G, b = bt / f.L, t = bt - b * f.L;
+    const int k = n & (NP - 1);
+    if (k >= f.N) return;
+    float s = 0.f;
+    if (t < chan_length(f.in.lens, b, f.L)) {
+        const float* p = a.pbc + ((bt * a.tiles + g * f.tpg) * 2 * NP) + n;
+        int q = 0;
+        for (; q + 4 <= f.tpg; q += 4) {
+            const float v0 = p[(int64_t)q * 2 * NP], v1 = p[(int64_t)(q + 1) * 2 * NP];
+            const float v2 = p[(int64_t)(q + 2) * 2 * NP], v3 = p[(int64_t)(q + 3) * 2 * NP];
+            s += (v0 + v1) + (v2 + v3);
+        }
+        for (; q < f.tpg; ++q) s += p[(int64_t)q * 2 * NP];
+    }
+    Elem<T>::store((n < NP ? dB : dC) + r * f.N + k, s);
+}
+
+// out[i] = sum over the segments of all batches of p[row][i], for dA, dskip and dbias
+__global__ __launch_bounds__(256) void k_chan_sum_rows(const float* __restrict__ pA, float* __restrict__ dA, int64_t nA,
+                                                       const float* __restrict__ ps, float* __restrict__ ds,
+                                                       const float* __restrict__ pb, float* __restrict__ db,
+                                                       int64_t D, int64_t rows)
+{
+    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = nA;
+    const float* p = pA;
+    float* out = dA;
+    if (i >= nA) {
+        i -= nA;
+        n = D;
+        if (i < D) { p = ps; out = ds; }
+        else { i -= D; p = pb; out = db; }
+        if (i >= D) return;
+    }
+    if (!out) return;
+    float s = 0.f;
+    int64_t r = 0;
+    for (; r + 4 <= rows; r += 4) {
+        const float v0 = p[r * n + i], v1 = p[(r + 1) * n + i], v2 = p[(r + 2) * n + i], v3 = p[(r + 3) * n + i];
+        s += (v0 + v1) + (v2 + v3);
+    }
+    for (; r < rows; ++r) s += p[r * n + i];
+    out[i] = s;
+}
+
+template <typename T, int NR, int CW>
+hipError_t run_bwd(const BwdArgs& a, const ChanShape& s, const ChanGrads& o, hipStream_t st) {
+    constexpr int NP = 256 / CW * NR;
+    const dim3 blk(256), grid((unsigned)a.tiles, (unsigned)a.f.nseg, (unsigned)s.Bz);
+    if (s.L > 0) {
+        if (a.f.nseg > 1) {
+            hipLaunchKernelGGL((k_chan_states<T, NR, CW, true>), grid, blk, 0, st, a);
+            const int64_t items = s.Bz * a.tiles * 256 * NR;
+            hipLaunchKernelGGL((k_chan_link<NR, CW>), dim3((unsigned)((items + 255) / 256)), blk, 0, st, a, items);
+        } else {
+            hipLaunchKernelGGL((k_chan_states<T, NR, CW, false>), grid, blk, 0, st, a);
+        }
+    }
+    if (a.f.nseg > 1) hipLaunchKernelGGL((k_chan_bwd<T, NR, CW, true>), grid, blk, 0, st, a);
+    else hipLaunchKernelGGL((k_chan_bwd<T, NR, CW, false>), grid, blk, 0, st, a);
+    if (s.L > 0) {
+        const int64_t items = s.Bz * s.L * s.G * 2 * NP;
+        hipLaunchKernelGGL(k_chan_sum_bc<T>, dim3((unsigned)((items + 255) / 256)), blk, 0, st, a, NP, (T*)o.dB,
+                           (T*)o.dC, items);
+    }
+    const int64_t cols = s.D * (s.N + 2);
+    hipLaunchKernelGGL(k_chan_sum_rows, dim3((unsigned)((cols + 255) / 256)), blk, 0, st, a.pA, o.dA, s.D * s.N, a.pskip,
+                       o.dskip, a.pbias, o.ddbias, s.D, s.Bz * a.f.nseg);
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t run_bwd_t(const BwdArgs& a, const ChanShape& s, const ChanGrads& o, hipStream_t st) {
+    if (s.N <= 8) return run_bwd<T, 2, 64>(a, s, o, st);
+    if (s.N <= 16) return run_bwd<T, 4, 64>(a, s, o, st);
+    if (s.N <= 32) return run_bwd<T, 4, 32>(a, s, o, st);
+    return run_bwd<T, 8, 32>(a, s, o, st);
+}
+
+}  // namespace
+
+hipError_t launch_chan_bwd(const ChanShape& s, const ChanBwdPlan& p, const ChanIn& in, const void* dy,
+                           const float* dh, const ChanGrads& o, void* ws, hipStream_t st)
+{
+    BwdArgs a = {};
+    a.f = chan_args(s, in);
+    a.f.seg = p.seg; a.f.nseg = p.nseg;
+    a.tiles = (int)chan_tiles(s, p.cw);
+    a.f.tpg = (int)(a.tiles / s.G);
+    a.nb = (int)p.nb;
+    a.dy = dy; a.dh = dh;
+    a.du = o.du; a.ddelta = o.ddelta; a.dgate = o.dgate; a.dh0 = o.dh0;
+    auto at = [&](int i) { return reinterpret_cast<float*>(static_cast<char*>(ws) + p.off[i]); };
+    a.ck = at(0); a.cdt = at(1); a.hs = at(2); a.gs = at(3); a.sumdt = at(4); a.pbc = at(5); a.pA = at(6);
+    a.pskip = o.dskip ? at(7) : nullptr;
+    a.pbias = o.ddbias ? at(8) : nullptr;
+    return s.bf16 ? run_bwd_t<u16>(a, s, o, st) : run_bwd_t<float>(a, s, o, st);
+}
+
+}  // namespace ssd

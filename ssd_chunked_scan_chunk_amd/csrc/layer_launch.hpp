@@ -52,6 +52,22 @@ int64_t chan_tiles(const ChanShape& s, int cw);   // workgroups over the channel
 size_t chan_fwd_bytes(const ChanShape& s, const ChanPlan& p);
 hipError_t launch_chan_fwd(const ChanShape& s, const ChanPlan& p, const ChanIn& in, void* y, float* hfin,
                            float* ws, hipStream_t st);
+// The backward's segments (64 or 32 channels per workgroup by the number of
+// states), batches of eight steps per segment, and the workspace's regions: states
+// of the batches and their sums of dt, states, adjoints and sums of dt of the
+// segments, the workgroups' sums of dB and dC, the segments' of dA, dskip, dbias.
+struct ChanBwdPlan {
+    int cw;
+    int64_t seg, nseg, nb;
+    size_t off[10];          // off[9]: bytes in all
+};
+struct ChanGrads {
+    void *du, *ddelta, *dgate, *dB, *dC;
+    float *dA, *dskip, *ddbias, *dh0;
+};
+ChanBwdPlan chan_bwd_plan(const ChanShape& s);
+hipError_t launch_chan_bwd(const ChanShape& s, const ChanBwdPlan& p, const ChanIn& in, const void* dy,
+                           const float* dh, const ChanGrads& o, void* ws, hipStream_t st);
 hipError_t launch_chan_step(const ChanShape& s, float* state, const ChanIn& in, void* y, hipStream_t st);
 
 }  // namespace ssd

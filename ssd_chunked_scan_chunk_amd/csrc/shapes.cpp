@@ -94,4 +94,27 @@ size_t chan_fwd_bytes(const ChanShape& s, const ChanPlan& p) {
     return (size_t)s.Bz * p.nseg * s.D * (s.N + 1) * sizeof(float);
 }
 
+ChanBwdPlan chan_bwd_plan(const ChanShape& s) {
+    ChanBwdPlan p;
+    p.cw = s.N <= 16 ? 64 : 32;
+    const int64_t tiles = chan_tiles(s, p.cw), pieces = 256 / p.cw;
+    const int64_t np = s.N <= 8 ? 8 : s.N <= 16 ? 16 : s.N <= 32 ? 32 : 64, nr = np / pieces;
+    p.nseg = 1;
+    p.seg = s.L > 0 ? (s.L + 7) / 8 * 8 : 8;
+    p.nb = p.seg / 8;
+    const int64_t rows = s.Bz * p.nseg;
+    const bool several = p.nseg > 1;
+    const int64_t floats[9] = {rows * p.nb * tiles * 256 * nr, several ? rows * p.nb * tiles * p.cw : 0,
+                               several ? rows * tiles * 256 * nr : 0, several ? rows * tiles * 256 * nr : 0,
+                               several ? rows * tiles * p.cw : 0, s.Bz * s.L * tiles * 2 * np, rows * s.D * s.N,
+                               rows * s.D, rows * s.D};
+    size_t o = 0;
+    for (int i = 0; i < 9; ++i) {
+        p.off[i] = o;
+        o += ((size_t)floats[i] * 4 + 255) / 256 * 256;
+    }
+    p.off[9] = s.Bz > 0 ? o : 0;
+    return p;
+}
+
 }  // namespace ssd

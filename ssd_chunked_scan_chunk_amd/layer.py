@@ -249,6 +249,43 @@ def channel_scan_fwd(u, delta, A, B, C, skip=None, gate=None, delta_bias=None, s
     return y, final_state
 
 
+def channel_scan_bwd_workspace_bytes(u, delta, A, B, C) -> int:
+    n = ctypes.c_size_t()
+    _lib.check(_L().ssd_channel_scan_bwd_workspace_bytes(
+        _chan_check(u, delta, A, B, C, None, None, None, True, 2), n))
+    return n.value
+
+
+def channel_scan_bwd(u, delta, A, B, C, dy, skip=None, gate=None, delta_bias=None, softplus=False,
+                     initial_state=None, dfinal_state=None, seqlens=None, return_dinitial_state=False,
+                     workspace=None):
+    """Gradients of channel_scan_fwd for upstream dy [Bz,L,D] and dfinal_state
+    (None: zero).
+
+    Returns a dict with du, ddelta, dB, dC and dgate (u's dtype), dA, dskip and
+    ddelta_bias (f32; dgate, dskip, ddelta_bias None without their input) and
+    dinitial_state (f32; None unless requested)."""
+    d = _chan_check(u, delta, A, B, C, skip, gate, delta_bias, softplus, 2)
+    dev, dt, f32, state = u.device, u.dtype, torch.float32, (u.shape[0], u.shape[2], A.shape[1])
+    _need("dy", dy)
+    _check("dy", dy, u.shape, dt, dev)
+    _check("initial_state", initial_state, state, f32, dev)
+    _check("dfinal_state", dfinal_state, state, f32, dev)
+    _seqlens(seqlens, u.shape[0], dev)
+    n = ctypes.c_size_t()
+    _lib.check(_L().ssd_channel_scan_bwd_workspace_bytes(d, n))
+    workspace, wsz = _workspace(workspace, n.value, dev)
+    new = lambda like, dtype, wanted: torch.empty(tuple(like), dtype=dtype, device=dev) if wanted else None
+    g = {"du": new(u.shape, dt, True), "ddelta": new(u.shape, dt, True), "dgate": new(u.shape, dt, gate is not None),
+         "dB": new(B.shape, dt, True), "dC": new(B.shape, dt, True), "dA": new(A.shape, f32, True),
+         "dskip": new(A.shape[:1], f32, skip is not None), "ddelta_bias": new(A.shape[:1], f32, delta_bias is not None),
+         "dinitial_state": new(state, f32, return_dinitial_state)}
+    _enqueue(dev, _L().ssd_channel_scan_bwd, d, _at(u), _at(delta), _at(A), _at(B), _at(C), _at(skip), _at(gate),
+             _at(delta_bias), _at(initial_state), _at(seqlens), _at(dy), _at(dfinal_state),
+             _lib.ChannelGrads(*map(_at, g.values())), _at(workspace), wsz)
+    return g
+
+
 def channel_step(state, u, delta, A, B, C, skip=None, gate=None, delta_bias=None, softplus=False, y=None):
     """One token: state [Bz,D,N] f32 is updated in place.  u, delta, gate [Bz,D] and
     B, C [Bz,G,N] with dense rows.  Returns y [Bz,D]."""

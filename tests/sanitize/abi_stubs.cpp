@@ -73,6 +73,8 @@ hipError_t launch_conv_step(const ConvShape&, void*, const void*, const float*, 
                             hipStream_t) { SSD_STUB; }
 hipError_t launch_chan_fwd(const ChanShape&, const ChanPlan&, const ChanIn&, void*, float*, float*,
                            hipStream_t) { SSD_STUB; }
+hipError_t launch_chan_bwd(const ChanShape&, const ChanBwdPlan&, const ChanIn&, const void*, const float*,
+                           const ChanGrads&, void*, hipStream_t) { SSD_STUB; }
 hipError_t launch_chan_step(const ChanShape&, float*, const ChanIn&, void*, hipStream_t) { SSD_STUB; }
 #undef SSD_STUB
 }  // namespace ssd

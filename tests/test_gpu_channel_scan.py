@@ -1,5 +1,5 @@
-"""GPU parity of the per-channel scan (forward, single-token step) against the
-plain 64-bit form."""
+"""GPU parity of the per-channel scan (forward, backward, single-token step)
+against the plain 64-bit form."""
 import numpy as np
 import pytest
 import torch
@@ -207,3 +207,126 @@ def test_repeats_streams_and_graphs():
         torch.cuda.synchronize()
         for got in (other, held, again):
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---- backward -----------------------------------------------------------------------
+
+def upstream(d, dtype, seed, carry=True):
+    gen = torch.Generator().manual_seed(seed)
+    Bz, L, D = d["u"].shape
+    dy = torch.randn(Bz, L, D, generator=gen).to(DT[dtype]).cuda()
+    return dy, torch.randn(Bz, D, d["A"].shape[1], generator=gen).cuda() if carry else None
+
+
+def check_backward(d, dtype, softplus, seqlens, dy, dh, adds=0):
+    g = ssd.channel_scan_bwd(**d, dy=dy, dfinal_state=dh, softplus=softplus, seqlens=lens_of(seqlens),
+                             return_dinitial_state=True)
+    torch.cuda.synchronize()
+    want = want_of(d, softplus, seqlens, adds=adds, dy=n64(dy), dh=n64(dh))
+    for k in ("du", "ddelta", "dgate", "dB", "dC"):
+        if k != "dgate" or d["gate"] is not None:
+            ref.check(k, g[k], want, dtype)
+    for k, given in (("dA", True), ("dskip", d["skip"] is not None), ("ddelta_bias", d["delta_bias"] is not None),
+                     ("dinitial_state", True)):
+        if given:
+            ref.check(k, g[k], want, "f32")
+        else:
+            assert g[k] is None
+    assert d["gate"] is not None or g["dgate"] is None
+    return g
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Bz,L,D,N,G,wide,seqlens,softplus,gate,skip,bias,carry", SHAPES)
+def test_backward(dtype, Bz, L, D, N, G, wide, seqlens, softplus, gate, skip, bias, carry):
+    log("channel scan bwd %s" % ((dtype, Bz, L, D, N, G, wide, seqlens, softplus, gate, skip, bias, carry),))
+    d = inputs(Bz, L, D, N, G, dtype, L + D, wide, gate, skip, bias, carry)
+    if not softplus:
+        d["delta"] = d["delta"].abs() * 0.1
+    dy, dh = upstream(d, dtype, L, carry)
+    check_backward(d, dtype, softplus, seqlens, dy, dh)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Bz,L,D,N,G,seqlens", [(1, 1000, 40, 16, 1, None), (3, 600, 24, 5, 3, [600, 0, 411]),
+                                                (2, 320, 64, 40, 1, [160, 320])])
+def test_backward_long(dtype, Bz, L, D, N, G, seqlens):
+    # few channels and many steps: segments that sequences end inside, before and at the end of
+    log("channel scan bwd long %s" % ((dtype, Bz, L, D, N, G, seqlens),))
+    d = inputs(Bz, L, D, N, G, dtype, L, wide=2)
+    dy, dh = upstream(d, dtype, L)
+    check_backward(d, dtype, True, seqlens, dy, dh, adds=L)
+
+
+def test_backward_against_differences():
+    # fp32 gradients against central differences of the 64-bit forward along
+    # random directions
+    log("channel scan bwd differences")
+    d = inputs(2, 21, 10, 5, 2, "f32", 8)
+    seqlens = [21, 13]
+    dy, dh = upstream(d, "f32", 9)
+    g = check_backward(d, "f32", True, seqlens, dy, dh)
+    names = {"u": "du", "delta": "ddelta", "A": "dA", "B": "dB", "C": "dC", "skip": "dskip", "gate": "dgate",
+             "delta_bias": "ddelta_bias", "initial_state": "dinitial_state"}
+    base = {k: n64(d[k]) for k in names}
+
+    def loss(v):
+        o = ref.scan(v["u"], v["delta"], v["A"], v["B"], v["C"], v["skip"], v["gate"], v["delta_bias"], True,
+                     v["initial_state"], seqlens)
+        return (o["y"] * n64(dy)).sum() + (o["final_state"] * n64(dh)).sum()
+
+    rng = np.random.default_rng(1)
+    for k, gk in names.items():
+        r = rng.standard_normal(base[k].shape)
+        step = 1e-5
+        num = (loss({**base, k: base[k] + step * r}) - loss({**base, k: base[k] - step * r})) / (2 * step)
+        ours = n64(g[gk])
+        # truncation ~ step^2, cancellation ~ 1e-16 |loss| / step, the gradient's own fp32 error
+        assert abs(num - (ours * r).sum()) <= 1e-5 * (np.abs(ours * r).sum() + 1), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_backward_rows_behind_the_end(dtype):
+    log("channel scan bwd NaN behind the end %s" % dtype)
+    d = inputs(3, 40, 48, 16, 2, dtype, 4)
+    seqlens = [0, 40, 22]
+    dy, dh = upstream(d, dtype, 5)
+    run = lambda: ssd.channel_scan_bwd(**d, dy=dy, dfinal_state=dh, softplus=True, seqlens=lens_of(seqlens),
+                                       return_dinitial_state=True)
+    g0 = run()
+    for t in (d["u"], d["delta"], d["gate"], d["B"], d["C"], dy):
+        for b, n in enumerate(seqlens):
+            t[b, n:] = float("nan")
+    g1 = run()
+    torch.cuda.synchronize()
+    for k in g0:
+        assert torch.equal(g0[k], g1[k]), k
+    for k in ("du", "ddelta", "dgate", "dB", "dC"):
+        assert not g0[k][0].any() and not g0[k][2, 22:].any(), k
+    assert torch.equal(g0["dinitial_state"][0], dh[0])
+
+
+def test_backward_repeats_streams_and_graphs():
+    log("channel scan bwd streams and graphs")
+    for L in (70, 900):
+        d = inputs(2, L, 80, 16, 1, "bf16", 6, wide=16)
+        dy, dh = upstream(d, "bf16", 7)
+        run = lambda: ssd.channel_scan_bwd(**d, dy=dy, dfinal_state=dh, softplus=True, return_dinitial_state=True)
+        want = run()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            other = run()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = run()
+        for _ in range(3):
+            for t in held.values():
+                t.fill_(7)
+            graph.replay()
+            again = run()
+            torch.cuda.synchronize()
+            for got in (other, held, again):
+                for k in want:
+                    assert torch.equal(got[k], want[k]), (L, k)

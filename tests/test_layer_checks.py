@@ -248,3 +248,52 @@ def test_scan_abi_pointers(lib):
     assert step(st=None) == step(y=None) == _lib.SSD_ERR_NULL
     assert step(st=P[0]) == step(y=P[8]) == _lib.SSD_ERR_ALIAS
     assert step(d=chan_desc(batch=0, seqlen=1)) == _lib.SSD_OK
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(dy=None), "dy is required"),
+    (dict(dy=torch.zeros(Bz, L, D)), "dy has dtype"),
+    (dict(dy=torch.zeros(Bz, D, L, dtype=BF).transpose(1, 2)), "dy must be contiguous"),
+    (dict(dfinal_state=torch.zeros(Bz, D, N, dtype=BF)), "dfinal_state has dtype"),
+    (dict(initial_state=torch.zeros(Bz, D + 1, N)), "initial_state has shape"),
+    (dict(workspace=torch.zeros(16, dtype=torch.uint8)), "workspace holds"),
+    (dict(seqlens=torch.zeros(Bz, dtype=torch.int64)), "seqlens has dtype"),
+    (dict(), "on the GPU"),
+])
+def test_scan_bwd(kw, match):
+    d = scan_args(dy=torch.zeros(Bz, L, D, dtype=BF))
+    d.update(kw)
+    with pytest.raises(ValueError, match=match):
+        ssd.channel_scan_bwd(**d)
+
+
+def test_scan_bwd_abi(lib):
+    n, odd = ctypes.c_size_t(), ctypes.c_void_p((1 << 20) + 1)
+    names = ("du", "ddelta", "dgate", "dB", "dC", "dA", "dskip", "ddelta_bias", "dinitial_state")
+    ws = ctypes.c_void_p(1 << 46)
+
+    def bwd(d=chan_desc(), wsz=None, ws=ws, dy=P[5], skip=None, gate=None, bias=None, dh=None, u=P[0], **kw):
+        assert lib.ssd_channel_scan_bwd_workspace_bytes(d, n) == 0
+        g = dict(zip(names, (P[6], P[7], None, P[8], P[9], P[10], None, None, None)))
+        g.update(kw)
+        grads = _lib.ChannelGrads(*[v.value if v is not None else None for v in g.values()])
+        return lib.ssd_channel_scan_bwd(d, u, *P[1:5], skip, gate, bias, None, None, dy, dh, grads, ws,
+                                        n.value if wsz is None else wsz, None)
+
+    for k in ("du", "ddelta", "dB", "dC", "dA"):
+        assert bwd(**{k: None}) == _lib.SSD_ERR_NULL
+        assert bwd(**{k: odd}) == _lib.SSD_ERR_ALIGN
+        assert bwd(**{k: P[0]}) == _lib.SSD_ERR_ALIAS
+    assert bwd(dy=None) == _lib.SSD_ERR_NULL
+    # gradients of optional inputs: given exactly with them
+    for k, i in (("dgate", "gate"), ("dskip", "skip"), ("ddelta_bias", "bias")):
+        assert bwd(**{k: P[12]}) == bwd(**{i: P[12]}) == _lib.SSD_ERR_NULL
+    assert bwd(dy=odd) == bwd(dh=odd) == bwd(dinitial_state=odd) == _lib.SSD_ERR_ALIGN
+    assert bwd(du=P[5]) == bwd(du=P[7]) == bwd(ws=P[6]) == bwd(dinitial_state=P[10]) == _lib.SSD_ERR_ALIAS
+    assert bwd(wsz=8) == bwd(ws=None) == _lib.SSD_ERR_WORKSPACE
+    assert bwd(ws=ctypes.c_void_p((1 << 46) + 8)) == _lib.SSD_ERR_ALIGN
+    assert lib.ssd_channel_scan_bwd(chan_desc(), *P[:5], None, None, None, None, None, P[5], None, None, ws, 1 << 40,
+                                    None) == _lib.SSD_ERR_NULL
+    # more rows than a launch of the sums of dB and dC reaches
+    big = chan_desc(batch=1, seqlen=1 << 30, u_bstride=0)
+    assert lib.ssd_channel_scan_bwd_workspace_bytes(big, n) == _lib.SSD_ERR_UNSUPPORTED
