@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
     constexpr int NE = (NBC + 255) / 256;           // of these, passed on by a thread
     constexpr bool EXACT = ES == 4;
     __shared__ float2 s_dt[2][TB][CW];
-    __shared__ __align__(16) float s_bc[2][NBC];    // [step][B, C][state]
+    __shared__ __align__(16) float s_bc[2][NBC];    // [B, C][step][state]
     __shared__ float s_y[FULL ? 2 : 1][FULL ? TB : 1][NPART][CW];
     const int tid = threadIdx.x, c = tid & (CW - 1), part = tid / CW, n0 = part * NR;
     const int g = blockIdx.x / a.tpg, cg = (blockIdx.x - g * a.tpg) * CW + c;
@@ -80,6 +80,8 @@ __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
     // This thread's pairs of a batch are the steps part + k NPART of channel c, its
     // elements of B and C those at e 256 + tid; offsets in the batch's rows.  Steps
     // past `last` repeat that one.
+    const int wave64 = __builtin_amdgcn_readfirstlane(tid >> 6) * 64;
+    auto in_C = [&](int e) { return FULL && e * 256 + wave64 >= TB * NP; };   // else in B
     uint32_t ou[TP], od[TP], oz[TP], obc[NE];
     auto offsets = [&](int last) {
 #pragma unroll
@@ -92,9 +94,9 @@ __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
         }
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
-            const int i = e * 256 + tid, s = i / (FULL ? 2 * NP : NP), n = i & (NP - 1);
+            const int i = e * 256 + tid, s = i / NP & (TB - 1), n = i & (NP - 1);
             const uint32_t r = s < last ? s : last;
-            obc[e] = r * (FULL && (i & NP) ? a.Cr : a.Br) + (uint32_t)(n < a.N ? n : a.N - 1) * ES;
+            obc[e] = r * (in_C(e) ? a.Cr : a.Br) + (uint32_t)(n < a.N ? n : a.N - 1) * ES;
         }
     };
     // two batches in flight
@@ -110,7 +112,7 @@ __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
         }
 #pragma unroll
         for (int e = 0; e < NE; ++e)
-            rbc[P][e] = FULL && ((e * 256 + tid) & NP) ? load_at<T>(Cp, obc[e]) : load_at<T>(Bp, obc[e]);
+            rbc[P][e] = load_at<T>(in_C(e) ? Cp : Bp, obc[e]);
         up += TB * (uint64_t)a.ur;
         dp += TB * (uint64_t)a.dr;
         zp += TB * (uint64_t)a.zr;
@@ -146,13 +148,13 @@ __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
 #pragma unroll
         for (int k = 0; k < TB; ++k) {
             const float2 d = s_dt[P][k][c];
-            const float* bc = s_bc[P] + k * (NBC / TB) + n0;
+            const float* bc = s_bc[P] + k * NP + n0;
             float y = 0.f;
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
                 const float e = fast_exp2(d.x * A2[i]);
                 h[i] = fmaf(e, h[i], d.y * bc[i]);
-                if (FULL) y = i == 0 ? h[i] * bc[NP + i] : fmaf(h[i], bc[NP + i], y);
+                if (FULL) y = i == 0 ? h[i] * bc[TB * NP + i] : fmaf(h[i], bc[TB * NP + i], y);
             }
             if (FULL) s_y[P][k][part][c] = y;
         }

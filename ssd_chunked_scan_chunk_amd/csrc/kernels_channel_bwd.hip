@@ -34,6 +34,7 @@ namespace {
 template <int V> using Int = std::integral_constant<int, V>;
 
 constexpr int TB = 8;   // steps of a batch
+constexpr int RB = 2;   // of these, taken in reverse together
 
 struct BwdArgs {
     ChanArgs f;
@@ -106,6 +107,27 @@ template <int NV, int W> struct LaneSum {
     __device__ static void run(float (&v)[NV], int l) { level<W / 2, NV>(v, l); }
 };
 
+// a lane's NR consecutive floats
+template <int NR> __device__ __forceinline__ void load_states(RowIn row, uint32_t off, float (&v)[NR]) {
+    typedef float vec __attribute__((ext_vector_type(NR < 4 ? NR : 4)));
+#pragma unroll
+    for (int i = 0; i < NR; i += 4) {
+        const vec q = load_at<vec>(row, off + i * 4);
+#pragma unroll
+        for (int k = 0; k < 4 && k < NR; ++k) v[i + k] = q[k];
+    }
+}
+template <int NR> __device__ __forceinline__ void store_states(RowOut row, uint32_t off, const float (&v)[NR]) {
+    typedef float vec __attribute__((ext_vector_type(NR < 4 ? NR : 4)));
+#pragma unroll
+    for (int i = 0; i < NR; i += 4) {
+        vec q;
+#pragma unroll
+        for (int k = 0; k < 4 && k < NR; ++k) q[k] = v[i + k];
+        *reinterpret_cast<__attribute__((address_space(1))) vec*>(row + off + i * 4) = q;
+    }
+}
+
 // The states at the start of every batch.  SEGS: from zero, with the segment's
 // adjoint, state and sum of dt; otherwise from the initial state.
 template <typename T, int NR, int CW, bool SEGS>
@@ -118,8 +140,9 @@ __global__ __launch_bounds__(256) void k_chan_states(BwdArgs a)
     const ChanArgs& f = a.f;
     __shared__ float2 s_dt[2][TB][CW];
     __shared__ float s_d[SEGS ? 2 : 1][SEGS ? TB : 1][CW];
-    __shared__ __align__(16) float s_bc[2][NBC];
+    __shared__ __align__(16) float s_bc[2][NBC];   // [B, C][step][state]
     const int tid = threadIdx.x, c = tid & (CW - 1), part = tid / CW, n0 = part * NR;
+    const int wave64 = __builtin_amdgcn_readfirstlane(tid >> 6) * 64;
     const int tile = blockIdx.x, g = tile / f.tpg, cg = (tile - g * f.tpg) * CW + c;
     const int cl = cg < f.per ? cg : f.per - 1;   // threads past the group repeat its last channel
     const uint32_t col = (uint32_t)cl * ES;
@@ -146,6 +169,7 @@ __global__ __launch_bounds__(256) void k_chan_states(BwdArgs a)
     const uint32_t yr = (uint32_t)f.D * ES;
     RowIn gp = row_in(a.dy, ((b * f.L + ts) * f.D + gch) * ES);
 
+    auto in_C = [&](int e) { return e * 256 + wave64 >= TB * NP; };   // else in B
     uint32_t ou[TP], od[TP], oz[TP], og[TP], obc[NE];
     auto offsets = [&](int last) {
 #pragma unroll
@@ -159,9 +183,9 @@ __global__ __launch_bounds__(256) void k_chan_states(BwdArgs a)
         }
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
-            const int i = e * 256 + tid, s = i / (SEGS ? 2 * NP : NP), n = i & (NP - 1);
+            const int i = e * 256 + tid, s = i / NP & (TB - 1), n = i & (NP - 1);
             const uint32_t r = s < last ? s : last;
-            obc[e] = r * (SEGS && (i & NP) ? f.Cr : f.Br) + (uint32_t)(n < f.N ? n : f.N - 1) * ES;
+            obc[e] = r * (SEGS && in_C(e) ? f.Cr : f.Br) + (uint32_t)(n < f.N ? n : f.N - 1) * ES;
         }
     };
     T ru[2][TP], rd[2][TP], rz[2][TP], rg[2][TP], rbc[2][NE];
@@ -179,7 +203,7 @@ __global__ __launch_bounds__(256) void k_chan_states(BwdArgs a)
         }
 #pragma unroll
         for (int e = 0; e < NE; ++e)
-            rbc[Q][e] = SEGS && ((e * 256 + tid) & NP) ? load_at<T>(Cp, obc[e]) : load_at<T>(Bp, obc[e]);
+            rbc[Q][e] = load_at<T>(SEGS && in_C(e) ? Cp : Bp, obc[e]);
         up += TB * (uint64_t)f.ur;
         dp += TB * (uint64_t)f.dr;
         zp += TB * (uint64_t)f.zr;
@@ -213,15 +237,14 @@ __global__ __launch_bounds__(256) void k_chan_states(BwdArgs a)
     auto batch = [&](int t, auto slot) {
         constexpr int Q = decltype(slot)::value;
         if (t + 2 * TB < te) fetch(slot, te - 1 - t - 2 * TB);
-#pragma unroll
-        for (int i = 0; i < NR; ++i) a.ck[(at * 256 + tid) * NR + i] = h[i];
+        store_states<NR>(row_out(a.ck, at * 256 * NR * 4), tid * NR * 4, h);
         if (SEGS && part == 0) a.cdt[at * CW + c] = sum;
         at += a.tiles;
         lds_barrier();
 #pragma unroll
         for (int k = 0; k < TB; ++k) {
             const float2 d = s_dt[Q][k][c];
-            const float* bc = s_bc[Q] + k * (NBC / TB) + n0;
+            const float* bc = s_bc[Q] + k * NP + n0;
             if (SEGS) sum += d.x;
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
@@ -229,7 +252,7 @@ __global__ __launch_bounds__(256) void k_chan_states(BwdArgs a)
                 h[i] = fmaf(e, h[i], d.y * bc[i]);
                 if constexpr (SEGS) {
                     P[i] *= e;
-                    G[i] = fmaf(P[i], s_d[Q][k][c] * bc[NP + i], G[i]);
+                    G[i] = fmaf(P[i], s_d[Q][k][c] * bc[TB * NP + i], G[i]);
                 }
             }
         }
@@ -298,7 +321,7 @@ __global__ __launch_bounds__(256) void k_chan_link(BwdArgs a, int64_t items)
 }
 
 template <typename T, int NR, int CW, bool SEGS>
-__global__ __launch_bounds__(256) void k_chan_bwd(BwdArgs a)
+__global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
 {
     constexpr int ES = sizeof(T), NPART = 256 / CW, NP = NPART * NR;
     constexpr int TP = TB * CW / 256, NBC = TB * NP * 2, NE = (NBC + 255) / 256;
@@ -306,9 +329,10 @@ __global__ __launch_bounds__(256) void k_chan_bwd(BwdArgs a)
     const ChanArgs& f = a.f;
     __shared__ float2 s_dt[TB][CW];
     __shared__ float s_d[TB][CW];
-    __shared__ __align__(16) float s_bc[NBC];          // [step][B, C][state]
+    __shared__ __align__(16) float s_bc[NBC];          // [B, C][step][state]
     __shared__ float s_part[3][TB][NPART][CW];         // parts of h C, g B and m A
     const int tid = threadIdx.x, c = tid & (CW - 1), part = tid / CW, n0 = part * NR, lane = tid & 63;
+    const int wave64 = __builtin_amdgcn_readfirstlane(tid >> 6) * 64;
     const int tile = blockIdx.x, g = tile / f.tpg, cg = (tile - g * f.tpg) * CW + c;
     const bool live = cg < f.per;
     // threads past the group repeat its last channel, store nothing and add nothing
@@ -342,59 +366,51 @@ __global__ __launch_bounds__(256) void k_chan_bwd(BwdArgs a)
     const RowIn gp = row_in(a.dy, dense);
     const RowOut dup = row_out(a.du, dense), ddp = row_out(a.ddelta, dense), dzp = row_out(a.dgate, dense);
 
-    // the share of batch j of this thread, as in the forward; offsets of whole batches
-    uint32_t ou[TP], od[TP], oz[TP], og[TP], obc[NE];
-    auto offsets = [&](int last) {
+    // The share of batch j of this thread, as in the forward: the steps part + k
+    // NPART of channel c, elements e 256 + tid of B and C.  Steps past `last` (in the
+    // last batch of a segment only) repeat that one.
+    T ru[TP], rd[TP], rz[TP], rg[TP], rbc[NE];
+    float rck[NR], rcdt = 0.f;
+    auto fetch = [&](int j, int last) {
+        const uint64_t t = (uint64_t)j * TB;
+        const RowIn ut = up + t * f.ur, dt = dp + t * f.dr, zt = zp + t * f.zr, gt = gp + t * yr;
 #pragma unroll
         for (int k = 0; k < TP; ++k) {
             const int s = part + k * NPART;
             const uint32_t r = s < last ? s : last;
-            ou[k] = r * f.ur + col;
-            od[k] = r * f.dr + col;
-            oz[k] = r * f.zr + col;
-            og[k] = r * yr + col;
+            ru[k] = load_at<T>(ut, r * f.ur + col);
+            rd[k] = load_at<T>(dt, r * f.dr + col);
+            rz[k] = load_at<T>(zt, r * f.zr + col);
+            rg[k] = load_at<T>(gt, r * yr + col);
         }
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
-            const int i = e * 256 + tid, s = i / (2 * NP), n = i & (NP - 1);
-            const uint32_t r = s < last ? s : last;
-            obc[e] = r * (i & NP ? f.Cr : f.Br) + (uint32_t)(n < f.N ? n : f.N - 1) * ES;
+            const int i = e * 256 + tid, s = i / NP & (TB - 1), n = i & (NP - 1);
+            const bool in_C = e * 256 + wave64 >= TB * NP;
+            const uint32_t r = s < last ? s : last, rs = in_C ? f.Cr : f.Br;
+            rbc[e] = load_at<T>((in_C ? Cp : Bp) + t * rs, r * rs + (uint32_t)(n < f.N ? n : f.N - 1) * ES);
         }
-    };
-    T ru[TP], rd[TP], rz[TP], rg[TP], rbc[NE];
-    float rck[NR], rcdt = 0.f;
-    auto fetch = [&](int j) {
-        const uint64_t t = (uint64_t)j * TB;
-#pragma unroll
-        for (int k = 0; k < TP; ++k) {
-            ru[k] = load_at<T>(up + t * f.ur, ou[k]);
-            rd[k] = load_at<T>(dp + t * f.dr, od[k]);
-            rz[k] = load_at<T>(zp + t * f.zr, oz[k]);
-            rg[k] = load_at<T>(gp + t * yr, og[k]);
-        }
-#pragma unroll
-        for (int e = 0; e < NE; ++e)
-            rbc[e] = (e * 256 + tid) & NP ? load_at<T>(Cp + t * f.Cr, obc[e]) : load_at<T>(Bp + t * f.Br, obc[e]);
         const int64_t at = ((b * f.nseg + seg) * a.nb + j) * a.tiles + tile;
-#pragma unroll
-        for (int i = 0; i < NR; ++i) rck[i] = a.ck[(at * 256 + tid) * NR + i];
-        if (SEGS) rcdt = a.cdt[at * CW + c];
+        load_states<NR>(row_in(a.ck, at * 256 * NR * 4), tid * NR * 4, rck);
+        if (SEGS) rcdt = load_at<float>(row_in(a.cdt, at * CW * 4), (uint32_t)c * 4);
     };
-    float u[TP], x[TP], z[TP], dyv[TP], dtv[TP], d[TP], h[NR], sskip = 0.f, sbias = 0.f;
+    // of a pair: u, dt, d, softplus' and dy silu'(gate)
+    float u[TP], dtv[TP], d[TP], sx[TP], dz[TP], h[NR], sskip = 0.f, sbias = 0.f;
     auto prepare = [&](int j) {
 #pragma unroll
         for (int k = 0; k < TP; ++k) {
             const int s = part + k * NPART;
-            const bool on = j * TB + s < te;   // a step past the end changes nothing
-            x[k] = as_f32(rd[k]) + bias;
-            const float sp = softplus_of<EXACT>(x[k]);
-            dtv[k] = on ? (f.softplus ? sp : x[k]) : 0.f;
+            const bool on = live && j * TB + s < te;   // neither a step past the end nor a channel past
+            const float x = as_f32(rd[k]) + bias;      // the group may add to anything
+            const float e = exp_neg_abs<EXACT>(x), r = __builtin_amdgcn_rcpf(1.f + e);
+            const float sp = fmaxf(x, 0.f) + log1p_unit(e);
+            dtv[k] = on ? (f.softplus ? sp : x) : 0.f;
+            sx[k] = f.softplus ? (x >= 0.f ? r : e * r) : 1.f;
             u[k] = as_f32(ru[k]);
-            z[k] = as_f32(rz[k]);
-            dyv[k] = on ? as_f32(rg[k]) : 0.f;
-            const float sz = z[k] * sigmoid_of(z[k]);
-            d[k] = on ? dyv[k] * (gated ? sz : 1.f) : 0.f;
-            s_dt[s][c] = make_float2(dtv[k], dtv[k] * u[k]);
+            const float z = as_f32(rz[k]), sg = sigmoid_of(z), dy = as_f32(rg[k]);
+            dz[k] = dy * (sg * fmaf(z, 1.f - sg, 1.f));
+            d[k] = on ? dy * (gated ? z * sg : 1.f) : 0.f;
+            s_dt[s][c] = make_float2(dtv[k], on ? dtv[k] * u[k] : 0.f);
             s_d[s][c] = d[k];
         }
 #pragma unroll
@@ -409,15 +425,18 @@ __global__ __launch_bounds__(256) void k_chan_bwd(BwdArgs a)
     };
 
     if (nb > 0) {
-        offsets(te - 1 - (nb - 1) * TB < TB - 1 ? te - 1 - (nb - 1) * TB : TB - 1);
-        fetch(nb - 1);
-        if (nb > 1) offsets(TB - 1);
+        fetch(nb - 1, te - 1 - (nb - 1) * TB);
         prepare(nb - 1);
     }
-    using Sum = LaneSum<TB * 2 * NR, CW>;
+    using Sum = LaneSum<RB * 2 * NR, CW>;
+    // the values this lane is left with, vi .. : state (part's n0 +) i of B or C at step k
     const int vi = Sum::index(lane);
+    auto place = [&](int e) {
+        const int m = vi + e, k = m / (2 * NR), which = m / NR & 1, i = m % NR;
+        return make_int2(k, ((k * a.tiles * 2 + which) * NP + n0 + i) * 4);
+    };
     for (int j = nb - 1; j >= 0; --j) {
-        if (j > 0) fetch(j - 1);
+        if (j > 0) fetch(j - 1, TB - 1);
         lds_barrier();
         // forward: states and decays of the batch
         float H[TB][NR], E[TB][NR], hfirst[NR];
@@ -426,47 +445,55 @@ __global__ __launch_bounds__(256) void k_chan_bwd(BwdArgs a)
 #pragma unroll
         for (int k = 0; k < TB; ++k) {
             const float2 dt = s_dt[k][c];
-            const float* bc = s_bc + k * 2 * NP + n0;
+            const float* bc = s_bc + k * NP + n0;
             float y = 0.f;
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
                 E[k][i] = fast_exp2(dt.x * A2[i]);
                 h[i] = fmaf(E[k][i], h[i], dt.y * bc[i]);
                 H[k][i] = h[i];
-                y = i == 0 ? h[i] * bc[NP + i] : fmaf(h[i], bc[NP + i], y);
+                y = i == 0 ? h[i] * bc[TB * NP + i] : fmaf(h[i], bc[TB * NP + i], y);
             }
             s_part[0][k][part][c] = y;
         }
-        // reverse: E[k] and H[k] give way to the terms of dB and dC
-        float v[TB * 2 * NR];
+        // Reverse, RB steps at a time, whose terms of dB and dC are summed over the
+        // channels before the next.  The batch's values are read from LDS again (the
+        // empty asm keeps the compiler from holding them): kept, they would cost a
+        // third of the registers and with them a wavefront per SIMD (876 against
+        // 532 us for 4 x 2048 x 5120 x 16 in four segments).
+        const RowOut pbc = row_out(a.pbc, (((b * f.L + ts + (int64_t)j * TB) * a.tiles + tile) * 2 * NP) * 4);
 #pragma unroll
-        for (int k = TB - 1; k >= 0; --k) {
-            const float2 dt = s_dt[k][c];
-            const float dk = s_d[k][c];
-            const float* bc = s_bc + k * 2 * NP + n0;
-            float fed = 0.f, ma = 0.f;
+        for (int k0 = TB - RB; k0 >= 0; k0 -= RB) {
+            asm volatile("" ::: "memory");
+            float v[RB * 2 * NR];
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                const float gr = fmaf(dk, bc[NP + i], carry[i]);
-                fed = i == 0 ? gr * bc[i] : fmaf(gr, bc[i], fed);
-                v[(k * 2) * NR + i] = live ? gr * dt.y : 0.f;
-                v[(k * 2 + 1) * NR + i] = live ? H[k][i] * dk : 0.f;
-                carry[i] = gr * E[k][i];
-                const float m = carry[i] * (k > 0 ? H[k > 0 ? k - 1 : 0][i] : hfirst[i]);
-                dA[i] = fmaf(m, dt.x, dA[i]);
-                ma = i == 0 ? m * A2[i] : fmaf(m, A2[i], ma);
+            for (int m = RB - 1; m >= 0; --m) {
+                const int k = k0 + m;
+                const float2 dt = s_dt[k][c];
+                const float dk = s_d[k][c];
+                const float* bc = s_bc + k * NP + n0;
+                float fed = 0.f, ma = 0.f;
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    const float gr = fmaf(dk, bc[TB * NP + i], carry[i]);
+                    fed = i == 0 ? gr * bc[i] : fmaf(gr, bc[i], fed);
+                    v[(m * 2) * NR + i] = gr * dt.y;
+                    v[(m * 2 + 1) * NR + i] = H[k][i] * dk;
+                    carry[i] = gr * E[k][i];
+                    const float mh = carry[i] * (k > 0 ? H[k > 0 ? k - 1 : 0][i] : hfirst[i]);
+                    dA[i] = fmaf(mh, dt.x, dA[i]);
+                    ma = i == 0 ? mh * A2[i] : fmaf(mh, A2[i], ma);
+                }
+                s_part[1][k][part][c] = fed;
+                s_part[2][k][part][c] = ma;
             }
-            s_part[1][k][part][c] = fed;
-            s_part[2][k][part][c] = ma;
-        }
-        Sum::run(v, lane);
+            Sum::run(v, lane);
 #pragma unroll
-        for (int e = 0; e < Sum::kLeft; ++e) {
-            // value vi + e: state (part's n0 +) i of B or C at step k
-            const int m = vi + e, k = m / (2 * NR), which = m / NR & 1, i = m % NR;
-            const int64_t t = ts + (int64_t)j * TB + k;
-            // lanes that share a value store it more than once, the same bits
-            if (j * TB + k < te) a.pbc[(((b * f.L + t) * a.tiles + tile) * 2 + which) * NP + n0 + i] = v[e];
+            for (int e = 0; e < Sum::kLeft; ++e) {
+                const int2 to = place(e);
+                // lanes that share a value store it more than once, the same bits
+                if (j * TB + k0 + to.x < te) store_at(pbc, (uint32_t)(k0 * a.tiles * 2 * NP) * 4 + to.y, v[e], 0.f);
+            }
         }
         lds_barrier();
         // this thread's pairs of the batch
@@ -481,22 +508,14 @@ __global__ __launch_bounds__(256) void k_chan_bwd(BwdArgs a)
                 ma += s_part[2][s][q][c];
             }
             // A2 = A log2(e)
-            const float ddt = fmaf(fed, u[k], ma * 0.69314718f);
-            const float e = exp_neg_abs<EXACT>(x[k]), r = __builtin_amdgcn_rcpf(1.f + e);
-            const float dd = f.softplus ? ddt * (x[k] >= 0.f ? r : e * r) : ddt;
+            const float dd = fmaf(fed, u[k], ma * 0.69314718f) * sx[k];
             const uint32_t at = s * yr + col;
-            const bool on = live && j * TB + s < te;
-            const RowOut row_u = dup + (uint64_t)j * TB * yr, row_d = ddp + (uint64_t)j * TB * yr;
-            if (on) {
+            if (live && j * TB + s < te) {
                 sskip = fmaf(d[k], u[k], sskip);
                 sbias += dd;
-                store_at(row_u, at, fmaf(fed, dtv[k], skip * d[k]), T());
-                store_at(row_d, at, dd, T());
-                if (gated) {
-                    const float sg = sigmoid_of(z[k]);
-                    store_at(dzp + (uint64_t)j * TB * yr, at,
-                             dyv[k] * fmaf(skip, u[k], y) * (sg * fmaf(z[k], 1.f - sg, 1.f)), T());
-                }
+                store_at(dup + (uint64_t)j * TB * yr, at, fmaf(fed, dtv[k], skip * d[k]), T());
+                store_at(ddp + (uint64_t)j * TB * yr, at, dd, T());
+                if (gated) store_at(dzp + (uint64_t)j * TB * yr, at, dz[k] * fmaf(skip, u[k], y), T());
             }
         }
         if (j > 0) prepare(j - 1);
