@@ -10,6 +10,7 @@ upstream gradients are contiguous.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -18,23 +19,34 @@ from . import _L, _check, _check_bytes, _dtype_code, _lib
 _P = ctypes.c_void_p * 3
 
 
+def _same(name, t, shape, dtype, device):
+    """_check, with the usual outcome decided first: these calls take tens of
+    microseconds for a token, so their checks have to be quick."""
+    if t is None or (t.__class__ is torch.Tensor and t.shape == shape and t.dtype is dtype and t.device == device
+                     and t.is_contiguous()):
+        return
+    _check(name, t, shape, dtype, device)
+
+
 def _rows(name, t, shape, dense, dtype, device):
     """Check a tensor of ``shape`` whose last ``dense`` dimensions are dense and
     return the strides of the leading ones."""
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s is required" % name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    strides, want = t.stride(), 1
-    for k in range(1, dense + 1):
-        if strides[-k] != want and t.shape[-k] > 1:
-            raise ValueError("the rows of %s must be contiguous" % name)
-        want *= t.shape[-k]
-    return strides[:t.dim() - dense]
+    strides = t.stride()
+    if strides[-1] != 1 or dense > 1:   # a dimension of size 1 may have any stride
+        want = 1
+        for k in range(1, dense + 1):
+            if strides[-k] != want and shape[-k] > 1:
+                raise ValueError("the rows of %s must be contiguous" % name)
+            want *= shape[-k]
+    return strides
 
 
 def _need(name, t):
@@ -47,16 +59,25 @@ def _at(t):
 
 
 def _seqlens(seqlens, Bz, device):
-    if seqlens is not None and not isinstance(seqlens, torch.Tensor):
-        raise TypeError("seqlens must be a torch.Tensor on the GPU")
-    _check("seqlens", seqlens, (Bz,), torch.int32, device)
+    if seqlens is not None:
+        if not isinstance(seqlens, torch.Tensor):
+            raise TypeError("seqlens must be a torch.Tensor on the GPU")
+        _same("seqlens", seqlens, (Bz,), torch.int32, device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes(query, kind, *sizes):
+    """The workspace an entry point asks for, by the sizes that decide it."""
+    n = ctypes.c_size_t()
+    _lib.check(getattr(_L(), query)(kind(*sizes), n))
+    return n.value
 
 
 def _workspace(workspace, nbytes, device):
+    if workspace is None:
+        return (torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes) if nbytes > 0 else (None, 0)
     _check_bytes("workspace", workspace, nbytes, device)
-    if workspace is None and nbytes > 0:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _enqueue(device, fn, *args):
@@ -64,12 +85,14 @@ def _enqueue(device, fn, *args):
     device being the current one."""
     if device.type != "cuda":
         raise ValueError("tensors must live on the GPU")
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        _lib.check(fn(*args, stream))
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if device.index == torch._C._cuda_getDevice():
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            _lib.check(fn(*args, stream))
+            status = fn(*args, stream)
+    if status:
+        _lib.check(status)
 
 
 # ---- short causal convolution ------------------------------------------------------
@@ -82,22 +105,26 @@ def _conv_check(x, weight, bias, silu, pieces, lead):
     strides = _rows("x", x, x.shape, 1, x.dtype, x.device)
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a 2-D tensor [channels, width]")
-    _check("weight", weight, (C, weight.shape[1]), torch.float32, x.device)
-    _check("bias", bias, (C,), torch.float32, x.device)
-    given = (C,) if pieces is None else tuple(int(w) for w in pieces)
-    if not 1 <= len(given) <= 3 or min(given) < 1 or sum(given) != C:
-        raise ValueError("pieces must be one to three widths that add up to the %d channels, got %s" % (C, given))
-    d = _lib.ConvDesc(x.shape[0], x.shape[1] if lead == 2 else 1, C, weight.shape[1], strides[0],
-                      strides[1] if lead == 2 else 0, given + (0,) * (3 - len(given)), len(given), code,
-                      int(bool(silu)), 0)
-    return d, given
+    W = weight.shape[1]
+    _same("weight", weight, (C, W), torch.float32, x.device)
+    _same("bias", bias, (C,), torch.float32, x.device)
+    if pieces is None:
+        given, three = (C,), (C, 0, 0)
+    else:
+        given = tuple(int(w) for w in pieces)
+        if not 1 <= len(given) <= 3 or min(given) < 1 or sum(given) != C:
+            raise ValueError("pieces must be one to three widths that add up to the %d channels, got %s" % (C, given))
+        three = given + (0,) * (3 - len(given))
+    L, xr = (x.shape[1], strides[1]) if lead == 2 else (1, 0)
+    return _lib.ConvDesc(x.shape[0], L, C, W, strides[0], xr, three, len(given), code, 1 if silu else 0, 0), given
 
 
 def _conv_outputs(x, given, pieces, y):
     """The y pieces to write, as a tuple, and what the caller gets back."""
     lead = tuple(x.shape[:-1])
     if y is None:
-        ys = tuple(torch.empty(lead + (w,), dtype=x.dtype, device=x.device) for w in given)
+        ys = [torch.empty(lead + (w,), dtype=x.dtype, device=x.device) for w in given]
+        ys = tuple(ys)
         return ys, ys[0] if pieces is None else ys
     ys = (y,) if pieces is None else tuple(y)
     _conv_given("y", ys, lead, given, x)
@@ -110,7 +137,7 @@ def _conv_given(name, ts, lead, given, x):
     for i, (t, w) in enumerate(zip(ts, given)):
         label = name if len(given) == 1 else "%s[%d]" % (name, i)
         _need(label, t)
-        _check(label, t, lead + (w,), x.dtype, x.device)
+        _same(label, t, lead + (w,), x.dtype, x.device)
 
 
 def short_conv_fwd(x, weight, bias=None, initial_window=None, seqlens=None, silu=True, pieces=None,
@@ -126,8 +153,8 @@ def short_conv_fwd(x, weight, bias=None, initial_window=None, seqlens=None, silu
     the window [Bz,W-1,C] continues the sequence here or in short_conv_step."""
     d, given = _conv_check(x, weight, bias, silu, pieces, 2)
     Bz, C, W = x.shape[0], x.shape[2], weight.shape[1]
-    _check("initial_window", initial_window, (Bz, W - 1, C), x.dtype, x.device)
-    _check("final_window", final_window, (Bz, W - 1, C), x.dtype, x.device)
+    _same("initial_window", initial_window, (Bz, W - 1, C), x.dtype, x.device)
+    _same("final_window", final_window, (Bz, W - 1, C), x.dtype, x.device)
     _seqlens(seqlens, Bz, x.device)
     ys, back = _conv_outputs(x, given, pieces, y)
     if final_window is None and return_final_window:
@@ -138,10 +165,13 @@ def short_conv_fwd(x, weight, bias=None, initial_window=None, seqlens=None, silu
 
 
 def short_conv_bwd_workspace_bytes(x, weight) -> int:
-    d, _ = _conv_check(x, weight, None, True, None, 2)
-    n = ctypes.c_size_t()
-    _lib.check(_L().ssd_short_conv_bwd_workspace_bytes(d, n))
-    return n.value
+    return _conv_bwd_bytes(_conv_check(x, weight, None, True, None, 2)[0])
+
+
+def _conv_bwd_bytes(d):
+    C = d.channels
+    return _bytes("ssd_short_conv_bwd_workspace_bytes", _lib.ConvDesc, d.batch, d.seqlen, C, d.width, 0, 0,
+                  (C, 0, 0), 1, d.dtype, 1, 0)
 
 
 def short_conv_bwd(x, weight, dy, bias=None, initial_window=None, dfinal_window=None, seqlens=None, silu=True,
@@ -161,12 +191,10 @@ def short_conv_bwd(x, weight, dy, bias=None, initial_window=None, dfinal_window=
     Bz, L, C = x.shape
     W = weight.shape[1]
     _conv_given("dy", dys, (Bz, L), given, x)
-    _check("initial_window", initial_window, (Bz, W - 1, C), x.dtype, x.device)
-    _check("dfinal_window", dfinal_window, (Bz, W - 1, C), x.dtype, x.device)
+    _same("initial_window", initial_window, (Bz, W - 1, C), x.dtype, x.device)
+    _same("dfinal_window", dfinal_window, (Bz, W - 1, C), x.dtype, x.device)
     _seqlens(seqlens, Bz, x.device)
-    n = ctypes.c_size_t()
-    _lib.check(_L().ssd_short_conv_bwd_workspace_bytes(d, n))
-    workspace, wsz = _workspace(workspace, n.value, x.device)
+    workspace, wsz = _workspace(workspace, _conv_bwd_bytes(d), x.device)
     dx = torch.empty((Bz, L, C), dtype=x.dtype, device=x.device)
     dweight = torch.empty_like(weight)
     dbias = torch.empty_like(bias) if bias is not None else None
@@ -181,7 +209,7 @@ def short_conv_step(window, x, weight, bias=None, silu=True, pieces=None, y=None
     updated in place.  Returns y [Bz,C], or its pieces as a tuple."""
     d, given = _conv_check(x, weight, bias, silu, pieces, 1)
     _need("window", window)
-    _check("window", window, (x.shape[0], weight.shape[1] - 1, x.shape[1]), x.dtype, x.device)
+    _same("window", window, (x.shape[0], weight.shape[1] - 1, x.shape[1]), x.dtype, x.device)
     ys, back = _conv_outputs(x, given, pieces, y)
     _enqueue(x.device, _L().ssd_short_conv_step, d, _at(window), _at(x), _at(weight), _at(bias), _P(*map(_at, ys)))
     return back
@@ -196,7 +224,7 @@ def _chan_check(u, delta, A, B, C, skip, gate, delta_bias, softplus, lead):
     code, dt, dev, D = _dtype_code(u), u.dtype, u.device, u.shape[-1]
     if not isinstance(A, torch.Tensor) or A.dim() != 2:
         raise ValueError("A must be a 2-D tensor [channels, dstate]")
-    _check("A", A, (D, A.shape[1]), torch.float32, dev)
+    _same("A", A, (D, A.shape[1]), torch.float32, dev)
     if not isinstance(B, torch.Tensor) or B.dim() != lead + 2:
         raise ValueError("B must be a %d-D tensor [batch, %sngroups, dstate]"
                          % (lead + 2, "seqlen, " if lead == 2 else ""))
@@ -206,17 +234,21 @@ def _chan_check(u, delta, A, B, C, skip, gate, delta_bias, softplus, lead):
     sz = _rows("gate", gate, u.shape, 1, dt, dev) if gate is not None else (0, 0)
     sB = _rows("B", B, rows + (G, N), 2, dt, dev)
     sC = _rows("C", C, rows + (G, N), 2, dt, dev)
-    _check("skip", skip, (D,), torch.float32, dev)
-    _check("delta_bias", delta_bias, (D,), torch.float32, dev)
-    strides = [s[i] if i < lead else 0 for s in (su, sd, sz, sB, sC) for i in (0, 1)]
-    return _lib.ChannelDesc(u.shape[0], u.shape[1] if lead == 2 else 1, D, N, G, *strides, code, int(bool(softplus)))
+    _same("skip", skip, (D,), torch.float32, dev)
+    _same("delta_bias", delta_bias, (D,), torch.float32, dev)
+    if lead == 2:
+        return _lib.ChannelDesc(rows[0], rows[1], D, N, G, su[0], su[1], sd[0], sd[1], sz[0], sz[1], sB[0], sB[1],
+                                sC[0], sC[1], code, 1 if softplus else 0)
+    return _lib.ChannelDesc(rows[0], 1, D, N, G, su[0], 0, sd[0], 0, sz[0], 0, sB[0], 0, sC[0], 0, code,
+                            1 if softplus else 0)
+
+
+def _chan_bytes(query, d):
+    return _bytes(query, _lib.ChannelDesc, d.batch, d.seqlen, d.channels, d.dstate, d.ngroups, *(0,) * 10, d.dtype, 1)
 
 
 def channel_scan_fwd_workspace_bytes(u, delta, A, B, C) -> int:
-    n = ctypes.c_size_t()
-    _lib.check(_L().ssd_channel_scan_fwd_workspace_bytes(
-        _chan_check(u, delta, A, B, C, None, None, None, True, 2), n))
-    return n.value
+    return _chan_bytes("ssd_channel_scan_fwd_workspace_bytes", _chan_check(u, delta, A, B, C, None, None, None, True, 2))
 
 
 def channel_scan_fwd(u, delta, A, B, C, skip=None, gate=None, delta_bias=None, softplus=False, initial_state=None,
@@ -233,27 +265,22 @@ def channel_scan_fwd(u, delta, A, B, C, skip=None, gate=None, delta_bias=None, s
     None); channel_step continues from the state."""
     d = _chan_check(u, delta, A, B, C, skip, gate, delta_bias, softplus, 2)
     dev, state = u.device, (u.shape[0], u.shape[2], A.shape[1])
-    _check("initial_state", initial_state, state, torch.float32, dev)
-    _check("final_state", final_state, state, torch.float32, dev)
-    _check("y", y, u.shape, u.dtype, dev)
+    _same("initial_state", initial_state, state, torch.float32, dev)
+    _same("final_state", final_state, state, torch.float32, dev)
+    _same("y", y, u.shape, u.dtype, dev)
     _seqlens(seqlens, u.shape[0], dev)
     if y is None:
         y = torch.empty(u.shape, dtype=u.dtype, device=dev)
     if final_state is None and return_final_state:
         final_state = torch.empty(state, dtype=torch.float32, device=dev)
-    n = ctypes.c_size_t()
-    _lib.check(_L().ssd_channel_scan_fwd_workspace_bytes(d, n))
-    workspace, wsz = _workspace(workspace, n.value, dev)
+    workspace, wsz = _workspace(workspace, _chan_bytes("ssd_channel_scan_fwd_workspace_bytes", d), dev)
     _enqueue(dev, _L().ssd_channel_scan_fwd, d, _at(u), _at(delta), _at(A), _at(B), _at(C), _at(skip), _at(gate),
              _at(delta_bias), _at(initial_state), _at(seqlens), _at(y), _at(final_state), _at(workspace), wsz)
     return y, final_state
 
 
 def channel_scan_bwd_workspace_bytes(u, delta, A, B, C) -> int:
-    n = ctypes.c_size_t()
-    _lib.check(_L().ssd_channel_scan_bwd_workspace_bytes(
-        _chan_check(u, delta, A, B, C, None, None, None, True, 2), n))
-    return n.value
+    return _chan_bytes("ssd_channel_scan_bwd_workspace_bytes", _chan_check(u, delta, A, B, C, None, None, None, True, 2))
 
 
 def channel_scan_bwd(u, delta, A, B, C, dy, skip=None, gate=None, delta_bias=None, softplus=False,
@@ -268,14 +295,12 @@ def channel_scan_bwd(u, delta, A, B, C, dy, skip=None, gate=None, delta_bias=Non
     d = _chan_check(u, delta, A, B, C, skip, gate, delta_bias, softplus, 2)
     dev, dt, f32, state = u.device, u.dtype, torch.float32, (u.shape[0], u.shape[2], A.shape[1])
     _need("dy", dy)
-    _check("dy", dy, u.shape, dt, dev)
-    _check("initial_state", initial_state, state, f32, dev)
-    _check("dfinal_state", dfinal_state, state, f32, dev)
+    _same("dy", dy, u.shape, dt, dev)
+    _same("initial_state", initial_state, state, f32, dev)
+    _same("dfinal_state", dfinal_state, state, f32, dev)
     _seqlens(seqlens, u.shape[0], dev)
-    n = ctypes.c_size_t()
-    _lib.check(_L().ssd_channel_scan_bwd_workspace_bytes(d, n))
-    workspace, wsz = _workspace(workspace, n.value, dev)
-    new = lambda like, dtype, wanted: torch.empty(tuple(like), dtype=dtype, device=dev) if wanted else None
+    workspace, wsz = _workspace(workspace, _chan_bytes("ssd_channel_scan_bwd_workspace_bytes", d), dev)
+    new = lambda like, dtype, wanted: torch.empty(like, dtype=dtype, device=dev) if wanted else None
     g = {"du": new(u.shape, dt, True), "ddelta": new(u.shape, dt, True), "dgate": new(u.shape, dt, gate is not None),
          "dB": new(B.shape, dt, True), "dC": new(B.shape, dt, True), "dA": new(A.shape, f32, True),
          "dskip": new(A.shape[:1], f32, skip is not None), "ddelta_bias": new(A.shape[:1], f32, delta_bias is not None),
@@ -291,8 +316,8 @@ def channel_step(state, u, delta, A, B, C, skip=None, gate=None, delta_bias=None
     B, C [Bz,G,N] with dense rows.  Returns y [Bz,D]."""
     d = _chan_check(u, delta, A, B, C, skip, gate, delta_bias, softplus, 1)
     _need("state", state)
-    _check("state", state, (u.shape[0], u.shape[1], A.shape[1]), torch.float32, u.device)
-    _check("y", y, u.shape, u.dtype, u.device)
+    _same("state", state, (u.shape[0], u.shape[1], A.shape[1]), torch.float32, u.device)
+    _same("y", y, u.shape, u.dtype, u.device)
     if y is None:
         y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
     _enqueue(u.device, _L().ssd_channel_step, d, _at(state), _at(u), _at(delta), _at(A), _at(B), _at(C), _at(skip),
