@@ -4,10 +4,11 @@
 // One filter of W taps (2..4) per channel along the sequence,
 //     pre[t] = bias + sum_k w[k] x'[t - (W-1) + k],   y = silu(pre) or pre,
 // with x' continued to the left by a window or zeros.  About one flop per byte:
-// bound by HBM.  A thread owns 16 bytes of consecutive channels (or one channel
-// where rows do not allow wide accesses) and walks `rows` steps with the last
-// W-1 inputs in registers, so every input row is read once but for the W-1 rows
-// ahead of each walk; a wavefront's accesses are one contiguous run.
+// bound by HBM.  A thread owns four consecutive channels (one where rows do not
+// allow wide accesses; eight in bf16 measured 3 to 5% slower, their registers
+// leaving two wavefronts per SIMD in the backward) and walks `rows` steps with the
+// last W-1 inputs in registers, so every input row is read once but for the W-1
+// rows ahead of each walk; a wavefront's accesses are one contiguous run.
 //
 // Backward, with dpre[t] = dy[t] act'(pre[t]) (0 outside the sequence):
 //     dx[t] = sum_k w[k] dpre[t + W-1 - k],  dw[k] = sum_t dpre[t] x'[t-(W-1)+k],
@@ -36,7 +37,7 @@ struct ConvArgs {
 template <typename T, int V> struct Row {   // V elements of a row, as stored
     T v[V];
 };
-template <> struct Row<u16, 8> { uint4 v; };
+template <> struct Row<u16, 4> { uint2 v; };
 template <> struct Row<float, 4> { float4 v; };
 
 template <typename T, int V> __device__ __forceinline__ Row<T, V> load_row(const T* p) {
@@ -47,9 +48,7 @@ template <typename T, int V> __device__ __forceinline__ Row<T, V> load_row(const
 }
 template <typename T, int V> __device__ __forceinline__ Row<T, V> zero_row() {
     Row<T, V> r;
-    if constexpr (V == 1) r.v[0] = 0;
-    else if constexpr (V == 8) r.v = make_uint4(0, 0, 0, 0);
-    else r.v = make_float4(0.f, 0.f, 0.f, 0.f);
+    __builtin_memset(&r, 0, sizeof(r));
     return r;
 }
 template <int V> __device__ __forceinline__ void widen(const Row<float, V>& r, float* f) {
@@ -60,9 +59,10 @@ template <int V> __device__ __forceinline__ void widen(const Row<u16, V>& r, flo
     if constexpr (V == 1) {
         f[0] = bf_bits_to_f32(r.v[0]);
     } else {
-        const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+        uint32_t w[V / 2];
+        __builtin_memcpy(w, &r, sizeof(w));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < V / 2; ++i) {
             f[2 * i] = __uint_as_float(w[i] << 16);
             f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
@@ -76,11 +76,13 @@ template <int V> __device__ __forceinline__ void store_row(u16* p, const float* 
     if constexpr (V == 1) {
         *p = f32_to_bf_bits(f[0]);
     } else {
-        uint32_t w[4];
+        Row<u16, V> r;
+        uint32_t w[V / 2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < V / 2; ++i)
             w[i] = (uint32_t)f32_to_bf_bits(f[2 * i]) | ((uint32_t)f32_to_bf_bits(f[2 * i + 1]) << 16);
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        __builtin_memcpy(&r, w, sizeof(w));
+        *reinterpret_cast<decltype(r.v)*>(p) = r.v;
     }
 }
 template <typename T, int V> __device__ __forceinline__ void store_raw(T* p, const Row<T, V>& r) {
@@ -421,7 +423,7 @@ template <typename T, int V, typename F> hipError_t by_width(const ConvShape& s,
     return f.template go<T, V, 2, false>();
 }
 template <typename F> hipError_t by_type(const ConvShape& s, int vec, F f) {
-    if (s.bf16) return vec > 1 ? by_width<u16, 8>(s, f) : by_width<u16, 1>(s, f);
+    if (s.bf16) return vec > 1 ? by_width<u16, 4>(s, f) : by_width<u16, 1>(s, f);
     return vec > 1 ? by_width<float, 4>(s, f) : by_width<float, 1>(s, f);
 }
 
@@ -487,9 +489,11 @@ struct StepCall {
 int conv_vec(const ConvShape& s, const void* x, const void* window, const void* const* y, const void* dx,
              const void* params, const void* params2)
 {
-    const int vec = s.bf16 ? 8 : 4;
-    auto wide = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-    bool ok = wide(x) && wide(window) && wide(dx) && wide(params) && wide(params2) && s.C % vec == 0 &&
+    constexpr int vec = 4;
+    const uintptr_t bytes = s.bf16 ? 8 : 16;
+    auto wide = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+    bool ok = wide(x) && wide(window) && wide(dx) && reinterpret_cast<uintptr_t>(params) % 16 == 0 &&
+              reinterpret_cast<uintptr_t>(params2) % 16 == 0 && s.C % vec == 0 &&
               s.xr % vec == 0 && s.xb % vec == 0;
     for (int i = 0; i < 3; ++i)
         if (s.piece[i]) ok = ok && s.piece[i] % vec == 0 && wide(y[i]);
@@ -499,7 +503,7 @@ int conv_vec(const ConvShape& s, const void* x, const void* window, const void* 
 hipError_t launch_conv_fwd(const ConvShape& s, const void* x, const float* weight, const float* bias,
                            const void* win0, const int32_t* lens, void* const* y, void* win1, hipStream_t st)
 {
-    int vec = conv_vec(s, x, win0, y, win1, weight, bias);
+    const int vec = conv_vec(s, x, win0, y, win1, weight, bias);
     return by_type(s, vec, FwdCall{s, args_of(s, vec, conv_rows(s, false)), x, weight, bias, win0, lens, y, win1, st});
 }
 
@@ -509,7 +513,7 @@ hipError_t launch_conv_bwd(const ConvShape& s, const void* x, const float* weigh
 {
     int vec = conv_vec(s, x, win0, dy, dx, weight, bias);
     const uintptr_t rest = reinterpret_cast<uintptr_t>(dwin0) | reinterpret_cast<uintptr_t>(dwin1);
-    if (rest % 16 != 0) vec = 1;
+    if (rest % (s.bf16 ? 8 : 16) != 0) vec = 1;
     hipError_t e = by_type(s, vec, BwdCall{s, args_of(s, vec, conv_rows(s, true)), x, weight, bias, win0, lens,
                                            dy, dwin1, dx, dwin0, parts, st});
     if (e != hipSuccess) return e;
