@@ -114,7 +114,8 @@ ssd_status chan_shape(const ssd_channel_desc* d, ssd::ChanShape* s) {
     if (d->softplus != 0 && d->softplus != 1) return fail(SSD_ERR_SHAPE, "softplus must be 0 or 1");
     if (d->dstate > 64)
         return fail(SSD_ERR_UNSUPPORTED, "dstate must be at most 64 (got %lld)", (long long)d->dstate);
-    if (d->batch > 65535 || d->seqlen > ((int64_t)1 << 31) || d->channels > ((int64_t)1 << 20) ||
+    // grid limits, and 32-bit steps and offsets inside a segment
+    if (d->batch > 65535 || d->ngroups > 65535 || d->seqlen > ((int64_t)1 << 30) || d->channels > ((int64_t)1 << 20) ||
         d->batch * d->seqlen > kMaxSize / d->channels)
         return fail(SSD_ERR_UNSUPPORTED, "sizes beyond the supported range");
     SSD_CHECK(check_stride("u", d->batch, d->u_bstride, d->seqlen, d->u_rstride));

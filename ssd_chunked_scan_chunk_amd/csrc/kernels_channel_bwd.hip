@@ -551,59 +551,52 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
     }
 }
 
-// dB and dC: the workgroups' sums of a step added, one thread per (batch, step,
-// group, B or C, state); zeros past a sequence's end.
-template <typename T>
-__global__ __launch_bounds__(256) void k_chan_sum_bc(BwdArgs a, int NP, T* __restrict__ dB, T* __restrict__ dC,
-                                                     int64_t items)
-{
-    const ChanArgs& f = a.f;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= items) return;
-    const int G = a.tiles / f.tpg;
-    const int n = (int)(i & (2 * NP - 1));              // [B, C][state]
-    const int64_t r = i / (2 * NP), g = r % G, bt = r / G, b = bt / f.L, t = bt - b * f.L;
-    const int k = n & (NP - 1);
-    if (k >= f.N) return;
-    float s = 0.f;
-    if (t < chan_length(f.in.lens, b, f.L)) {
-        const float* p = a.pbc + ((bt * a.tiles + g * f.tpg) * 2 * NP) + n;
-        int q = 0;
-        for (; q + 4 <= f.tpg; q += 4) {
-            const float v0 = p[(int64_t)q * 2 * NP], v1 = p[(int64_t)(q + 1) * 2 * NP];
-            const float v2 = p[(int64_t)(q + 2) * 2 * NP], v3 = p[(int64_t)(q + 3) * 2 * NP];
-            s += (v0 + v1) + (v2 + v3);
-        }
-        for (; q < f.tpg; ++q) s += p[(int64_t)q * 2 * NP];
-    }
-    Elem<T>::store((n < NP ? dB : dC) + r * f.N + k, s);
-}
-
-// out[i] = sum over the segments of all batches of p[row][i], for dA, dskip and dbias
-__global__ __launch_bounds__(256) void k_chan_sum_rows(const float* __restrict__ pA, float* __restrict__ dA, int64_t nA,
-                                                       const float* __restrict__ ps, float* __restrict__ ds,
-                                                       const float* __restrict__ pb, float* __restrict__ db,
-                                                       int64_t D, int64_t rows)
-{
-    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = nA;
-    const float* p = pA;
-    float* out = dA;
-    if (i >= nA) {
-        i -= nA;
-        n = D;
-        if (i < D) { p = ps; out = ds; }
-        else { i -= D; p = pb; out = db; }
-        if (i >= D) return;
-    }
-    if (!out) return;
+// The sums over workgroups, in a fixed order.  The first `bc_blocks` workgroups:
+// dB and dC, one thread per (batch, step, group, B or C, state), zeros past a
+// sequence's end.  The others: dA, dskip and dbias over the segments of all
+// batches, one thread per column.
+__device__ __forceinline__ float sum_strided(const float* p, int64_t n, int64_t stride) {
     float s = 0.f;
     int64_t r = 0;
-    for (; r + 4 <= rows; r += 4) {
-        const float v0 = p[r * n + i], v1 = p[(r + 1) * n + i], v2 = p[(r + 2) * n + i], v3 = p[(r + 3) * n + i];
-        s += (v0 + v1) + (v2 + v3);
+    constexpr int U = 8;   // loads in flight
+    for (; r + U <= n; r += U) {
+        float v[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) v[k] = p[(r + k) * stride];
+        s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
-    for (; r < rows; ++r) s += p[r * n + i];
-    out[i] = s;
+    for (; r < n; ++r) s += p[r * stride];
+    return s;
+}
+template <typename T>
+__global__ __launch_bounds__(256) void k_chan_sums(BwdArgs a, int NP, unsigned bc_blocks, int64_t rows,
+                                                   int64_t segs, ChanGrads o)
+{
+    const ChanArgs& f = a.f;
+    if (blockIdx.x < bc_blocks) {
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+        const int G = a.tiles / f.tpg, n = (int)(i & (2 * NP - 1)), k = n & (NP - 1);   // [B, C][state]
+        const int64_t r = i / (2 * NP), g = r % G, bt = r / G, b = bt / f.L, t = bt - b * f.L;
+        if (bt >= rows || k >= f.N) return;
+        const float s = t < chan_length(f.in.lens, b, f.L)
+                            ? sum_strided(a.pbc + (bt * a.tiles + g * f.tpg) * 2 * NP + n, f.tpg, 2 * NP) : 0.f;
+        Elem<T>::store((T*)(n < NP ? o.dB : o.dC) + r * f.N + k, s);
+        return;
+    }
+    int64_t i = (int64_t)(blockIdx.x - bc_blocks) * 256 + threadIdx.x;
+    const int64_t nA = f.D * f.N;
+    const float* p = a.pA;
+    float* out = o.dA;
+    int64_t n = nA;
+    if (i >= nA) {
+        i -= nA;
+        n = f.D;
+        p = i < f.D ? a.pskip : a.pbias;
+        out = i < f.D ? o.dskip : o.ddbias;
+        if (i >= f.D) i -= f.D;
+        if (i >= f.D) return;
+    }
+    if (out) out[i] = sum_strided(p + i, segs, n);
 }
 
 template <typename T, int NR, int CW>
@@ -621,14 +614,10 @@ hipError_t run_bwd(const BwdArgs& a, const ChanShape& s, const ChanGrads& o, hip
     }
     if (a.f.nseg > 1) hipLaunchKernelGGL((k_chan_bwd<T, NR, CW, true>), grid, blk, 0, st, a);
     else hipLaunchKernelGGL((k_chan_bwd<T, NR, CW, false>), grid, blk, 0, st, a);
-    if (s.L > 0) {
-        const int64_t items = s.Bz * s.L * s.G * 2 * NP;
-        hipLaunchKernelGGL(k_chan_sum_bc<T>, dim3((unsigned)((items + 255) / 256)), blk, 0, st, a, NP, (T*)o.dB,
-                           (T*)o.dC, items);
-    }
-    const int64_t cols = s.D * (s.N + 2);
-    hipLaunchKernelGGL(k_chan_sum_rows, dim3((unsigned)((cols + 255) / 256)), blk, 0, st, a.pA, o.dA, s.D * s.N, a.pskip,
-                       o.dskip, a.pbias, o.ddbias, s.D, s.Bz * a.f.nseg);
+    const unsigned bc_blocks = (unsigned)((s.Bz * s.L * s.G * 2 * NP + 255) / 256);
+    const unsigned columns = (unsigned)((s.D * (s.N + 2) + 255) / 256);
+    hipLaunchKernelGGL(k_chan_sums<T>, dim3(bc_blocks + columns), blk, 0, st, a, NP, bc_blocks, s.Bz * s.L,
+                       s.Bz * a.f.nseg, o);
     return hipGetLastError();
 }
 template <typename T>

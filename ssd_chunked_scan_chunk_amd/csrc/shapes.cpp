@@ -101,7 +101,7 @@ size_t chan_fwd_bytes(const ChanShape& s, const ChanPlan& p) {
     return (size_t)s.Bz * p.nseg * s.D * (s.N + 1) * sizeof(float);
 }
 
-// Segments until the GPU holds about six workgroups per CU, none shorter than 32
+// Segments until the GPU holds about six workgroups per CU, none shorter than 16
 // steps: 4 x 2048 x 5120 x 16 takes 1092 us in one segment, 730 in four (1280
 // workgroups), 711 in eight, 783 in 32; 1 x 2048 x 1536 x 16 826 us in one, 101 in 16,
 // 83 in 32 and 88 in 48.  64 channels to a workgroup measured faster than 32 (711
@@ -114,7 +114,7 @@ ChanBwdPlan chan_bwd_plan(const ChanShape& s) {
     const int64_t np = s.N <= 8 ? 8 : s.N <= 16 ? 16 : s.N <= 32 ? 32 : 64, nr = np / pieces;
     const int64_t groups = s.Bz * tiles > 0 ? s.Bz * tiles : 1, want = (1536 + groups - 1) / groups;
     p.seg = ((s.L + want - 1) / want + 7) / 8 * 8;
-    if (p.seg < 32) p.seg = 32;
+    if (p.seg < 16) p.seg = 16;
     p.nseg = s.L > 0 ? (s.L + p.seg - 1) / p.seg : 1;
     p.nb = p.seg / 8;
     const int64_t rows = s.Bz * p.nseg;

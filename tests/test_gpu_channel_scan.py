@@ -330,3 +330,76 @@ def test_backward_repeats_streams_and_graphs():
             for got in (other, held, again):
                 for k in want:
                     assert torch.equal(got[k], want[k]), (L, k)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_sequences(dtype):
+    # an empty batch: nothing but the parameters' gradients, which are zero
+    log("channel scan empty batch %s" % dtype)
+    d = inputs(0, 9, 24, 16, 1, dtype)
+    y, h = ssd.channel_scan_fwd(**d, softplus=True, return_final_state=True)
+    g = ssd.channel_scan_bwd(**d, dy=torch.zeros_like(d["u"]), softplus=True, return_dinitial_state=True)
+    torch.cuda.synchronize()
+    assert y.shape == (0, 9, 24) and h.shape == (0, 24, 16)
+    for k in ("dA", "dskip", "ddelta_bias"):
+        assert g[k].shape[0] == 24 and not g[k].any(), k
+
+
+def test_convolution_into_the_chunked_scan():
+    # the convolution's pieces are the chunked scan's X, B and C, forward and
+    # backward, a prompt and then tokens
+    log("short conv into the chunked scan")
+    Bz, L, H, P, N, G, W = 2, 150, 4, 64, 64, 1, 4
+    gen = torch.Generator().manual_seed(3)
+    r = lambda *s, dt=torch.bfloat16: torch.randn(s, generator=gen).to(dt).cuda()
+    pieces = (H * P, G * N, G * N)
+    rows = r(Bz, L + 1, 32 + sum(pieces))
+    x, weight, bias = rows[:, :, 32:], r(sum(pieces), W, dt=torch.float32) * 0.5, r(sum(pieces), dt=torch.float32) * 0.1
+    a = -torch.rand(Bz, L + 1, H, generator=gen).cuda() * 0.2
+    split = lambda ys, *lead: (ys[0].view(*lead, H, P), ys[1].view(*lead, G, N), ys[2].view(*lead, G, N))
+    ys, win = ssd.short_conv_fwd(x[:, :L], weight, bias, pieces=pieces, return_final_window=True)
+    X, B, C = split(ys, Bz, L)
+    a0 = a[:, :L].contiguous()
+    Y, S = ssd.chunk_scan_fwd(X, a0, B, C, 64, return_final_state=True)
+    dY = r(Bz, L, H, P)
+    g = ssd.chunk_scan_bwd(X, a0, B, C, dY, 64)
+    gc = ssd.short_conv_bwd(x[:, :L], weight, tuple(g[k].view(Bz, L, -1) for k in ("dX", "dB", "dC")), bias)
+    xt, Bt, Ct = split(ssd.short_conv_step(win, x[:, L], weight, bias, pieces=pieces), Bz)
+    y1 = ssd.step(S, xt, a[:, L].contiguous(), Bt, Ct)
+    torch.cuda.synchronize()
+    # the convolution itself is exact to its tolerance ...
+    w = ref.conv(n64(x), n64(weight), n64(bias), None, None, True)
+    ref.check("y", torch.cat([torch.cat(ys, 2), torch.cat([t.reshape(Bz, 1, -1) for t in (xt, Bt, Ct)], 2)], 1), w,
+              "bf16")
+    # ... and the scan sees exactly its output: one oracle run over prompt and token
+    import oracle
+    X64, B64, C64 = (np.concatenate([n64(p), n64(q)[:, None]], 1) for p, q in ((X, xt), (B, Bt), (C, Ct)))
+    Yr, Sr = oracle.fwd(X64, n64(a), B64, C64)
+    got = np.concatenate([n64(Y), n64(y1)[:, None]], 1)
+    assert np.abs(got - Yr).max() <= 2e-2 * np.abs(Yr).max()     # the chunked scan's own tolerance
+    assert np.abs(n64(S) - Sr).max() <= 2e-2 * np.abs(Sr).max()
+    dyc = np.concatenate([n64(g[k]).reshape(Bz, L, -1) for k in ("dX", "dB", "dC")], 2)
+    wb = ref.conv(n64(x[:, :L]), n64(weight), n64(bias), None, None, True, dyc)
+    ref.check("dx", gc["dx"], wb, "bf16")
+    ref.check("dweight", gc["dweight"], wb, "f32")
+    ref.check("dbias", gc["dbias"], wb, "f32")
+
+
+def test_large_strides_and_many_steps():
+    # batches far apart in memory (offsets past 2^31 elements), a sequence of 9000
+    # steps, the last batch alone live
+    log("channel scan far batches")
+    if torch.cuda.get_device_properties(0).total_memory < (48 << 30):
+        pytest.skip("needs 24 GiB of device memory")
+    far = (1 << 31) + 64                       # elements between batches of u
+    L, D = 9000, 32
+    d = inputs(2, L, D, 4, 1, "bf16", 12, gate=True)
+    buf = torch.empty(far + L * D, dtype=torch.bfloat16, device="cuda")
+    u = torch.as_strided(buf, (2, L, D), (far, D, 1))
+    u.copy_(d["u"])
+    want = ssd.channel_scan_fwd(**d, softplus=True)[0]
+    got = ssd.channel_scan_fwd(**dict(d, u=u), softplus=True)[0]
+    x, _ = ssd.short_conv_fwd(u, d["A"], d["skip"])
+    x0, _ = ssd.short_conv_fwd(d["u"].contiguous(), d["A"], d["skip"])
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(x, x0)

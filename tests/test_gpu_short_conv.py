@@ -179,3 +179,35 @@ def test_given_outputs_and_their_surroundings():
         assert bool((buf[:32] == 5).all()) and bool((buf[32 + Bz * L * C:] == 5).all())
         with pytest.raises(ssd.SSDError, match="SSD_ERR_ALIAS"):
             ssd.short_conv_fwd(y, d["weight"], y=y)
+
+
+def test_no_sequences():
+    log("short conv empty batch")
+    d = inputs(0, 9, 24, 4, "bf16")
+    y, win = ssd.short_conv_fwd(d["x"], d["weight"], d["bias"], return_final_window=True)
+    g = ssd.short_conv_bwd(d["x"], d["weight"], d["dy"][0], d["bias"])
+    torch.cuda.synchronize()
+    assert y.shape == (0, 9, 24) and win.shape == (0, 3, 24)
+    assert not g["dweight"].any() and not g["dbias"].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shift", [1, 2, 3, 4])
+def test_any_alignment(dtype, shift):
+    # every tensor `shift` elements into its buffer: wide accesses where the
+    # addresses allow them, single elements elsewhere, the same values
+    log("short conv alignment %s %d" % (dtype, shift))
+    d = inputs(2, 21, 16, 4, dtype, seed=shift)
+    move = lambda t: torch.cat([t.new_zeros(shift), t.flatten()])[shift:].view(t.shape)
+    run = lambda d, y: (ssd.short_conv_fwd(d["x"], d["weight"], d["bias"], initial_window=d["win"], y=y,
+                                           return_final_window=True),
+                        ssd.short_conv_bwd(d["x"], d["weight"], d["dy"][0], d["bias"], initial_window=d["win"],
+                                           dfinal_window=d["dwin"], return_dinitial_window=True))
+    (y, win), g = run(d, None)
+    m = {k: move(v) if k != "dy" else [move(v[0])] for k, v in d.items()}
+    (ym, winm), gm = run(m, move(torch.zeros_like(y)))
+    torch.cuda.synchronize()
+    assert torch.equal(y, ym) and torch.equal(win, winm)
+    for k in g:
+        # dweight and dbias: a walk covers the same steps either way
+        assert torch.equal(g[k], gm[k]), k

@@ -204,7 +204,9 @@ def chan_desc(**kw):
     (dict(ngroups=3), _lib.SSD_ERR_SHAPE), (dict(dtype=2), _lib.SSD_ERR_DTYPE), (dict(softplus=2), _lib.SSD_ERR_SHAPE),
     (dict(B_rstride=-1), _lib.SSD_ERR_SHAPE), (dict(C_bstride=1 << 60), _lib.SSD_ERR_UNSUPPORTED),
     (dict(batch=1 << 20), _lib.SSD_ERR_UNSUPPORTED), (dict(channels=1 << 30), _lib.SSD_ERR_UNSUPPORTED),
-    (dict(seqlen=1 << 40), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(seqlen=1 << 40), _lib.SSD_ERR_UNSUPPORTED), (dict(seqlen=(1 << 30) + 1), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(channels=1 << 17, ngroups=1 << 17), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(u_rstride=(1 << 24) + 1), _lib.SSD_ERR_UNSUPPORTED),
     (dict(batch=1 << 15, channels=1 << 12), _lib.SSD_ERR_UNSUPPORTED),
 ])
 def test_scan_abi_shapes(lib, kw, code):
@@ -234,13 +236,15 @@ def test_scan_abi_pointers(lib):
         assert fwd(**{k: odd}) == _lib.SSD_ERR_ALIGN
     assert fwd(y=P[0]) == fwd(fin=P[2]) == fwd(h0=P[7], fin=P[7]) == fwd(fin=P[6]) == _lib.SSD_ERR_ALIAS
     assert fwd(d=chan_desc(batch=0), u=None, y=None) == fwd(d=chan_desc(seqlen=0), y=None) == _lib.SSD_OK
+    # a single step has no stride between steps
+    assert fwd(d=chan_desc(seqlen=1, u_rstride=1 << 39), u=None) == _lib.SSD_ERR_NULL
     # a long sequence of few channels is cut into segments, which need a workspace
     long = chan_desc(batch=1, seqlen=1 << 16, u_bstride=0)
     assert lib.ssd_channel_scan_fwd_workspace_bytes(long, n) == 0
-    if n.value:
-        assert fwd(d=long, ws=None) == fwd(d=long, wsz=n.value - 1) == _lib.SSD_ERR_WORKSPACE
-        assert fwd(d=long, wsz=n.value, ws=ctypes.c_void_p((1 << 45) + 4)) == _lib.SSD_ERR_ALIGN
-        assert fwd(d=long, wsz=n.value, ws=P[6]) == _lib.SSD_ERR_ALIAS
+    assert n.value > 0
+    assert fwd(d=long, ws=None) == fwd(d=long, wsz=n.value - 1) == _lib.SSD_ERR_WORKSPACE
+    assert fwd(d=long, wsz=n.value, ws=ctypes.c_void_p((1 << 45) + 4)) == _lib.SSD_ERR_ALIGN
+    assert fwd(d=long, wsz=n.value, ws=P[6]) == _lib.SSD_ERR_ALIAS
 
     one = chan_desc(seqlen=1)
     step = lambda st=P[8], y=P[6], d=one: lib.ssd_channel_step(d, st, *P[:5], None, None, None, y, None)
