@@ -101,20 +101,33 @@ size_t chan_fwd_bytes(const ChanShape& s, const ChanPlan& p) {
     return (size_t)s.Bz * p.nseg * s.D * (s.N + 1) * sizeof(float);
 }
 
-// Segments until the GPU holds about six workgroups per CU, none shorter than 16
-// steps: 4 x 2048 x 5120 x 16 takes 1092 us in one segment, 730 in four (1280
-// workgroups), 711 in eight, 783 in 32; 1 x 2048 x 1536 x 16 826 us in one, 101 in 16,
-// 83 in 32 and 88 in 48.  64 channels to a workgroup measured faster than 32 (711
-// against 835 us) wherever a lane's states of a batch fit the registers (dstate up
-// to 16).
+// Segments of the backward: three to eleven workgroups per CU in all, as evenly as
+// they come (the CU with one more sets the time), the fewer the better as each
+// costs some twelve steps' time of its own, and none shorter than 16 steps.  4 x
+// 2048 x 5120 x 16 (320 workgroups per segment) takes 1092 us in one segment, 730 in
+// four, 753 in five, 711 in eight, 783 in 32; 1 x 2048 x 1536 x 16 (24) 826 us in
+// one, 101 in 16, 83 in 32, 88 in 48.  64 channels to a workgroup measured faster
+// than 32 (711 against 835 us) wherever a lane's states of a batch fit the registers
+// (dstate up to 16).
 ChanBwdPlan chan_bwd_plan(const ChanShape& s) {
     ChanBwdPlan p;
     p.cw = s.N <= 16 ? 64 : 32;
     const int64_t tiles = chan_tiles(s, p.cw), pieces = 256 / p.cw;
     const int64_t np = s.N <= 8 ? 8 : s.N <= 16 ? 16 : s.N <= 32 ? 32 : 64, nr = np / pieces;
-    const int64_t groups = s.Bz * tiles > 0 ? s.Bz * tiles : 1, want = (1536 + groups - 1) / groups;
-    p.seg = ((s.L + want - 1) / want + 7) / 8 * 8;
-    if (p.seg < 16) p.seg = 16;
+    const int64_t groups = s.Bz * tiles > 0 ? s.Bz * tiles : 1, most = s.L > 16 ? (s.L + 15) / 16 : 1;
+    int64_t want = groups >= 768 ? 1 : (768 + groups - 1) / groups;
+    if (want > most) want = most;
+    double least = 1e300;
+    p.seg = 16;
+    for (int64_t k = want; k == want || (k <= most && groups * k <= 2816); k += 1 + k / 16) {
+        const int64_t seg = ((s.L + k - 1) / k + 7) / 8 * 8, w = groups * k;
+        const double uneven = (double)((w + 255) / 256 * 256) / (double)w;
+        const double cost = uneven * (1.0 + 12.0 / (double)(seg > 0 ? seg : 8)) * (1.0 + 64.0 / (double)w);
+        if (cost < least) {
+            least = cost;
+            p.seg = seg > 16 ? seg : 16;
+        }
+    }
     p.nseg = s.L > 0 ? (s.L + p.seg - 1) / p.seg : 1;
     p.nb = p.seg / 8;
     const int64_t rows = s.Bz * p.nseg;
