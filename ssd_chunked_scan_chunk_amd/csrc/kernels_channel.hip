@@ -30,28 +30,36 @@ namespace {
 
 template <int V> using Int = std::integral_constant<int, V>;
 
+constexpr int TB = 8;   // steps of a batch
+
+template <int NR, int CW, bool FULL> struct FwdLds {
+    static constexpr int kParts = 256 / CW;
+    float2 dt[2][TB][CW];                                    // dt, dt u
+    float bc[2][TB * kParts * NR * (FULL ? 2 : 1)];          // [B, C][step][state]
+    float y[FULL ? 2 : 1][FULL ? TB : 1][kParts][CW];
+};
+
+// The scan of the CW channels from cg0 on of group g, in segment `seg` of batch b.
 // CW: channels of a workgroup (64, or 32 with half the states in each half of a
 // wavefront); NR: states of a lane, 256 / CW parts of a channel's states.
 // FULL: outputs from the states entering each segment; otherwise each segment's
 // end state from zero (S) and its sum of dt.
 template <typename T, int NR, int CW, bool FULL>
-__global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
+__device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>& lds, int g, int cg0, int64_t b,
+                                         int64_t seg)
 {
     constexpr int ES = sizeof(T), NPART = 256 / CW, NP = NPART * NR;
-    constexpr int TB = 8, TP = TB * CW / 256;       // steps of a batch; (step, channel) pairs of a thread
+    constexpr int TP = TB * CW / 256;               // (step, channel) pairs of a thread
     constexpr int NBC = TB * NP * (FULL ? 2 : 1);   // elements of B and C in a batch
     constexpr int NE = (NBC + 255) / 256;           // of these, passed on by a thread
     constexpr bool EXACT = ES == 4;
-    __shared__ float2 s_dt[2][TB][CW];
-    __shared__ __align__(16) float s_bc[2][NBC];    // [B, C][step][state]
-    __shared__ float s_y[FULL ? 2 : 1][FULL ? TB : 1][NPART][CW];
     const int tid = threadIdx.x, c = tid & (CW - 1), part = tid / CW, n0 = part * NR;
-    const int g = blockIdx.x / a.tpg, cg = (blockIdx.x - g * a.tpg) * CW + c;
+    const int cg = cg0 + c;
     const bool live = cg < a.per;
     // threads past the group repeat its last channel and store nothing
     const int cl = live ? cg : a.per - 1;
     const uint32_t col = (uint32_t)cl * ES;
-    const int64_t gch = (int64_t)g * a.per, ch = gch + cl, b = blockIdx.z, seg = blockIdx.y;
+    const int64_t gch = (int64_t)g * a.per, ch = gch + cl;
     const int64_t ts = seg * a.seg, t1 = ts + a.seg < a.L ? ts + a.seg : a.L;
     const int64_t len = chan_length(a.in.lens, b, a.L);
     const int te = (int)(len < ts ? 0 : (len < t1 ? len : t1) - ts);   // steps to compute from ts on
@@ -131,12 +139,12 @@ __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
             u[k] = as_f32(ru[P][k]);
             z[k] = as_f32(rz[P][k]);
             sdt += dt;
-            s_dt[P][s][c] = make_float2(dt, dt * u[k]);
+            lds.dt[P][s][c] = make_float2(dt, dt * u[k]);
         }
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             const int i = e * 256 + tid;
-            if (NBC % 256 == 0 || i < NBC) s_bc[P][i] = (i & (NP - 1)) < a.N ? as_f32(rbc[P][e]) : 0.f;
+            if (NBC % 256 == 0 || i < NBC) lds.bc[P][i] = (i & (NP - 1)) < a.N ? as_f32(rbc[P][e]) : 0.f;
         }
     };
     // The batch at t, whose values lie in slot P; the inputs of the one after the
@@ -147,8 +155,8 @@ __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
         if (t == 0 || !FULL) lds_barrier();   // otherwise the one below has ordered slot P
 #pragma unroll
         for (int k = 0; k < TB; ++k) {
-            const float2 d = s_dt[P][k][c];
-            const float* bc = s_bc[P] + k * NP + n0;
+            const float2 d = lds.dt[P][k][c];
+            const float* bc = lds.bc[P] + k * NP + n0;
             float y = 0.f;
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
@@ -156,7 +164,7 @@ __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
                 h[i] = fmaf(e, h[i], d.y * bc[i]);
                 if (FULL) y = i == 0 ? h[i] * bc[TB * NP + i] : fmaf(h[i], bc[TB * NP + i], y);
             }
-            if (FULL) s_y[P][k][part][c] = y;
+            if (FULL) lds.y[P][k][part][c] = y;
         }
         float pu[TP], pz[TP];
 #pragma unroll
@@ -169,7 +177,7 @@ __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
                 const int s = part + k * NPART;
                 float y = 0.f;
 #pragma unroll
-                for (int q = 0; q < NPART; q += 2) y += s_y[P][s][q][c] + s_y[P][s][q + 1][c];
+                for (int q = 0; q < NPART; q += 2) y += lds.y[P][s][q][c] + lds.y[P][s][q + 1][c];
                 y = fmaf(skip, pu[k], y);
                 const float sz = pz[k] * sigmoid_of(pz[k]);
                 y *= gated ? sz : 1.f;
@@ -202,7 +210,7 @@ __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
             if (live && n0 + i < a.N) out[(row * a.D + ch) * a.N + n0 + i] = h[i];
         if constexpr (!FULL) {   // each thread summed its own share of the steps
             __syncthreads();
-            float* sum = &s_dt[0][0][0].x;
+            float* sum = &lds.dt[0][0][0].x;
             sum[tid] = sdt;
             __syncthreads();
             sdt = 0.f;
@@ -210,6 +218,31 @@ __global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
             for (int q = 0; q < NPART; ++q) sdt += sum[q * CW + c];
             if (live && part == 0) a.sumdt[row * a.D + ch] = sdt;
         }
+    }
+}
+
+template <typename T, int NR, int CW, bool FULL>
+__global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
+{
+    __shared__ __align__(16) FwdLds<NR, CW, FULL> lds;
+    const int g = blockIdx.x / a.tpg;
+    chan_fwd<T, NR, CW, FULL>(a, lds, g, (blockIdx.x - g * a.tpg) * CW, blockIdx.z, blockIdx.y);
+}
+
+// One segment, the first `whole` workgroups 64 channels wide, the others the halves
+// of the remaining 64-wide tiles: where the channels come to a few workgroups per CU
+// and up to half a one more, the halves even out what the CUs get.
+template <typename T, int NR>
+__global__ __launch_bounds__(256) void k_chan_fwd_mixed(ChanArgs a, int whole, int tiles)
+{
+    __shared__ __align__(16) union { FwdLds<NR, 64, true> w; FwdLds<NR / 2, 32, true> n; } lds;
+    const int past = (int)blockIdx.x - whole, flat = past < 0 ? blockIdx.x : whole + past / 2;
+    const int b = flat / tiles, tile = flat - b * tiles, g = tile / a.tpg, cg0 = (tile - g * a.tpg) * 64;
+    if (past < 0) {
+        chan_fwd<T, NR, 64, true>(a, lds.w, g, cg0, b, 0);
+    } else {
+        const int half = cg0 + (past & 1) * 32;
+        if (half < a.per) chan_fwd<T, NR / 2, 32, true>(a, lds.n, g, half, b, 0);
     }
 }
 
@@ -314,8 +347,21 @@ template <typename T, int NR, int CW> hipError_t run_fwd(const ChanArgs& a, cons
     hipLaunchKernelGGL((k_chan_fwd<T, NR, CW, true>), grid, blk, 0, st, a);
     return hipGetLastError();
 }
-template <typename T> hipError_t run_fwd_t(const ChanArgs& a, const ChanShape& s, int cw, hipStream_t st) {
-    if (cw == 32) {
+template <typename T, int NR>
+hipError_t run_fwd_mixed(const ChanArgs& a, const ChanShape& s, int64_t whole, hipStream_t st) {
+    const int64_t tiles = chan_tiles(s, 64), flats = s.Bz * tiles;
+    hipLaunchKernelGGL((k_chan_fwd_mixed<T, NR>), dim3((unsigned)(whole + 2 * (flats - whole))), dim3(256), 0, st, a,
+                       (int)whole, (int)tiles);
+    return hipGetLastError();
+}
+template <typename T> hipError_t run_fwd_t(const ChanArgs& a, const ChanShape& s, const ChanPlan& p, hipStream_t st) {
+    if (p.whole > 0) {
+        if (s.N <= 8) return run_fwd_mixed<T, 2>(a, s, p.whole, st);
+        if (s.N <= 16) return run_fwd_mixed<T, 4>(a, s, p.whole, st);
+        if (s.N <= 32) return run_fwd_mixed<T, 8>(a, s, p.whole, st);
+        return run_fwd_mixed<T, 16>(a, s, p.whole, st);
+    }
+    if (p.cw == 32) {
         if (s.N <= 8) return run_fwd<T, 1, 32>(a, s, st);
         if (s.N <= 16) return run_fwd<T, 2, 32>(a, s, st);
         if (s.N <= 32) return run_fwd<T, 4, 32>(a, s, st);
@@ -350,7 +396,7 @@ hipError_t launch_chan_fwd(const ChanShape& s, const ChanPlan& p, const ChanIn& 
     a.y = y; a.hfin = hfin;
     a.S = ws;
     a.sumdt = ws ? ws + s.Bz * p.nseg * s.D * s.N : nullptr;
-    return s.bf16 ? run_fwd_t<u16>(a, s, p.cw, st) : run_fwd_t<float>(a, s, p.cw, st);
+    return s.bf16 ? run_fwd_t<u16>(a, s, p, st) : run_fwd_t<float>(a, s, p, st);
 }
 
 hipError_t launch_chan_step(const ChanShape& s, float* state, const ChanIn& in, void* y, hipStream_t st)

@@ -42,10 +42,11 @@ struct ChanIn {
     const int32_t* lens;
 };
 // How the forward is laid over the GPU (shapes.cpp): channels of a workgroup (64
-// or 32), and segments of `seg` steps the sequence is cut into.
+// or 32), and segments of `seg` steps the sequence is cut into; whole > 0: one
+// segment, that many workgroups of 64 channels, the rest of 32.
 struct ChanPlan {
     int cw;
-    int64_t seg, nseg;
+    int64_t seg, nseg, whole;
 };
 ChanPlan chan_fwd_plan(const ChanShape& s);
 int64_t chan_tiles(const ChanShape& s, int cw);   // workgroups over the channels of one batch

@@ -71,9 +71,10 @@ static double chan_step_ns(int cw, int64_t N, int64_t r) {
 // Segments pay a second pass (0.72 of the steps' time), the scan over them (one
 // read and one write of their states) and two launches: 2 x 2048 x 5120 x 16 takes
 // 244 us in one segment, 151 us in 16; 8 x 2048 x 5120 x 16, whose channels fill
-// the GPU, 411 us in one and 544 us in 16.
+// the GPU, 408 us in one and 544 us in 16.
 ChanPlan chan_fwd_plan(const ChanShape& s) {
-    ChanPlan best{64, s.L > 0 ? s.L : 1, 1};
+    const int64_t all = s.L > 0 ? s.L : 1;
+    ChanPlan best{64, all, 1, 0};
     double least = 1e300;
     constexpr int kCounts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256};
     for (const int cw : {64, 32}) {
@@ -88,9 +89,18 @@ ChanPlan chan_fwd_plan(const ChanShape& s) {
                 us = 1.05 * (1.72 * steps + 10 + 0.05 * (double)nseg + 1e-6 * (double)(nseg * s.Bz * s.D * s.N));
             if (us < least) {
                 least = us;
-                best = ChanPlan{cw, nseg > 1 ? seg : (s.L > 0 ? s.L : 1), nseg};
+                best = ChanPlan{cw, nseg > 1 ? seg : all, nseg, 0};
             }
         }
+    }
+    // up to half a 64-wide workgroup per CU left over: as halves they add half a
+    // workgroup's time to every CU, not a whole one's to some (8 x 2048 x 5120 x 16, 640
+    // workgroups: 349 us against 408)
+    const int64_t flats = s.Bz * chan_tiles(s, 64), full = flats / 256, rest = flats % 256;
+    if (full > 0 && rest > 0 && rest <= 128) {
+        const double w = chan_step_ns(64, s.N, full), n = 16 + 1.41 * (double)s.N;
+        const double us = (double)s.L * (w + 0.8 * n) * 1e-3;
+        if (us < least) best = ChanPlan{64, all, 1, full * 256};
     }
     return best;
 }

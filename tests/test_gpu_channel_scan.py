@@ -88,6 +88,24 @@ def test_segments(dtype, Bz, L, D, N, G, seqlens):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,G,N", [(96, 2, 16), (64, 1, 16), (16, 1, 5)])
+def test_many_sequences(dtype, D, G, N):
+    # two workgroups of channels for every CU and a few more, which are halved; groups
+    # of 48 channels leave half a half empty
+    log("channel scan many sequences %s %d %d" % (dtype, D, N))
+    Bz = 520 // (2 if D == 96 else 1)
+    d = inputs(Bz, 9, D, N, G, dtype, D, wide=2)
+    seqlens = [(7 * b) % 10 for b in range(Bz)]
+    y, h = ssd.channel_scan_fwd(**d, softplus=True, seqlens=lens_of(seqlens), return_final_state=True)
+    torch.cuda.synchronize()
+    pick = list(range(0, Bz, 13)) + list(range(Bz - 9, Bz))   # the last are the halved ones
+    d = {k: v[pick] if k not in ("A", "skip", "delta_bias") else v for k, v in d.items()}
+    want = want_of(d, True, [seqlens[b] for b in pick])
+    ref.check("y", y[pick], want, dtype)
+    ref.check("final_state", h[pick], want, "f32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_extreme_step_sizes(dtype):
     # softplus over its whole range: steps that vanish, and steps so long that
     # nothing of the state is left
