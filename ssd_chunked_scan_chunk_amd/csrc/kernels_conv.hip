@@ -4,9 +4,9 @@
 // One filter of W taps (2..4) per channel along the sequence,
 //     pre[t] = bias + sum_k w[k] x'[t - (W-1) + k],   y = silu(pre) or pre,
 // with x' continued to the left by a window or zeros.  About one flop per byte:
-// bound by HBM.  A thread owns four consecutive channels (one where rows do not
-// allow wide accesses; eight in bf16 measured 3 to 5% slower, their registers
-// leaving two wavefronts per SIMD in the backward) and walks `rows` steps with the
+// bound by HBM.  A thread owns four consecutive channels (one in pieces of fewer;
+// eight in bf16 measured 3 to 5% slower, their registers leaving two wavefronts per
+// SIMD in the backward) and walks `rows` steps with the
 // last W-1 inputs in registers, so every input row is read once but for the W-1
 // rows ahead of each walk; a wavefront's accesses are one contiguous run.
 //
@@ -31,20 +31,37 @@ struct ConvArgs {
     int64_t end0, end1;      // first channels of the second and third piece
     int64_t pw[3];
     int64_t rows;            // steps of one wavefront's walk
+    unsigned across, first1, first2;   // threads across the channels, the first of the second and third piece
     unsigned cblocks, tblocks;
 };
 
-template <typename T, int V> struct Row {   // V elements of a row, as stored
+// V consecutive elements of a row as stored.  Rows need no alignment beyond an
+// element's: the hardware takes wide accesses anywhere.
+template <typename T, int V> struct Row {
     T v[V];
 };
-template <> struct Row<u16, 4> { uint2 v; };
-template <> struct Row<float, 4> { float4 v; };
+template <typename T> struct Wide;
+template <> struct Wide<u16> { typedef u16 type __attribute__((ext_vector_type(4), aligned(2))); };
+template <> struct Wide<float> { typedef float type __attribute__((ext_vector_type(4), aligned(4))); };
 
 template <typename T, int V> __device__ __forceinline__ Row<T, V> load_row(const T* p) {
     Row<T, V> r;
-    if constexpr (V == 1) r.v[0] = *p;
-    else r.v = *reinterpret_cast<const decltype(r.v)*>(p);
+    if constexpr (V == 1) {
+        r.v[0] = *p;
+    } else {
+        const typename Wide<T>::type q = *reinterpret_cast<const typename Wide<T>::type*>(p);
+        __builtin_memcpy(&r, &q, sizeof(r));
+    }
     return r;
+}
+template <typename T, int V> __device__ __forceinline__ void store_raw(T* p, const Row<T, V>& r) {
+    if constexpr (V == 1) {
+        *p = r.v[0];
+    } else {
+        typename Wide<T>::type q;
+        __builtin_memcpy(&q, &r, sizeof(q));
+        *reinterpret_cast<typename Wide<T>::type*>(p) = q;
+    }
 }
 template <typename T, int V> __device__ __forceinline__ Row<T, V> zero_row() {
     Row<T, V> r;
@@ -52,64 +69,38 @@ template <typename T, int V> __device__ __forceinline__ Row<T, V> zero_row() {
     return r;
 }
 template <int V> __device__ __forceinline__ void widen(const Row<float, V>& r, float* f) {
-    if constexpr (V == 1) f[0] = r.v[0];
-    else { f[0] = r.v.x; f[1] = r.v.y; f[2] = r.v.z; f[3] = r.v.w; }
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = r.v[i];
 }
 template <int V> __device__ __forceinline__ void widen(const Row<u16, V>& r, float* f) {
-    if constexpr (V == 1) {
-        f[0] = bf_bits_to_f32(r.v[0]);
-    } else {
-        uint32_t w[V / 2];
-        __builtin_memcpy(w, &r, sizeof(w));
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
+    for (int i = 0; i < V; ++i) f[i] = bf_bits_to_f32(r.v[i]);
 }
 template <int V> __device__ __forceinline__ void store_row(float* p, const float* f) {
-    if constexpr (V == 1) *p = f[0];
-    else *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    Row<float, V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = f[i];
+    store_raw<float, V>(p, r);
 }
 template <int V> __device__ __forceinline__ void store_row(u16* p, const float* f) {
-    if constexpr (V == 1) {
-        *p = f32_to_bf_bits(f[0]);
-    } else {
-        Row<u16, V> r;
-        uint32_t w[V / 2];
+    Row<u16, V> r;
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i)
-            w[i] = (uint32_t)f32_to_bf_bits(f[2 * i]) | ((uint32_t)f32_to_bf_bits(f[2 * i + 1]) << 16);
-        __builtin_memcpy(&r, w, sizeof(w));
-        *reinterpret_cast<decltype(r.v)*>(p) = r.v;
-    }
-}
-template <typename T, int V> __device__ __forceinline__ void store_raw(T* p, const Row<T, V>& r) {
-    if constexpr (V == 1) *p = r.v[0];
-    else *reinterpret_cast<decltype(r.v)*>(p) = r.v;
+    for (int i = 0; i < V; ++i) r.v[i] = f32_to_bf_bits(f[i]);
+    store_raw<u16, V>(p, r);
 }
 
-// V * W consecutive filter taps and V biases (16-byte aligned when V > 1)
+// V * W consecutive filter taps and V biases
 template <int V, int W>
 __device__ __forceinline__ void load_filter(const float* __restrict__ weight, const float* __restrict__ bias,
                                             int64_t c, float (&w)[V][W], float (&bs)[V]) {
     float* wf = &w[0][0];
-    if constexpr (V == 1) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) wf[k] = weight[c * W + k];
-        bs[0] = bias ? bias[c] : 0.f;
+    for (int i = 0; i < V * W; i += V) widen<V>(load_row<float, V>(weight + c * W + i), wf + i);
+    if (bias) {
+        widen<V>(load_row<float, V>(bias + c), bs);
     } else {
 #pragma unroll
-        for (int i = 0; i < V * W / 4; ++i) {
-            const float4 q = reinterpret_cast<const float4*>(weight + c * W)[i];
-            wf[4 * i] = q.x; wf[4 * i + 1] = q.y; wf[4 * i + 2] = q.z; wf[4 * i + 3] = q.w;
-        }
-#pragma unroll
-        for (int i = 0; i < V / 4; ++i) {
-            const float4 q = bias ? reinterpret_cast<const float4*>(bias + c)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-            bs[4 * i] = q.x; bs[4 * i + 1] = q.y; bs[4 * i + 2] = q.z; bs[4 * i + 3] = q.w;
-        }
+        for (int i = 0; i < V; ++i) bs[i] = 0.f;
     }
 }
 
@@ -117,15 +108,24 @@ __device__ __forceinline__ float sigmoid(float v) {
     return __builtin_amdgcn_rcpf(1.f + fast_exp2(-kLog2e * v));
 }
 
-// the piece that holds channel c, its row width and c's place in it
 template <typename P> struct Pieces { P p[3]; };
-template <typename P>
-__device__ __forceinline__ P piece_of(const ConvArgs& a, const Pieces<P>& y, int64_t c, int64_t* width, int64_t* at) {
-    const bool p1 = c >= a.end0, p2 = c >= a.end1;
-    *width = p2 ? a.pw[2] : p1 ? a.pw[1] : a.pw[0];
-    *at = c - (p2 ? a.end1 : p1 ? a.end0 : 0);
-    return p2 ? y.p[2] : p1 ? y.p[1] : y.p[0];
-}
+
+// The V channels of thread t across: c of all, pc of their piece, which is pw wide.
+// The last thread of a piece whose width V does not divide starts earlier and repeats
+// some of its neighbour's channels, with the same results.
+template <int V, typename P> struct Cut {
+    int64_t c, pc, pw, left;   // left: channels from where the thread would have started
+    P p;
+    __device__ __forceinline__ Cut(const ConvArgs& a, const Pieces<P>& y, unsigned t) {
+        const bool p1 = t >= a.first1, p2 = t >= a.first2;
+        pw = p2 ? a.pw[2] : p1 ? a.pw[1] : a.pw[0];
+        p = p2 ? y.p[2] : p1 ? y.p[1] : y.p[0];
+        pc = (int64_t)(t - (p2 ? a.first2 : p1 ? a.first1 : 0)) * V;
+        left = pw - pc;
+        if (left < V) pc = pw - V;
+        c = pc + (p2 ? a.end1 : p1 ? a.end0 : 0);
+    }
+};
 
 __device__ __forceinline__ int64_t length_of(const int32_t* lens, int64_t b, int64_t L) {
     if (!lens) return L;
@@ -158,17 +158,17 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_fwd(ConvArgs a, const T* _
     constexpr int U = 8;   // rows in flight
     const unsigned cb = blockIdx.x % a.cblocks, tb = blockIdx.x / a.cblocks;
     const int64_t b = blockIdx.y;
-    const int64_t c = ((int64_t)cb * 64 + (threadIdx.x & 63)) * V;
+    const unsigned across = cb * 64 + (threadIdx.x & 63);
     const int64_t t0 = ((int64_t)tb * kWaves + (threadIdx.x >> 6)) * a.rows;
-    if (c >= a.C || (t0 >= a.L && t0 > 0)) return;
+    if (across >= a.across || (t0 >= a.L && t0 > 0)) return;
+    const Cut<V, T*> cut(a, y, across);
+    const int64_t c = cut.c, pw = cut.pw;
     const int64_t t1 = t0 + a.rows < a.L ? t0 + a.rows : a.L;
     const int64_t n = length_of(lens, b, a.L);
     const int64_t te = t1 < n ? t1 : n;      // steps t0 .. te are computed, te .. t1 are zero
     const T* xc = x + b * a.xb + c;
     const T* w0 = win0 ? win0 + b * (W - 1) * a.C + c : nullptr;
-    int64_t pw, pc;
-    T* yp = piece_of(a, y, c, &pw, &pc);
-    yp += b * a.L * pw + pc;
+    T* yp = cut.p + b * a.L * pw + cut.pc;
 
     float w[V][W], bs[V];
     load_filter<V, W>(weight, bias, c, w, bs);
@@ -229,10 +229,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvArgs a, const T* _
     const unsigned cb = blockIdx.x % a.cblocks, tb = blockIdx.x / a.cblocks;
     const int64_t b = blockIdx.y;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = ((int64_t)cb * 64 + lane) * V;
+    const bool on = cb * 64 + lane < a.across;
+    const Cut<V, const T*> cut(a, dy, on ? cb * 64 + lane : a.across - 1);
+    const int64_t c = cut.c, pw = cut.pw;
     const int64_t t0 = ((int64_t)tb * kWaves + wave) * a.rows;
     float dw[V][W] = {}, db[V] = {};
-    if (c < a.C && (t0 < a.L || t0 == 0)) {
+    if (on && (t0 < a.L || t0 == 0)) {
         const int64_t t1 = t0 + a.rows < a.L ? t0 + a.rows : a.L;
         const int64_t n = length_of(lens, b, a.L);
         const T* xc = x + b * a.xb + c;
@@ -240,9 +242,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvArgs a, const T* _
         const T* g1 = dwin1 ? dwin1 + b * (W - 1) * a.C + c : nullptr;
         T* g0 = dwin0 ? dwin0 + b * (W - 1) * a.C + c : nullptr;
         T* dxc = dx + b * a.L * a.C + c;
-        int64_t pw, pc;
-        const T* dyp = piece_of(a, dy, c, &pw, &pc);
-        dyp += b * a.L * pw + pc;
+        const T* dyp = cut.p + b * a.L * pw + cut.pc;
 
         float w[V][W], bs[V];
         load_filter<V, W>(weight, bias, c, w, bs);
@@ -320,7 +320,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvArgs a, const T* _
         }
     }
     __syncthreads();
-    if (wave == 0 && c < a.C) {
+    if (wave == 0 && on) {
         float* out = parts + ((int64_t)b * a.tblocks + tb) * (W + 1) * a.C + c;
 #pragma unroll
         for (int k = 0; k <= W; ++k) {
@@ -367,18 +367,13 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_sum(const float* __restric
 }
 
 template <typename T, int V, int W, bool SILU>
-__global__ __launch_bounds__(256) void k_conv_step(ConvArgs a, T* __restrict__ window, const T* __restrict__ x,
-                                                   const float* __restrict__ weight, const float* __restrict__ bias,
-                                                   Pieces<T*> y, int64_t items)
+__device__ __forceinline__ void conv_step(const ConvArgs& a, T* wp, const T* xp, const float* __restrict__ weight,
+                                          const float* __restrict__ bias, int64_t c, T* yp)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, cv = a.C / V;
-    if (i >= items) return;
-    const int64_t b = i / cv, c = (i - b * cv) * V;
-    T* wp = window + b * (W - 1) * a.C + c;
     Row<T, V> in[W];
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) in[k] = load_row<T, V>(wp + k * a.C);
-    in[W - 1] = load_row<T, V>(x + b * a.xb + c);
+    in[W - 1] = load_row<T, V>(xp);
     float w[V][W], o[V];
     load_filter<V, W>(weight, bias, c, w, o);
 #pragma unroll
@@ -392,11 +387,29 @@ __global__ __launch_bounds__(256) void k_conv_step(ConvArgs a, T* __restrict__ w
 #pragma unroll
         for (int v = 0; v < V; ++v) o[v] *= sigmoid(o[v]);
     }
-    int64_t pw, pc;
-    T* yp = piece_of(a, y, c, &pw, &pc);
-    store_row<V>(yp + b * pw + pc, o);
+    store_row<V>(yp, o);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) store_raw<T, V>(wp + k * a.C, in[k + 1]);
+}
+
+template <typename T, int V, int W, bool SILU>
+__global__ __launch_bounds__(256) void k_conv_step(ConvArgs a, T* __restrict__ window, const T* __restrict__ x,
+                                                   const float* __restrict__ weight, const float* __restrict__ bias,
+                                                   Pieces<T*> y, int64_t items)
+{
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= items) return;
+    const int64_t b = i / a.across;
+    const Cut<V, T*> cut(a, y, (unsigned)(i - b * a.across));
+    T* wp = window + b * (W - 1) * a.C;
+    const T* xp = x + b * a.xb;
+    T* yp = cut.p + b * cut.pw;
+    if (cut.left >= V) {
+        conv_step<T, V, W, SILU>(a, wp + cut.c, xp + cut.c, weight, bias, cut.c, yp + cut.pc);
+    } else {   // in place: no channel may be shifted twice
+        for (int64_t k = V - cut.left; k < V; ++k)
+            conv_step<T, 1, W, SILU>(a, wp + cut.c + k, xp + cut.c + k, weight, bias, cut.c + k, yp + cut.pc + k);
+    }
 }
 
 ConvArgs args_of(const ConvShape& s, int vec, int64_t rows) {
@@ -406,7 +419,11 @@ ConvArgs args_of(const ConvShape& s, int vec, int64_t rows) {
     a.end1 = s.piece[2] ? s.piece[0] + s.piece[1] : s.C;
     for (int i = 0; i < 3; ++i) a.pw[i] = s.piece[i];
     a.rows = rows;
-    a.cblocks = (unsigned)((s.C + 64 * vec - 1) / (64 * vec));
+    const auto threads = [&](int i) { return (unsigned)((s.piece[i] + vec - 1) / vec); };
+    a.first1 = threads(0);
+    a.first2 = a.first1 + threads(1);
+    a.across = a.first2 + threads(2);
+    a.cblocks = (a.across + 63) / 64;
     a.tblocks = (unsigned)conv_time_blocks(s, rows);
     return a;
 }
@@ -477,7 +494,7 @@ struct StepCall {
     void* const* y;
     hipStream_t st;
     template <typename T, int V, int W, bool SILU> hipError_t go() {
-        const int64_t items = s.Bz * (s.C / V);
+        const int64_t items = s.Bz * a.across;
         hipLaunchKernelGGL((k_conv_step<T, V, W, SILU>), dim3((unsigned)((items + 255) / 256)), dim3(256), 0, st, a,
                            (T*)window, (const T*)x, weight, bias, (pieces_of<T*>(s, y)), items);
         return hipGetLastError();
@@ -486,24 +503,10 @@ struct StepCall {
 
 }  // namespace
 
-int conv_vec(const ConvShape& s, const void* x, const void* window, const void* const* y, const void* dx,
-             const void* params, const void* params2)
-{
-    constexpr int vec = 4;
-    const uintptr_t bytes = s.bf16 ? 8 : 16;
-    auto wide = [&](const void* p) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
-    bool ok = wide(x) && wide(window) && wide(dx) && reinterpret_cast<uintptr_t>(params) % 16 == 0 &&
-              reinterpret_cast<uintptr_t>(params2) % 16 == 0 && s.C % vec == 0 &&
-              s.xr % vec == 0 && s.xb % vec == 0;
-    for (int i = 0; i < 3; ++i)
-        if (s.piece[i]) ok = ok && s.piece[i] % vec == 0 && wide(y[i]);
-    return ok ? vec : 1;
-}
-
 hipError_t launch_conv_fwd(const ConvShape& s, const void* x, const float* weight, const float* bias,
                            const void* win0, const int32_t* lens, void* const* y, void* win1, hipStream_t st)
 {
-    const int vec = conv_vec(s, x, win0, y, win1, weight, bias);
+    const int vec = conv_vec(s);
     return by_type(s, vec, FwdCall{s, args_of(s, vec, conv_rows(s, false)), x, weight, bias, win0, lens, y, win1, st});
 }
 
@@ -511,9 +514,7 @@ hipError_t launch_conv_bwd(const ConvShape& s, const void* x, const float* weigh
                            const void* win0, const int32_t* lens, const void* const* dy, const void* dwin1,
                            void* dx, float* dweight, float* dbias, void* dwin0, float* parts, hipStream_t st)
 {
-    int vec = conv_vec(s, x, win0, dy, dx, weight, bias);
-    const uintptr_t rest = reinterpret_cast<uintptr_t>(dwin0) | reinterpret_cast<uintptr_t>(dwin1);
-    if (rest % (s.bf16 ? 8 : 16) != 0) vec = 1;
+    const int vec = conv_vec(s);
     hipError_t e = by_type(s, vec, BwdCall{s, args_of(s, vec, conv_rows(s, true)), x, weight, bias, win0, lens,
                                            dy, dwin1, dx, dwin0, parts, st});
     if (e != hipSuccess) return e;
@@ -526,7 +527,7 @@ hipError_t launch_conv_bwd(const ConvShape& s, const void* x, const float* weigh
 hipError_t launch_conv_step(const ConvShape& s, void* window, const void* x, const float* weight,
                             const float* bias, void* const* y, hipStream_t st)
 {
-    const int vec = conv_vec(s, x, window, y, nullptr, weight, bias);
+    const int vec = conv_vec(s);
     return by_type(s, vec, StepCall{s, args_of(s, vec, 1), window, x, weight, bias, y, st});
 }
 

@@ -18,6 +18,7 @@ struct ConvShape {
 // Steps one wavefront walks; a workgroup is kConvWaves wavefronts consecutive
 // in time (shapes.cpp).
 constexpr int kConvWaves = 4;
+int conv_vec(const ConvShape& s);   // channels of a thread: 4, or 1 where a piece has fewer
 int64_t conv_rows(const ConvShape& s, bool bwd);
 int64_t conv_time_blocks(const ConvShape& s, int64_t rows);   // workgroups along a sequence, at least 1
 // The backward's parts of dweight and dbias: [Bz * time blocks][W + 1][C]

@@ -38,6 +38,11 @@ int64_t cb_tiles_bytes(const FwdShape& s) {
     return s.Bz * s.nc * s.G * (nI * (nI + 1) / 2) * 1024 * 4;
 }
 
+int conv_vec(const ConvShape& s) {
+    for (const int64_t w : s.piece)
+        if (w > 0 && w < 4) return 1;
+    return 4;
+}
 // The longest walk that leaves enough wavefronts: short walks read their filters
 // and the rows ahead of them more often (the backward also redoes W-1 steps and
 // writes more parts of dweight), long ones are too few to hide latency.  On MI355X,
@@ -45,7 +50,7 @@ int64_t cb_tiles_bytes(const FwdShape& s) {
 // 143 and 148 us, 1 x 1024 x 1792 at 4, 16 and 64 5.1, 6.3 and 15 us; backward 4 x
 // 2048 x 5376 136, 81 and 73 us, 4 x 2048 x 1792 at 8, 32 and 64 39, 33 and 47 us.
 int64_t conv_rows(const ConvShape& s, bool bwd) {
-    const int64_t wide = s.C % 4 == 0 ? 256 : 64, across = s.Bz * ((s.C + wide - 1) / wide);
+    const int64_t wide = 64 * conv_vec(s), across = s.Bz * ((s.C + wide - 1) / wide);
     int64_t rows = bwd ? 64 : 16;
     while (rows > 4 && across * ((s.L + rows - 1) / rows) < (bwd ? 1700 : 1024)) rows /= 2;
     return rows;

@@ -164,14 +164,13 @@ def short_conv_fwd(x, weight, bias=None, initial_window=None, seqlens=None, silu
     return back, final_window
 
 
-def short_conv_bwd_workspace_bytes(x, weight) -> int:
-    return _conv_bwd_bytes(_conv_check(x, weight, None, True, None, 2)[0])
+def short_conv_bwd_workspace_bytes(x, weight, pieces=None) -> int:
+    return _conv_bwd_bytes(_conv_check(x, weight, None, True, pieces, 2)[0])
 
 
 def _conv_bwd_bytes(d):
-    C = d.channels
-    return _bytes("ssd_short_conv_bwd_workspace_bytes", _lib.ConvDesc, d.batch, d.seqlen, C, d.width, 0, 0,
-                  (C, 0, 0), 1, d.dtype, 1, 0)
+    return _bytes("ssd_short_conv_bwd_workspace_bytes", _lib.ConvDesc, d.batch, d.seqlen, d.channels, d.width, 0, 0,
+                  tuple(d.piece), d.npieces, d.dtype, 1, 0)
 
 
 def short_conv_bwd(x, weight, dy, bias=None, initial_window=None, dfinal_window=None, seqlens=None, silu=True,

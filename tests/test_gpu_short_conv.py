@@ -61,6 +61,8 @@ def both(d, seqlens, silu, pieces, dtype):
     (2, 65, 7, 4, 0, None, [65, 64], True, True, True),     # odd: one channel at a time
     (2, 70, 136, 4, 5, (131, 5), None, True, True, True),   # pieces and rows at odd places
     (1, 5, 1, 3, 0, None, None, True, True, False),
+    (3, 40, 24, 4, 1, (17, 3, 4), [40, 0, 9], True, True, True),    # a piece narrower than a thread's channels
+    (2, 400, 1031, 4, 3, (1021, 5, 5), None, True, True, True),     # ends of pieces inside a thread's channels
     (1, 2100, 64, 4, 0, None, None, True, True, True),
     (3, 0, 16, 4, 0, None, None, True, True, True),         # no steps at all: the windows go through
 ])
@@ -96,7 +98,7 @@ def test_rows_behind_the_end_are_not_read(dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("C,W,wide,pieces", [(64, 4, 16, (32, 16, 16)), (24, 3, 0, None), (13, 2, 3, (10, 3)),
-                                             (2048, 4, 0, None)])
+                                             (2048, 4, 0, None), (27, 4, 1, (9, 7, 11)), (5, 4, 0, None)])
 def test_steps_continue_a_prompt(dtype, C, W, wide, pieces):
     # a prompt, then single tokens from its final window: the bits of one longer prompt
     log("short conv steps %s" % ((dtype, C, W, wide, pieces),))
@@ -194,8 +196,7 @@ def test_no_sequences():
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("shift", [1, 2, 3, 4])
 def test_any_alignment(dtype, shift):
-    # every tensor `shift` elements into its buffer: wide accesses where the
-    # addresses allow them, single elements elsewhere, the same values
+    # every tensor `shift` elements into its buffer: the same values
     log("short conv alignment %s %d" % (dtype, shift))
     d = inputs(2, 21, 16, 4, dtype, seed=shift)
     move = lambda t: torch.cat([t.new_zeros(shift), t.flatten()])[shift:].view(t.shape)
