@@ -11,7 +11,7 @@ struct ChanArgs {
     uint32_t ur, dr, zr, Br, Cr;           // step strides in bytes
     int64_t seg, nseg;
     int N, per, tpg;          // states; channels of a group and its workgroups
-    int softplus, wide;
+    int softplus;
     void* y;
     float *hfin, *S, *sumdt;
 };
@@ -38,17 +38,18 @@ __device__ __forceinline__ void store_at(RowOut row, uint32_t off, float v, u16)
     *reinterpret_cast<__attribute__((address_space(1))) u16*>(row + off) = f32_to_bf_bits(v);
 }
 
-// four consecutive elements of a row (16 bytes of fp32, 8 of bf16)
+// four consecutive elements of a row, at any element's alignment
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef u16 u16x4_any __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ void load_quad(const float* p, float (&f)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    const f32x4_any v = *reinterpret_cast<const f32x4_any*>(p);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = v[k];
 }
 __device__ __forceinline__ void load_quad(const u16* p, float (&f)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    f[0] = __uint_as_float(v.x << 16);
-    f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16);
-    f[3] = __uint_as_float(v.y & 0xffff0000u);
+    const u16x4_any v = *reinterpret_cast<const u16x4_any*>(p);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[k] = bf_bits_to_f32(v[k]);
 }
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(u16 v) { return bf_bits_to_f32(v); }
