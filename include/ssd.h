@@ -320,7 +320,10 @@ ssd_status ssd_short_conv_step(const ssd_conv_desc* desc, void* window, const vo
  *   y, dy            [batch][seqlen][channels] dense
  * dstate is 1 to 64.  u, delta, gate, B, C, y and the gradients need the
  * alignment of an element.  Outputs must not overlap inputs, each other or
- * the workspace. */
+ * the workspace.  Values are not inspected; NaN and infinities stay within
+ * their channel (and the sums over channels dB and dC).  Sequences may be
+ * evaluated in segments joined through e^{A sum dt}: with growing states
+ * (dt A > 0) results overflow where that factor does. */
 typedef struct ssd_channel_desc {
     int64_t batch, seqlen, channels, dstate, ngroups;
     int64_t u_bstride, u_rstride, delta_bstride, delta_rstride, gate_bstride, gate_rstride;

@@ -133,10 +133,11 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
 #pragma unroll
         for (int k = 0; k < TP; ++k) {
             const int s = part + k * NPART;
+            const bool on = t + s < te;   // a step past the end changes nothing, whatever it repeats
             const float x = as_f32(rd[P][k]) + bias, sp = softplus_of<EXACT>(x);
             float dt = a.softplus ? sp : x;
-            dt = t + s < te ? dt : 0.f;   // a step past the end changes nothing
-            u[k] = as_f32(ru[P][k]);
+            dt = on ? dt : 0.f;
+            u[k] = on ? as_f32(ru[P][k]) : 0.f;
             z[k] = as_f32(rz[P][k]);
             sdt += dt;
             lds.dt[P][s][c] = make_float2(dt, dt * u[k]);
@@ -144,7 +145,8 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             const int i = e * 256 + tid;
-            if (NBC % 256 == 0 || i < NBC) lds.bc[P][i] = (i & (NP - 1)) < a.N ? as_f32(rbc[P][e]) : 0.f;
+            const bool in = (i & (NP - 1)) < a.N && t + (i / NP & (TB - 1)) < te;
+            if (NBC % 256 == 0 || i < NBC) lds.bc[P][i] = in ? as_f32(rbc[P][e]) : 0.f;
         }
     };
     // The batch at t, whose values lie in slot P; the inputs of the one after the

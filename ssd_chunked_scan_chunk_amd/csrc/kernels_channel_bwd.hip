@@ -220,7 +220,7 @@ __global__ __launch_bounds__(256) void k_chan_states(BwdArgs a)
             const float x = as_f32(rd[Q][k]) + bias, sp = softplus_of<EXACT>(x);
             float dt = f.softplus ? sp : x;
             dt = on ? dt : 0.f;
-            s_dt[Q][s][c] = make_float2(dt, dt * as_f32(ru[Q][k]));
+            s_dt[Q][s][c] = make_float2(dt, on ? dt * as_f32(ru[Q][k]) : 0.f);
             if (SEGS) {
                 const float z = as_f32(rz[Q][k]), sz = z * sigmoid_of(z);
                 const float d = as_f32(rg[Q][k]) * (gated ? sz : 1.f);
@@ -230,7 +230,8 @@ __global__ __launch_bounds__(256) void k_chan_states(BwdArgs a)
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             const int i = e * 256 + tid;
-            if (NBC % 256 == 0 || i < NBC) s_bc[Q][i] = (i & (NP - 1)) < f.N ? as_f32(rbc[Q][e]) : 0.f;
+            const bool in = (i & (NP - 1)) < f.N && t + (i / NP & (TB - 1)) < te;
+            if (NBC % 256 == 0 || i < NBC) s_bc[Q][i] = in ? as_f32(rbc[Q][e]) : 0.f;
         }
     };
     int64_t at = (b * f.nseg + seg) * a.nb * a.tiles + tile;   // (batch, tile)
@@ -416,7 +417,8 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             const int i = e * 256 + tid;
-            if (NBC % 256 == 0 || i < NBC) s_bc[i] = (i & (NP - 1)) < f.N ? as_f32(rbc[e]) : 0.f;
+            const bool in = (i & (NP - 1)) < f.N && j * TB + (i / NP & (TB - 1)) < te;
+            if (NBC % 256 == 0 || i < NBC) s_bc[i] = in ? as_f32(rbc[e]) : 0.f;
         }
         // the state entering the batch
 #pragma unroll

@@ -138,6 +138,28 @@ def test_rows_behind_the_end_are_not_read(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_infinities_and_nans_stay_where_they_are(dtype):
+    # an infinite input in the last step of a partial batch and a NaN in another
+    # channel: the state is infinite (not NaN: the steps the kernel repeats past the end
+    # add nothing), the other channels and sequences are untouched
+    log("channel scan infinities %s" % dtype)
+    d = inputs(2, 13, 40, 16, 1, dtype, 14, carry=False)
+    run = lambda: ssd.channel_scan_fwd(**d, softplus=True, seqlens=lens_of([13, 11]), return_final_state=True)
+    y0, h0 = run()
+    d["u"][0, 12, 3] = float("inf")
+    d["u"][1, 10, 5] = float("inf")
+    d["u"][1, 4, 7] = float("nan")
+    y1, h1 = run()
+    torch.cuda.synchronize()
+    assert bool(h1[0, 3].isinf().all()) and bool(h1[1, 5].isinf().all()) and bool(h1[1, 7].isnan().all())
+    assert bool(y1[1, 4:11, 7].isnan().all()) and not y1[1, 11:].any()
+    ok = torch.ones_like(y0, dtype=torch.bool)
+    ok[0, 12, 3] = ok[1, 10, 5] = False
+    ok[1, 4:, 7] = False
+    assert torch.equal(y0[ok], y1[ok])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("Bz,D,N,G,wide,gate,skip,bias,softplus", [
     (1, 1, 1, 1, 0, False, False, False, False), (3, 64, 16, 1, 0, True, True, True, True),
     (2, 35, 12, 5, 3, True, True, True, True), (5, 20, 64, 2, 0, True, False, True, True),
