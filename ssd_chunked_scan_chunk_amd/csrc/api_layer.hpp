@@ -1,6 +1,6 @@
-// api_layer.hpp -- the C ABI of the operators around the chunked scan: the
-// short causal convolution and the per-channel scan.  Included once, at the end of api.cpp, whose error
-// state and range checks it shares.
+// api_layer.hpp -- the C ABI of the operators around the chunked scan: the short
+// causal convolution and the per-channel scan.  Included once, at the end of
+// api.cpp, whose error state and range checks it shares.
 #include "layer_launch.hpp"
 
 namespace {
@@ -74,10 +74,10 @@ ssd_status conv_shape(const ssd_conv_desc* d, ssd::ConvShape* s) {
     s->Bz = d->batch; s->L = d->seqlen; s->C = d->channels; s->W = (int)d->width;
     s->xb = d->x_bstride; s->xr = d->x_rstride;
     s->bf16 = d->dtype == SSD_BF16; s->silu = d->silu == 1;
-    // worst case of one channel per thread
+    // worst case of one channel per thread; the step's threads in workgroups of 256
     const int64_t blocks = ((s->C + 63) / 64) * ssd::conv_time_blocks(*s, ssd::conv_rows(*s, true));
     const int64_t fblocks = ((s->C + 63) / 64) * ssd::conv_time_blocks(*s, ssd::conv_rows(*s, false));
-    if ((blocks > fblocks ? blocks : fblocks) * 256 >= ((int64_t)1 << 32) || s->Bz * s->C >= ((int64_t)1 << 32))
+    if ((blocks > fblocks ? blocks : fblocks) * 256 >= ((int64_t)1 << 32) || s->Bz * s->C > ((int64_t)1 << 32) - 256)
         return fail(SSD_ERR_UNSUPPORTED, "seqlen*channels or batch*channels too large for one launch");
     return SSD_OK;
 }

@@ -101,6 +101,7 @@ def pieces(*p):
     (dict(x_bstride=1 << 62), _lib.SSD_ERR_UNSUPPORTED), (dict(batch=1 << 40), _lib.SSD_ERR_UNSUPPORTED),
     (dict(seqlen=1 << 50), _lib.SSD_ERR_UNSUPPORTED),
     (dict(seqlen=1 << 31, channels=1 << 24, piece=(1 << 24, 0, 0)), _lib.SSD_ERR_UNSUPPORTED),
+    (dict(batch=65535, seqlen=1, channels=65537, piece=(65535, 2, 0), npieces=2), _lib.SSD_ERR_UNSUPPORTED),
 ])
 def test_conv_abi_shapes(lib, kw, code):
     d, n = conv_desc(**kw), ctypes.c_size_t()
