@@ -31,6 +31,10 @@ def _same(name, t, shape, dtype, device):
 def _rows(name, t, shape, dense, dtype, device):
     """Check a tensor of ``shape`` whose last ``dense`` dimensions are dense and
     return the strides of the leading ones."""
+    if t.__class__ is torch.Tensor and t.shape == shape and t.dtype is dtype and t.device == device:
+        strides = t.stride()   # the usual outcome first, as in _same
+        if strides[-1] == 1 and (dense == 1 or shape[-2] == 1 or strides[-2] == shape[-1]):
+            return strides
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s is required" % name)
     if t.shape != shape:
@@ -101,13 +105,14 @@ def _conv_check(x, weight, bias, silu, pieces, lead):
     """(desc, pieces) of a convolution of x [*lead, channels]."""
     if not isinstance(x, torch.Tensor) or x.dim() != lead + 1:
         raise ValueError("x must be a %d-D tensor [batch, %schannels]" % (lead + 1, "seqlen, " if lead == 2 else ""))
-    code, C = _dtype_code(x), x.shape[-1]
-    strides = _rows("x", x, x.shape, 1, x.dtype, x.device)
+    code, shape, dev = _dtype_code(x), x.shape, x.device
+    C = shape[-1]
+    strides = _rows("x", x, shape, 1, x.dtype, dev)
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a 2-D tensor [channels, width]")
     W = weight.shape[1]
-    _same("weight", weight, (C, W), torch.float32, x.device)
-    _same("bias", bias, (C,), torch.float32, x.device)
+    _same("weight", weight, (C, W), torch.float32, dev)
+    _same("bias", bias, (C,), torch.float32, dev)
     if pieces is None:
         given, three = (C,), (C, 0, 0)
     else:
@@ -115,16 +120,15 @@ def _conv_check(x, weight, bias, silu, pieces, lead):
         if not 1 <= len(given) <= 3 or min(given) < 1 or sum(given) != C:
             raise ValueError("pieces must be one to three widths that add up to the %d channels, got %s" % (C, given))
         three = given + (0,) * (3 - len(given))
-    L, xr = (x.shape[1], strides[1]) if lead == 2 else (1, 0)
-    return _lib.ConvDesc(x.shape[0], L, C, W, strides[0], xr, three, len(given), code, 1 if silu else 0, 0), given
+    L, xr = (shape[1], strides[1]) if lead == 2 else (1, 0)
+    return _lib.ConvDesc(shape[0], L, C, W, strides[0], xr, three, len(given), code, 1 if silu else 0, 0), given
 
 
 def _conv_outputs(x, given, pieces, y):
     """The y pieces to write, as a tuple, and what the caller gets back."""
     lead = tuple(x.shape[:-1])
     if y is None:
-        ys = [torch.empty(lead + (w,), dtype=x.dtype, device=x.device) for w in given]
-        ys = tuple(ys)
+        ys = tuple([x.new_empty(lead + (w,)) for w in given])
         return ys, ys[0] if pieces is None else ys
     ys = (y,) if pieces is None else tuple(y)
     _conv_given("y", ys, lead, given, x)
@@ -152,14 +156,14 @@ def short_conv_fwd(x, weight, bias=None, initial_window=None, seqlens=None, silu
     B and C for chunk_scan_fwd, after a view).  Returns (y, final_window or None):
     the window [Bz,W-1,C] continues the sequence here or in short_conv_step."""
     d, given = _conv_check(x, weight, bias, silu, pieces, 2)
-    Bz, C, W = x.shape[0], x.shape[2], weight.shape[1]
-    _same("initial_window", initial_window, (Bz, W - 1, C), x.dtype, x.device)
-    _same("final_window", final_window, (Bz, W - 1, C), x.dtype, x.device)
-    _seqlens(seqlens, Bz, x.device)
+    dev, Bz, window = x.device, d.batch, (d.batch, d.width - 1, d.channels)
+    _same("initial_window", initial_window, window, x.dtype, dev)
+    _same("final_window", final_window, window, x.dtype, dev)
+    _seqlens(seqlens, Bz, dev)
     ys, back = _conv_outputs(x, given, pieces, y)
     if final_window is None and return_final_window:
-        final_window = torch.empty((Bz, max(W - 1, 0), C), dtype=x.dtype, device=x.device)
-    _enqueue(x.device, _L().ssd_short_conv_fwd, d, _at(x), _at(weight), _at(bias), _at(initial_window), _at(seqlens),
+        final_window = x.new_empty(window if d.width > 0 else (Bz, 0, d.channels))
+    _enqueue(dev, _L().ssd_short_conv_fwd, d, _at(x), _at(weight), _at(bias), _at(initial_window), _at(seqlens),
              _P(*map(_at, ys)), _at(final_window))
     return back, final_window
 
@@ -194,10 +198,10 @@ def short_conv_bwd(x, weight, dy, bias=None, initial_window=None, dfinal_window=
     _same("dfinal_window", dfinal_window, (Bz, W - 1, C), x.dtype, x.device)
     _seqlens(seqlens, Bz, x.device)
     workspace, wsz = _workspace(workspace, _conv_bwd_bytes(d), x.device)
-    dx = torch.empty((Bz, L, C), dtype=x.dtype, device=x.device)
+    dx = x.new_empty((Bz, L, C))
     dweight = torch.empty_like(weight)
     dbias = torch.empty_like(bias) if bias is not None else None
-    dwin = torch.empty((Bz, W - 1, C), dtype=x.dtype, device=x.device) if return_dinitial_window else None
+    dwin = x.new_empty((Bz, W - 1, C)) if return_dinitial_window else None
     _enqueue(x.device, _L().ssd_short_conv_bwd, d, _at(x), _at(weight), _at(bias), _at(initial_window), _at(seqlens),
              _P(*map(_at, dys)), _at(dfinal_window), _at(dx), _at(dweight), _at(dbias), _at(dwin), _at(workspace), wsz)
     return {"dx": dx, "dweight": dweight, "dbias": dbias, "dinitial_window": dwin}
@@ -208,9 +212,10 @@ def short_conv_step(window, x, weight, bias=None, silu=True, pieces=None, y=None
     updated in place.  Returns y [Bz,C], or its pieces as a tuple."""
     d, given = _conv_check(x, weight, bias, silu, pieces, 1)
     _need("window", window)
-    _same("window", window, (x.shape[0], weight.shape[1] - 1, x.shape[1]), x.dtype, x.device)
+    dev = x.device
+    _same("window", window, (d.batch, d.width - 1, d.channels), x.dtype, dev)
     ys, back = _conv_outputs(x, given, pieces, y)
-    _enqueue(x.device, _L().ssd_short_conv_step, d, _at(window), _at(x), _at(weight), _at(bias), _P(*map(_at, ys)))
+    _enqueue(dev, _L().ssd_short_conv_step, d, _at(window), _at(x), _at(weight), _at(bias), _P(*map(_at, ys)))
     return back
 
 
@@ -269,9 +274,9 @@ def channel_scan_fwd(u, delta, A, B, C, skip=None, gate=None, delta_bias=None, s
     _same("y", y, u.shape, u.dtype, dev)
     _seqlens(seqlens, u.shape[0], dev)
     if y is None:
-        y = torch.empty(u.shape, dtype=u.dtype, device=dev)
+        y = torch.empty_like(u, memory_format=torch.contiguous_format)
     if final_state is None and return_final_state:
-        final_state = torch.empty(state, dtype=torch.float32, device=dev)
+        final_state = A.new_empty(state)
     workspace, wsz = _workspace(workspace, _chan_bytes("ssd_channel_scan_fwd_workspace_bytes", d), dev)
     _enqueue(dev, _L().ssd_channel_scan_fwd, d, _at(u), _at(delta), _at(A), _at(B), _at(C), _at(skip), _at(gate),
              _at(delta_bias), _at(initial_state), _at(seqlens), _at(y), _at(final_state), _at(workspace), wsz)
@@ -299,11 +304,12 @@ def channel_scan_bwd(u, delta, A, B, C, dy, skip=None, gate=None, delta_bias=Non
     _same("dfinal_state", dfinal_state, state, f32, dev)
     _seqlens(seqlens, u.shape[0], dev)
     workspace, wsz = _workspace(workspace, _chan_bytes("ssd_channel_scan_bwd_workspace_bytes", d), dev)
-    new = lambda like, dtype, wanted: torch.empty(like, dtype=dtype, device=dev) if wanted else None
-    g = {"du": new(u.shape, dt, True), "ddelta": new(u.shape, dt, True), "dgate": new(u.shape, dt, gate is not None),
-         "dB": new(B.shape, dt, True), "dC": new(B.shape, dt, True), "dA": new(A.shape, f32, True),
-         "dskip": new(A.shape[:1], f32, skip is not None), "ddelta_bias": new(A.shape[:1], f32, delta_bias is not None),
-         "dinitial_state": new(state, f32, return_dinitial_state)}
+    rows, cols = u.new_empty, A.new_empty   # in the type of the inputs and of the parameters
+    g = {"du": rows(u.shape), "ddelta": rows(u.shape), "dgate": rows(u.shape) if gate is not None else None,
+         "dB": rows(B.shape), "dC": rows(B.shape), "dA": cols(A.shape),
+         "dskip": cols(A.shape[:1]) if skip is not None else None,
+         "ddelta_bias": cols(A.shape[:1]) if delta_bias is not None else None,
+         "dinitial_state": cols(state) if return_dinitial_state else None}
     _enqueue(dev, _L().ssd_channel_scan_bwd, d, _at(u), _at(delta), _at(A), _at(B), _at(C), _at(skip), _at(gate),
              _at(delta_bias), _at(initial_state), _at(seqlens), _at(dy), _at(dfinal_state),
              _lib.ChannelGrads(*map(_at, g.values())), _at(workspace), wsz)
@@ -318,7 +324,7 @@ def channel_step(state, u, delta, A, B, C, skip=None, gate=None, delta_bias=None
     _same("state", state, (u.shape[0], u.shape[1], A.shape[1]), torch.float32, u.device)
     _same("y", y, u.shape, u.dtype, u.device)
     if y is None:
-        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
+        y = torch.empty_like(u, memory_format=torch.contiguous_format)
     _enqueue(u.device, _L().ssd_channel_step, d, _at(state), _at(u), _at(delta), _at(A), _at(B), _at(C), _at(skip),
              _at(gate), _at(delta_bias), _at(y))
     return y
