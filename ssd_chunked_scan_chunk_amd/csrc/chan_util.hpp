@@ -19,21 +19,22 @@ struct ChanArgs {
 // A row that is the same for the whole wavefront: a base in scalar registers, to
 // which a lane adds its 32-bit byte offset.  The empty asm keeps the offset's
 // extension to 64 bits beside the access, where it is free: hoisted out of a loop
-// it took two vector registers per access and an addition each time.
+// it took two vector registers per access and an addition each time.  It works on
+// the caller's variable: on a copy, every access in a loop costs the move of it.
 typedef __attribute__((address_space(1))) char GlobalByte;
 typedef GlobalByte* RowOut;
 typedef const GlobalByte* RowIn;
 __device__ __forceinline__ RowIn row_in(const void* p, int64_t bytes) { return (RowIn)(uintptr_t)p + bytes; }
 __device__ __forceinline__ RowOut row_out(void* p, int64_t bytes) { return (RowOut)(uintptr_t)p + bytes; }
-template <typename T> __device__ __forceinline__ T load_at(RowIn row, uint32_t off) {
+template <typename T> __device__ __forceinline__ T load_at(RowIn row, uint32_t& off) {
     asm volatile("" : "+v"(off));
     return *reinterpret_cast<const __attribute__((address_space(1))) T*>(row + off);
 }
-__device__ __forceinline__ void store_at(RowOut row, uint32_t off, float v, float) {
+__device__ __forceinline__ void store_at(RowOut row, uint32_t& off, float v, float) {
     asm volatile("" : "+v"(off));
     *reinterpret_cast<__attribute__((address_space(1))) float*>(row + off) = v;
 }
-__device__ __forceinline__ void store_at(RowOut row, uint32_t off, float v, u16) {
+__device__ __forceinline__ void store_at(RowOut row, uint32_t& off, float v, u16) {
     asm volatile("" : "+v"(off));
     *reinterpret_cast<__attribute__((address_space(1))) u16*>(row + off) = f32_to_bf_bits(v);
 }

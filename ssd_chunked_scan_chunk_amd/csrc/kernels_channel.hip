@@ -58,7 +58,7 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
     const bool live = cg < a.per;
     // threads past the group repeat its last channel and store nothing
     const int cl = live ? cg : a.per - 1;
-    const uint32_t col = (uint32_t)cl * ES;
+    uint32_t col = (uint32_t)cl * ES;
     const int64_t gch = (int64_t)g * a.per, ch = gch + cl;
     const int64_t ts = seg * a.seg, t1 = ts + a.seg < a.L ? ts + a.seg : a.L;
     const int64_t len = chan_length(a.in.lens, b, a.L);
@@ -90,7 +90,7 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
     // past `last` repeat that one.
     const int wave64 = __builtin_amdgcn_readfirstlane(tid >> 6) * 64;
     auto in_C = [&](int e) { return FULL && e * 256 + wave64 >= TB * NP; };   // else in B
-    uint32_t ou[TP], od[TP], oz[TP], obc[NE];
+    uint32_t ou[TP], od[TP], oz[TP], oy[TP], obc[NE];
     auto offsets = [&](int last) {
 #pragma unroll
         for (int k = 0; k < TP; ++k) {
@@ -127,7 +127,7 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
         Bp += TB * (uint64_t)a.Br;
         Cp += TB * (uint64_t)a.Cr;
     };
-    float u[TP], z[TP];
+    float u[2][TP], z[2][TP];
     auto prepare = [&](int t, auto slot) {
         constexpr int P = decltype(slot)::value;
 #pragma unroll
@@ -137,10 +137,10 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
             const float x = as_f32(rd[P][k]) + bias, sp = softplus_of<EXACT>(x);
             float dt = a.softplus ? sp : x;
             dt = on ? dt : 0.f;
-            u[k] = on ? as_f32(ru[P][k]) : 0.f;
-            z[k] = as_f32(rz[P][k]);
+            u[P][k] = on ? as_f32(ru[P][k]) : 0.f;
+            z[P][k] = as_f32(rz[P][k]);
             sdt += dt;
-            lds.dt[P][s][c] = make_float2(dt, dt * u[k]);
+            lds.dt[P][s][c] = make_float2(dt, dt * u[P][k]);
         }
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
@@ -168,9 +168,6 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
             }
             if (FULL) lds.y[P][k][part][c] = y;
         }
-        float pu[TP], pz[TP];
-#pragma unroll
-        for (int k = 0; k < TP; ++k) { pu[k] = u[k]; pz[k] = z[k]; }
         if (t + TB < te) prepare(t + TB, Int<P ^ 1>());
         if constexpr (FULL) {
             lds_barrier();
@@ -180,14 +177,16 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
                 float y = 0.f;
 #pragma unroll
                 for (int q = 0; q < NPART; q += 2) y += lds.y[P][s][q][c] + lds.y[P][s][q + 1][c];
-                y = fmaf(skip, pu[k], y);
-                const float sz = pz[k] * sigmoid_of(pz[k]);
+                y = fmaf(skip, u[P][k], y);
+                const float sz = z[P][k] * sigmoid_of(z[P][k]);
                 y *= gated ? sz : 1.f;
-                if (live && t + s < te) store_at(yp, s * yr + col, y, T());
+                if (live && t + s < te) store_at(yp, oy[k], y, T());
             }
         }
         yp += TB * (uint64_t)yr;
     };
+#pragma unroll
+    for (int k = 0; k < TP; ++k) oy[k] = (part + k * NPART) * yr + col;
     if (te > 0) {
         offsets(TB - 1);
         fetch(Int<0>(), te - 1);

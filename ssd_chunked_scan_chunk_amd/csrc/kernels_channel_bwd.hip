@@ -108,11 +108,11 @@ template <int NV, int W> struct LaneSum {
 };
 
 // a lane's NR consecutive floats
-template <int NR> __device__ __forceinline__ void load_states(RowIn row, uint32_t off, float (&v)[NR]) {
+template <int NR> __device__ __forceinline__ void load_states(RowIn row, uint32_t& off, float (&v)[NR]) {
     typedef float vec __attribute__((ext_vector_type(NR < 4 ? NR : 4)));
 #pragma unroll
     for (int i = 0; i < NR; i += 4) {
-        const vec q = load_at<vec>(row, off + i * 4);
+        const vec q = load_at<vec>(row + i * 4, off);
 #pragma unroll
         for (int k = 0; k < 4 && k < NR; ++k) v[i + k] = q[k];
     }
@@ -339,7 +339,7 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
     // threads past the group repeat its last channel, store nothing and add nothing
     // to sums over channels
     const int cl = live ? cg : f.per - 1;
-    const uint32_t col = (uint32_t)cl * ES;
+    uint32_t col = (uint32_t)cl * ES;
     const int64_t gch = (int64_t)g * f.per, ch = gch + cl, b = blockIdx.z, seg = blockIdx.y;
     const int64_t ts = seg * f.seg, t1 = ts + f.seg < f.L ? ts + f.seg : f.L;
     const int64_t len = chan_length(f.in.lens, b, f.L);
@@ -370,30 +370,43 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
     // The share of batch j of this thread, as in the forward: the steps part + k
     // NPART of channel c, elements e 256 + tid of B and C.  Steps past `last` (in the
     // last batch of a segment only) repeat that one.
-    T ru[TP], rd[TP], rz[TP], rg[TP], rbc[NE];
-    float rck[NR], rcdt = 0.f;
-    auto fetch = [&](int j, int last) {
-        const uint64_t t = (uint64_t)j * TB;
-        const RowIn ut = up + t * f.ur, dt = dp + t * f.dr, zt = zp + t * f.zr, gt = gp + t * yr;
+    auto in_C = [&](int e) { return e * 256 + wave64 >= TB * NP; };   // else in B
+    uint32_t ou[TP], od[TP], oz[TP], oy[TP], obc[NE], ock = tid * NR * 4, ocdt = c * 4;
+    auto offsets = [&](int last) {
 #pragma unroll
         for (int k = 0; k < TP; ++k) {
             const int s = part + k * NPART;
             const uint32_t r = s < last ? s : last;
-            ru[k] = load_at<T>(ut, r * f.ur + col);
-            rd[k] = load_at<T>(dt, r * f.dr + col);
-            rz[k] = load_at<T>(zt, r * f.zr + col);
-            rg[k] = load_at<T>(gt, r * yr + col);
+            ou[k] = r * f.ur + col;
+            od[k] = r * f.dr + col;
+            oz[k] = r * f.zr + col;
+            oy[k] = r * yr + col;
         }
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             const int i = e * 256 + tid, s = i / NP & (TB - 1), n = i & (NP - 1);
-            const bool in_C = e * 256 + wave64 >= TB * NP;
-            const uint32_t r = s < last ? s : last, rs = in_C ? f.Cr : f.Br;
-            rbc[e] = load_at<T>((in_C ? Cp : Bp) + t * rs, r * rs + (uint32_t)(n < f.N ? n : f.N - 1) * ES);
+            const uint32_t r = s < last ? s : last;
+            obc[e] = r * (in_C(e) ? f.Cr : f.Br) + (uint32_t)(n < f.N ? n : f.N - 1) * ES;
         }
+    };
+    T ru[TP], rd[TP], rz[TP], rg[TP], rbc[NE];
+    float rck[NR], rcdt = 0.f;
+    auto fetch = [&](int j) {
+        const uint64_t t = (uint64_t)j * TB;
+        const RowIn ut = up + t * f.ur, dt = dp + t * f.dr, zt = zp + t * f.zr, gt = gp + t * yr;
+#pragma unroll
+        for (int k = 0; k < TP; ++k) {
+            ru[k] = load_at<T>(ut, ou[k]);
+            rd[k] = load_at<T>(dt, od[k]);
+            rz[k] = load_at<T>(zt, oz[k]);
+            rg[k] = load_at<T>(gt, oy[k]);
+        }
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+            rbc[e] = load_at<T>((in_C(e) ? Cp : Bp) + t * (in_C(e) ? f.Cr : f.Br), obc[e]);
         const int64_t at = ((b * f.nseg + seg) * a.nb + j) * a.tiles + tile;
-        load_states<NR>(row_in(a.ck, at * 256 * NR * 4), tid * NR * 4, rck);
-        if (SEGS) rcdt = load_at<float>(row_in(a.cdt, at * CW * 4), (uint32_t)c * 4);
+        load_states<NR>(row_in(a.ck, at * 256 * NR * 4), ock, rck);
+        if (SEGS) rcdt = load_at<float>(row_in(a.cdt, at * CW * 4), ocdt);
     };
     // of a pair: u, dt, d, softplus' and dy silu'(gate)
     float u[TP], dtv[TP], d[TP], sx[TP], dz[TP], h[NR], sskip = 0.f, sbias = 0.f;
@@ -427,18 +440,28 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
     };
 
     if (nb > 0) {
-        fetch(nb - 1, te - 1 - (nb - 1) * TB);
+        offsets(te - 1 - (nb - 1) * TB);
+        fetch(nb - 1);
         prepare(nb - 1);
     }
+    offsets(TB - 1);   // of all other batches, and of the outputs
     using Sum = LaneSum<RB * 2 * NR, CW>;
     // the values this lane is left with, vi .. : state (part's n0 +) i of B or C at step k
     const int vi = Sum::index(lane);
-    auto place = [&](int e) {
+    int vk[Sum::kLeft];                // the step of each in its RB
+    uint32_t ov[TB / RB][Sum::kLeft];
+#pragma unroll
+    for (int e = 0; e < Sum::kLeft; ++e) {
         const int m = vi + e, k = m / (2 * NR), which = m / NR & 1, i = m % NR;
-        return make_int2(k, ((k * a.tiles * 2 + which) * NP + n0 + i) * 4);
-    };
+        vk[e] = k;
+#pragma unroll
+        for (int r = 0; r < TB / RB; ++r) ov[r][e] = (uint32_t)((((r * RB + k) * a.tiles * 2 + which) * NP + n0 + i) * 4);
+    }
+    // what was loaded so far has arrived before the loop counts its own loads
+#pragma unroll
+    for (int i = 0; i < NR; ++i) asm volatile("" : "+v"(carry[i]), "+v"(hin[i]));
     for (int j = nb - 1; j >= 0; --j) {
-        if (j > 0) fetch(j - 1, TB - 1);
+        if (j > 0) fetch(j - 1);
         lds_barrier();
         // forward: states and decays of the batch
         float H[TB][NR], E[TB][NR], hfirst[NR];
@@ -492,9 +515,9 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
             Sum::run(v, lane);
 #pragma unroll
             for (int e = 0; e < Sum::kLeft; ++e) {
-                const int2 to = place(e);
+                asm volatile("" : "+v"(v[e]));   // the last addition stays ahead of the branch, in one instruction
                 // lanes that share a value store it more than once, the same bits
-                if (j * TB + k0 + to.x < te) store_at(pbc, (uint32_t)(k0 * a.tiles * 2 * NP) * 4 + to.y, v[e], 0.f);
+                if (j * TB + k0 + vk[e] < te) store_at(pbc, ov[k0 / RB][e], v[e], 0.f);
             }
         }
         lds_barrier();
@@ -511,13 +534,12 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
             }
             // A2 = A log2(e)
             const float dd = fmaf(fed, u[k], ma * 0.69314718f) * sx[k];
-            const uint32_t at = s * yr + col;
             if (live && j * TB + s < te) {
                 sskip = fmaf(d[k], u[k], sskip);
                 sbias += dd;
-                store_at(dup + (uint64_t)j * TB * yr, at, fmaf(fed, dtv[k], skip * d[k]), T());
-                store_at(ddp + (uint64_t)j * TB * yr, at, dd, T());
-                if (gated) store_at(dzp + (uint64_t)j * TB * yr, at, dz[k] * fmaf(skip, u[k], y), T());
+                store_at(dup + (uint64_t)j * TB * yr, oy[k], fmaf(fed, dtv[k], skip * d[k]), T());
+                store_at(ddp + (uint64_t)j * TB * yr, oy[k], dd, T());
+                if (gated) store_at(dzp + (uint64_t)j * TB * yr, oy[k], dz[k] * fmaf(skip, u[k], y), T());
             }
         }
         if (j > 0) prepare(j - 1);
