@@ -54,46 +54,86 @@ struct BwdArgs {
 };
 
 // A wavefront's reduction of NV values over W neighbouring lanes (64 or 32): lane l
-// is left with values index(l) .. of sum over the lanes.  Each level pairs
-// lanes, which hand over one half of their values each.
+// is left with values index(l) .. of sum over the lanes.  Each level pairs lanes,
+// which hand over one half of their values each.  Levels in the order of their cost
+// per pair of values: 8 and 4 lanes apart two instructions (an addition with the
+// partner by DPP for the one value in all lanes, for the other in those that keep it),
+// 32 and 16 apart an exchange, which takes two issue slots, and an addition, then
+// 2 and 1 apart, inside the quads that masks do not divide, two selections and an
+// addition.
 template <int CTRL> __device__ __forceinline__ float dpp(float v) {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
 }
+// d + (d of the partner) in the lanes whose bit D is clear, s + (s of the partner) in
+// the others.  A DPP operand may not be read within two slots of its write, which the
+// compiler sees to around its own instructions only, hence the s_nop on both sides.
+#define SSD_ADD_8(d, s)                                                      \
+    "v_add_f32_dpp " d ", " d ", " d " row_ror:8 row_mask:0xf bank_mask:0x3\n\t" \
+    "v_add_f32_dpp " d ", " s ", " s " row_ror:8 row_mask:0xf bank_mask:0xc\n\t"
+#define SSD_ADD_4(d, s)                                                            \
+    "v_add_f32_dpp " d ", " d ", " d " row_half_mirror row_mask:0xf bank_mask:0x5\n\t" \
+    "v_add_f32_dpp " d ", " s ", " s " row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+#define SSD_ADD_PAIRS(ADD)                                                                               \
+    if constexpr (K % 4 == 0) {                                                                          \
+        _Pragma("unroll") for (int j = 0; j < K; j += 4)                                                 \
+            asm("s_nop 1\n\t" ADD("%0", "%4") ADD("%1", "%5") ADD("%2", "%6") ADD("%3", "%7") "s_nop 1"  \
+                : "+&v"(d[j]), "+&v"(d[j + 1]), "+&v"(d[j + 2]), "+&v"(d[j + 3])                          \
+                : "v"(s[j]), "v"(s[j + 1]), "v"(s[j + 2]), "v"(s[j + 3]));                               \
+    } else {                                                                                             \
+        _Pragma("unroll") for (int j = 0; j < K; ++j)                                                    \
+            asm("s_nop 1\n\t" ADD("%0", "%1") "s_nop 1" : "+&v"(d[j]) : "v"(s[j]));                      \
+    }
+template <int D, int K> __device__ __forceinline__ void add_partners(float* d, const float* s) {
+    if constexpr (D == 8) {
+        SSD_ADD_PAIRS(SSD_ADD_8)
+    } else {
+        SSD_ADD_PAIRS(SSD_ADD_4)
+    }
+}
+#undef SSD_ADD_PAIRS
+#undef SSD_ADD_4
+#undef SSD_ADD_8
+
 template <int NV, int W> struct LaneSum {
     static constexpr int kLeft = NV > W ? NV / W : 1;
+    static constexpr int after(int D) { return D == 8 ? 4 : D == 4 ? W / 2 : D == 32 ? 16 : D == 16 ? 2 : D / 2; }
     // first value of lane l; lanes that share one (NV < W) hold the same sum
     __device__ static int index(int l) {
         int at = 0, m = NV;
 #pragma unroll
-        for (int d = W / 2; d >= 1; d >>= 1)
+        for (int d = 8; d >= 1; d = after(d))
             if (m > 1) {
                 m /= 2;
                 if (l & d) at += m;
             }
         return at;
     }
+    template <int D> __device__ static float exchanged(float a, float b) {
+        const unsigned x = __float_as_uint(a), y = __float_as_uint(b);
+        const auto r = D == 32 ? __builtin_amdgcn_permlane32_swap(x, y, false, false)
+                               : __builtin_amdgcn_permlane16_swap(x, y, false, false);
+        return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
     template <int D, int M> __device__ static void level(float (&v)[NV], int l) {
         if constexpr (D >= 1) {
-            if constexpr (M > 1) {
+            constexpr int K = M > 1 ? M / 2 : 1;
+            if constexpr (M > 1 && (D == 8 || D == 4)) {
+                add_partners<D, K>(v, v + K);
+            } else {
 #pragma unroll
-                for (int j = 0; j < M / 2; ++j) {
-                    const float a = v[j], b = v[j + M / 2];
+                for (int j = 0; j < K; ++j) {
+                    const float a = v[j], b = v[M > 1 ? j + K : j];
                     if constexpr (D >= 16) {
-                        const unsigned x = __float_as_uint(a), y = __float_as_uint(b);
-                        const auto r = D == 32 ? __builtin_amdgcn_permlane32_swap(x, y, false, false)
-                                               : __builtin_amdgcn_permlane16_swap(x, y, false, false);
-                        v[j] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-                    } else {
+                        v[j] = exchanged<D>(a, b);
+                    } else if constexpr (M > 1) {
                         const float keep = (l & D) ? b : a, give = (l & D) ? a : b;
                         v[j] = keep + across<D>(give);
+                    } else {
+                        v[j] = a + across<D>(a);
                     }
                 }
-                level<D / 2, M / 2>(v, l);
-            } else {
-                if constexpr (D >= 16) v[0] += __shfl_xor(v[0], D, 64);
-                else v[0] += across<D>(v[0]);
-                level<D / 2, 1>(v, l);
             }
+            level<after(D), K>(v, l);
         }
     }
     // the partner's value: row rotation by 8, mirror of 8, quad exchanges (each
@@ -104,7 +144,7 @@ template <int NV, int W> struct LaneSum {
         else if constexpr (D == 2) return dpp<0x4E>(v);
         else return dpp<0xB1>(v);
     }
-    __device__ static void run(float (&v)[NV], int l) { level<W / 2, NV>(v, l); }
+    __device__ static void run(float (&v)[NV], int l) { level<8, NV>(v, l); }
 };
 
 // a lane's NR consecutive floats
