@@ -222,8 +222,11 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
     }
 }
 
+// Five wavefronts per SIMD need two registers fewer than the compiler takes with up to
+// four states in a lane (16 x 1024 x 5120 x 16, five workgroups per CU: 348 us at four,
+// 335 at five; six would spill, 696 us).
 template <typename T, int NR, int CW, bool FULL>
-__global__ __launch_bounds__(256) void k_chan_fwd(ChanArgs a)
+__global__ __launch_bounds__(256, NR <= 4 ? 5 : 2) void k_chan_fwd(ChanArgs a)
 {
     __shared__ __align__(16) FwdLds<NR, CW, FULL> lds;
     const int g = blockIdx.x / a.tpg;

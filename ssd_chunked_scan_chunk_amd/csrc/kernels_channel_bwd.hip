@@ -170,8 +170,10 @@ template <int NR> __device__ __forceinline__ void store_states(RowOut row, uint3
 
 // The states at the start of every batch.  SEGS: from zero, with the segment's
 // adjoint, state and sum of dt; otherwise from the initial state.
+// Up to four states in a lane fit five wavefronts per SIMD, a few registers short of
+// what the compiler would take (4 x 2048 x 5120 x 16: 192 us at four, 184 at five).
 template <typename T, int NR, int CW, bool SEGS>
-__global__ __launch_bounds__(256) void k_chan_states(BwdArgs a)
+__global__ __launch_bounds__(256, NR <= 4 ? 5 : 2) void k_chan_states(BwdArgs a)
 {
     constexpr int ES = sizeof(T), NPART = 256 / CW, NP = NPART * NR;
     constexpr int TP = TB * CW / 256;
