@@ -75,8 +75,8 @@ static double chan_step_ns(int cw, int64_t N, int64_t r) {
 // The cheapest of a few segment counts at 64 and at 32 channels per workgroup.
 // Segments pay a second pass (0.72 of the steps' time), the scan over them (one
 // read and one write of their states) and two launches: 2 x 2048 x 5120 x 16 takes
-// 244 us in one segment, 151 us in 16; 8 x 2048 x 5120 x 16, whose channels fill
-// the GPU, 408 us in one and 544 us in 16.
+// 295 us of kernels in one segment, 167 us in 16; 8 x 2048 x 5120 x 16, whose
+// channels fill the GPU, 442 us in one and 571 us in 16.
 ChanPlan chan_fwd_plan(const ChanShape& s) {
     const int64_t all = s.L > 0 ? s.L : 1;
     ChanPlan best{64, all, 1, 0};
@@ -100,7 +100,7 @@ ChanPlan chan_fwd_plan(const ChanShape& s) {
     }
     // up to half a 64-wide workgroup per CU left over: as halves they add half a
     // workgroup's time to every CU, not a whole one's to some (8 x 2048 x 5120 x 16, 640
-    // workgroups: 349 us against 408)
+    // workgroups: 382 us of kernels against 442)
     const int64_t flats = s.Bz * chan_tiles(s, 64), full = flats / 256, rest = flats % 256;
     if (full > 0 && rest > 0 && rest <= 128) {
         const double w = chan_step_ns(64, s.N, full), n = 16 + 1.41 * (double)s.N;
@@ -119,10 +119,10 @@ size_t chan_fwd_bytes(const ChanShape& s, const ChanPlan& p) {
 // Segments of the backward: three to eleven workgroups per CU in all, as evenly as
 // they come (the CU with one more sets the time), the fewer the better as each
 // costs some twelve steps' time of its own, and none shorter than 16 steps.  4 x
-// 2048 x 5120 x 16 (320 workgroups per segment) takes 1092 us in one segment, 730 in
-// four, 753 in five, 711 in eight, 783 in 32; 1 x 2048 x 1536 x 16 (24) 826 us in
-// one, 101 in 16, 83 in 32, 88 in 48.  64 channels to a workgroup measured faster
-// than 32 (711 against 835 us) wherever a lane's states of a batch fit the registers
+// 2048 x 5120 x 16 (320 workgroups per segment) takes 1039 us of kernels in one
+// segment, 693 in four, 723 in five, 691 in eight, 754 in 32; 1 x 2048 x 1536 x 16
+// (24) 781 us in one, 99 in 16, 86 in 32, 89 in 43.  64 channels to a workgroup
+// measured 15% faster than 32 wherever a lane's states of a batch fit the registers
 // (dstate up to 16).
 ChanBwdPlan chan_bwd_plan(const ChanShape& s) {
     ChanBwdPlan p;
