@@ -52,6 +52,15 @@ __device__ __forceinline__ void load_quad(const u16* p, float (&f)[4]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) f[k] = bf_bits_to_f32(v[k]);
 }
+// Values n0 .. of a channel's N, 0 past them.  All are read, those past N as the last:
+// a condition around each read would have it wait for its own value, one memory
+// latency after the other.
+template <int NR> __device__ __forceinline__ void load_values(const float* p, int n0, int N, float (&v)[NR]) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) v[i] = p[n0 + i < N ? n0 + i : N - 1];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) v[i] = n0 + i < N ? v[i] : 0.f;
+}
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(u16 v) { return bf_bits_to_f32(v); }
 

@@ -65,17 +65,11 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
     const int te = (int)(len < ts ? 0 : (len < t1 ? len : t1) - ts);   // steps to compute from ts on
     const bool gated = a.in.gate != nullptr;
 
-    float A2[NR], h[NR], sdt = 0.f;
+    float A2[NR], h[NR] = {}, sdt = 0.f;
     const float bias = a.in.dbias ? a.in.dbias[ch] : 0.f, skip = a.in.skip ? a.in.skip[ch] : 0.f;
     const float* h0 = !FULL ? nullptr
                       : seg > 0 ? a.S + ((b * a.nseg + seg) * a.D + ch) * a.N
                       : a.in.h0 ? a.in.h0 + (b * a.D + ch) * a.N : nullptr;
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const bool in = n0 + i < a.N;   // states past N: A = B = C = 0
-        A2[i] = in ? a.in.A[ch * a.N + n0 + i] * kLog2e : 0.f;
-        h[i] = in && h0 ? h0[n0 + i] : 0.f;
-    }
     // rows of the batch being fetched, and of the one being written
     RowIn up = row_in(a.in.u, (b * a.ub + gch) * ES + ts * a.ur);
     RowIn dp = row_in(a.in.delta, (b * a.db + gch) * ES + ts * a.dr);
@@ -191,7 +185,13 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
         offsets(TB - 1);
         fetch(Int<0>(), te - 1);
         if (TB < te) fetch(Int<1>(), te - 1 - TB);
+    }
+    load_values<NR>(a.in.A + ch * a.N, n0, a.N, A2);   // states past N: A = B = C = 0
+    if (h0) load_values<NR>(h0, n0, a.N, h);
+    if (te > 0) {
         prepare(0, Int<0>());
+#pragma unroll
+        for (int i = 0; i < NR; ++i) A2[i] *= kLog2e;
         for (int t = 0; t < te; t += 2 * TB) {
             batch(t, Int<0>());
             if (t + TB < te) batch(t + TB, Int<1>());
@@ -226,7 +226,7 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
 // four states in a lane (16 x 1024 x 5120 x 16, five workgroups per CU: 348 us at four,
 // 335 at five; six would spill, 696 us).
 template <typename T, int NR, int CW, bool FULL>
-__global__ __launch_bounds__(256, NR <= 4 ? 5 : 2) void k_chan_fwd(ChanArgs a)
+__global__ __launch_bounds__(256, NR <= 4 ? 5 : FULL ? 4 : 2) void k_chan_fwd(ChanArgs a)
 {
     __shared__ __align__(16) FwdLds<NR, CW, FULL> lds;
     const int g = blockIdx.x / a.tpg;
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(256, NR <= 4 ? 5 : 2) void k_chan_fwd(ChanArgs a)
 // of the remaining 64-wide tiles: where the channels come to a few workgroups per CU
 // and up to half a one more, the halves even out what the CUs get.
 template <typename T, int NR>
-__global__ __launch_bounds__(256) void k_chan_fwd_mixed(ChanArgs a, int whole, int tiles)
+__global__ __launch_bounds__(256, 4) void k_chan_fwd_mixed(ChanArgs a, int whole, int tiles)
 {
     __shared__ __align__(16) union { FwdLds<NR, 64, true> w; FwdLds<NR / 2, 32, true> n; } lds;
     const int past = (int)blockIdx.x - whole, flat = past < 0 ? blockIdx.x : whole + past / 2;

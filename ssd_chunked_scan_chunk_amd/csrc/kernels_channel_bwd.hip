@@ -196,15 +196,8 @@ __global__ __launch_bounds__(256, NR <= 4 ? 5 : 2) void k_chan_states(BwdArgs a)
     const int te = (int)(len < ts ? 0 : (len < t1 ? len : t1) - ts);
     const bool gated = f.in.gate != nullptr;
 
-    float A2[NR], h[NR], G[NR] = {}, P[NR], sum = 0.f;
+    float A2[NR], h[NR] = {}, G[NR] = {}, P[NR], sum = 0.f;
     const float bias = f.in.dbias ? f.in.dbias[ch] : 0.f;
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const bool in = n0 + i < f.N;
-        A2[i] = in ? f.in.A[ch * f.N + n0 + i] * kLog2e : 0.f;
-        h[i] = !SEGS && in && f.in.h0 ? f.in.h0[(b * f.D + ch) * f.N + n0 + i] : 0.f;
-        P[i] = 1.f;
-    }
     RowIn up = row_in(f.in.u, (b * f.ub + gch) * ES + ts * f.ur);
     RowIn dp = row_in(f.in.delta, (b * f.db + gch) * ES + ts * f.dr);
     RowIn zp = row_in(gated ? f.in.gate : f.in.u, (b * f.zb + gch) * ES + ts * f.zr);
@@ -307,7 +300,14 @@ __global__ __launch_bounds__(256, NR <= 4 ? 5 : 2) void k_chan_states(BwdArgs a)
         offsets(TB - 1);
         fetch(Int<0>(), te - 1);
         if (TB < te) fetch(Int<1>(), te - 1 - TB);
+        load_values<NR>(f.in.A + ch * f.N, n0, f.N, A2);
+        if (!SEGS && f.in.h0) load_values<NR>(f.in.h0 + (b * f.D + ch) * f.N, n0, f.N, h);
         prepare(0, Int<0>());
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            A2[i] *= kLog2e;
+            P[i] = 1.f;
+        }
         for (int t = 0; t < te; t += 2 * TB) {
             batch(t, Int<0>());
             if (t + TB < te) batch(t + TB, Int<1>());
@@ -338,8 +338,12 @@ __global__ __launch_bounds__(256) void k_chan_link(BwdArgs a, int64_t items)
     const int g = tile / f.tpg, cg = (tile - g * f.tpg) * CW + c;
     const int64_t ch = (int64_t)g * f.per + (cg < f.per ? cg : f.per - 1), at = (b * f.D + ch) * f.N + n;
     const bool in = n < f.N;
-    const float A2 = in ? f.in.A[ch * f.N + n] * kLog2e : 0.f;
-    float h = in && f.in.h0 ? f.in.h0[at] : 0.f, gr = in && a.dh ? a.dh[at] : 0.f;
+    const int last = in ? 0 : n - f.N + 1;   // states past N read the last one's values
+    const float A = f.in.A[ch * f.N + n - last];
+    float h = f.in.h0 ? f.in.h0[at - last] : 0.f, gr = a.dh ? a.dh[at - last] : 0.f;
+    const float A2 = in ? A * kLog2e : 0.f;
+    h = in ? h : 0.f;
+    gr = in ? gr : 0.f;
     float* S = a.hs + b * f.nseg * per_b + k;
     float* G = a.gs + b * f.nseg * per_b + k;
     const int64_t per_s = (int64_t)a.tiles * CW;
@@ -391,16 +395,9 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
     const bool gated = f.in.gate != nullptr;
     const int nb = (te + TB - 1) / TB;                 // batches of this segment
 
-    float A2[NR], dA[NR] = {}, carry[NR], hin[NR];
+    float A2[NR], dA[NR] = {}, carry[NR] = {}, hin[NR] = {};
     const float bias = f.in.dbias ? f.in.dbias[ch] : 0.f, skip = f.in.skip ? f.in.skip[ch] : 0.f;
     const int64_t sat = (((b * f.nseg + seg) * a.tiles + tile) * 256 + tid) * NR;
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const bool in = n0 + i < f.N;
-        A2[i] = in ? f.in.A[ch * f.N + n0 + i] * kLog2e : 0.f;
-        carry[i] = SEGS ? a.gs[sat + i] : in && a.dh ? a.dh[(b * f.D + ch) * f.N + n0 + i] : 0.f;
-        hin[i] = SEGS ? a.hs[sat + i] : 0.f;
-    }
     const RowIn up = row_in(f.in.u, (b * f.ub + gch) * ES + ts * f.ur);
     const RowIn dp = row_in(f.in.delta, (b * f.db + gch) * ES + ts * f.dr);
     const RowIn zp = row_in(gated ? f.in.gate : f.in.u, (b * f.zb + gch) * ES + ts * f.zr);
@@ -486,8 +483,17 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
     if (nb > 0) {
         offsets(te - 1 - (nb - 1) * TB);
         fetch(nb - 1);
-        prepare(nb - 1);
     }
+    load_values<NR>(f.in.A + ch * f.N, n0, f.N, A2);
+    if (SEGS) {
+        load_values<NR>(a.gs + sat, 0, NR, carry);
+        load_values<NR>(a.hs + sat, 0, NR, hin);
+    } else if (a.dh) {
+        load_values<NR>(a.dh + (b * f.D + ch) * f.N, n0, f.N, carry);
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) A2[i] *= kLog2e;
+    if (nb > 0) prepare(nb - 1);
     offsets(TB - 1);   // of all other batches, and of the outputs
     using Sum = LaneSum<RB * 2 * NR, CW>;
     // the values this lane is left with, vi .. : state (part's n0 +) i of B or C at step k
