@@ -101,11 +101,12 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
             obc[e] = r * (in_C(e) ? a.Cr : a.Br) + (uint32_t)(n < a.N ? n : a.N - 1) * ES;
         }
     };
-    // two batches in flight
+    // Two batches in flight: the one at t, or past the end the last one again.
     T ru[2][TP], rd[2][TP], rz[2][TP], rbc[2][NE];
-    auto fetch = [&](auto slot, int last) {
+    auto fetch = [&](auto slot, int t) {
         constexpr int P = decltype(slot)::value;
-        if (last < TB - 1) offsets(last);
+        const int last = te - 1 - t;
+        if ((FULL || last >= 0) && last < TB - 1) offsets(last);
 #pragma unroll
         for (int k = 0; k < TP; ++k) {
             ru[P][k] = load_at<T>(up, ou[k]);
@@ -115,11 +116,13 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
 #pragma unroll
         for (int e = 0; e < NE; ++e)
             rbc[P][e] = load_at<T>(in_C(e) ? Cp : Bp, obc[e]);
-        up += TB * (uint64_t)a.ur;
-        dp += TB * (uint64_t)a.dr;
-        zp += TB * (uint64_t)a.zr;
-        Bp += TB * (uint64_t)a.Br;
-        Cp += TB * (uint64_t)a.Cr;
+        if (FULL || last >= TB) {
+            up += TB * (uint64_t)a.ur;
+            dp += TB * (uint64_t)a.dr;
+            zp += TB * (uint64_t)a.zr;
+            Bp += TB * (uint64_t)a.Br;
+            Cp += TB * (uint64_t)a.Cr;
+        }
     };
     float u[2][TP], z[2][TP];
     auto prepare = [&](int t, auto slot) {
@@ -147,7 +150,11 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
     // next are fetched into that slot, those of the next prepared.
     auto batch = [&](int t, auto slot) {
         constexpr int P = decltype(slot)::value;
-        if (t + 2 * TB < te) fetch(slot, te - 1 - t - 2 * TB);
+        // Without outputs to write, reading the last batch again past the end is faster:
+        // beside reads that may not take place the compiler waits for both batches (147
+        // against 139 us in 1 x 32768 x 1536 x 16).  With them it is slower (358 against 369
+        // us in 8 x 2048 x 5120 x 16).
+        if (!FULL || t + 2 * TB < te) fetch(slot, t + 2 * TB);
         if (t == 0 || !FULL) lds_barrier();   // otherwise the one below has ordered slot P
 #pragma unroll
         for (int k = 0; k < TB; ++k) {
@@ -183,8 +190,8 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
     for (int k = 0; k < TP; ++k) oy[k] = (part + k * NPART) * yr + col;
     if (te > 0) {
         offsets(TB - 1);
-        fetch(Int<0>(), te - 1);
-        if (TB < te) fetch(Int<1>(), te - 1 - TB);
+        fetch(Int<0>(), 0);
+        if (!FULL || TB < te) fetch(Int<1>(), TB);
     }
     load_values<NR>(a.in.A + ch * a.N, n0, a.N, A2);   // states past N: A = B = C = 0
     if (h0) load_values<NR>(h0, n0, a.N, h);
