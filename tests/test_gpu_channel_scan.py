@@ -346,6 +346,31 @@ def test_backward_rows_behind_the_end(dtype):
     assert torch.equal(g0["dinitial_state"][0], dh[0])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L,N", [(13, 16), (77, 40)])   # in one segment and in several
+def test_backward_infinities_stay_where_they_are(dtype, L, N):
+    # an infinite u in the last step of a partial batch touches its channel, and of the
+    # sums over channels its own step (dB and, through the state, dC)
+    log("channel scan bwd infinities %s %d %d" % (dtype, L, N))
+    d = inputs(2, L, 40, N, 1, dtype, 14, carry=False)
+    dy, dh = upstream(d, dtype, 5)
+    run = lambda: ssd.channel_scan_bwd(**d, dy=dy, dfinal_state=dh, softplus=True, return_dinitial_state=True)
+    g0 = run()
+    d["u"][0, L - 1, 3] = float("inf")
+    g1 = run()
+    torch.cuda.synchronize()
+    others = [c for c in range(40) if c != 3]
+    for k in ("du", "ddelta", "dgate"):
+        assert torch.equal(g0[k][..., others], g1[k][..., others]) and torch.equal(g0[k][1], g1[k][1]), k
+    for k in ("dA", "dskip", "ddelta_bias"):
+        assert torch.equal(g0[k][others], g1[k][others]), k
+    for k in ("dB", "dC"):
+        assert torch.equal(g0[k][0, :L - 1], g1[k][0, :L - 1]) and torch.equal(g0[k][1], g1[k][1]), k
+        assert not g1[k][0, L - 1].isfinite().any(), k
+    assert torch.equal(g0["du"][0, :, 3], g1["du"][0, :, 3])   # no gradient of u depends on u
+    assert torch.equal(g0["dinitial_state"], g1["dinitial_state"])
+
+
 def test_backward_repeats_streams_and_graphs():
     log("channel scan bwd streams and graphs")
     for L in (70, 900):
