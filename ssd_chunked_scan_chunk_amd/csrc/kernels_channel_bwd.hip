@@ -47,13 +47,20 @@ struct BwdArgs {
     // workspace: states at the start of every batch [b][batch][tile][thread][NR]
     // and, with several segments, the sums of dt before them [b][batch][tile][CW]
     float *ck, *cdt;
-    // per segment [b][seg][tile][thread][NR]: state and adjoint from zero, then
-    // (k_chan_link) those that enter it; its sum of dt [b][seg][tile][CW]
+    // per segment [b][seg][tile][thread][NR]: state and adjoint from zero, if linked
+    // then those that enter it; its sum of dt [b][seg][tile][CW]
     float *hs, *gs, *sumdt;
     float* pbc;                   // [b][t][tile][B, C][NP]: sums over a workgroup's channels
     float *pA, *pskip, *pbias;    // [b][seg][channel]([state])
     int tiles, nb;                // workgroups along the channels, batches of a segment
+    bool linked;                  // k_chan_link runs
 };
+
+// Up to this many segments every workgroup joins them by itself, above it a kernel of
+// its own does it once (kernels in us, joined by the workgroups and by the kernel: 4 x
+// 2048 x 5120 x 16, eight segments, 674 and 700; 3 x 301 x 770 x 12, 19, 38.1 and
+// 39.2; 1 x 2048 x 1536 x 16, 32, 84.1 and 83.6; 1 x 4096 x 256 x 16, 256, 74.8 and 68.1).
+constexpr int kJoinMost = 24;
 
 // A wavefront's reduction of NV values over W neighbouring lanes (64 or 32): lane l
 // is left with values index(l) .. of sum over the lanes.  Each level pairs lanes,
@@ -324,6 +331,29 @@ __global__ __launch_bounds__(256, NR <= 4 ? 5 : 2) void k_chan_states(BwdArgs a)
     }
 }
 
+// h through `count` segments: their end states from zero S (a thread's NR) and sums of
+// dt sd, at steps of ss and ds
+template <int NR>
+__device__ __forceinline__ void join_segments(const float* S, int64_t ss, const float* sd, int64_t ds, int count,
+                                              const float (&A2)[NR], float (&h)[NR]) {
+    constexpr int U = NR <= 4 ? 8 : 4;   // in flight
+    for (int s = 0; s < count; s += U) {
+        float v[U][NR], d[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int64_t q = s + k < count ? s + k : count - 1;
+            load_values<NR>(S + q * ss, 0, NR, v[k]);
+            d[k] = sd[q * ds];
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (s + k < count) {
+#pragma unroll
+                for (int i = 0; i < NR; ++i) h[i] = fmaf(fast_exp2(A2[i] * d[k]), h[i], v[k][i]);
+            }
+    }
+}
+
 // Segments joined: hs[seg] becomes the state that enters it, gs[seg] the adjoint
 // that enters it from behind.  One thread per (batch, tile, thread, state).
 template <int NR, int CW>
@@ -485,14 +515,22 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
         fetch(nb - 1);
     }
     load_values<NR>(f.in.A + ch * f.N, n0, f.N, A2);
-    if (SEGS) {
+    if (SEGS && a.linked) {
         load_values<NR>(a.gs + sat, 0, NR, carry);
         load_values<NR>(a.hs + sat, 0, NR, hin);
-    } else if (a.dh) {
-        load_values<NR>(a.dh + (b * f.D + ch) * f.N, n0, f.N, carry);
+    } else {
+        if (a.dh) load_values<NR>(a.dh + (b * f.D + ch) * f.N, n0, f.N, carry);
+        if (SEGS && f.in.h0) load_values<NR>(f.in.h0 + (b * f.D + ch) * f.N, n0, f.N, hin);
     }
 #pragma unroll
     for (int i = 0; i < NR; ++i) A2[i] *= kLog2e;
+    if (SEGS && !a.linked) {   // states from the segments before, adjoints from those behind
+        const int64_t ss = (int64_t)a.tiles * 256 * NR, ds = (int64_t)a.tiles * CW, nth = f.nseg - 1;
+        const int64_t first = b * f.nseg * ss + ((int64_t)tile * 256 + tid) * NR;
+        const int64_t dfirst = b * f.nseg * ds + (int64_t)tile * CW + c;
+        join_segments<NR>(a.hs + first, ss, a.sumdt + dfirst, ds, (int)seg, A2, hin);
+        join_segments<NR>(a.gs + first + nth * ss, -ss, a.sumdt + dfirst + nth * ds, -ds, (int)(nth - seg), A2, carry);
+    }
     if (nb > 0) prepare(nb - 1);
     offsets(TB - 1);   // of all other batches, and of the outputs
     using Sum = LaneSum<RB * 2 * NR, CW>;
@@ -680,8 +718,10 @@ hipError_t run_bwd(const BwdArgs& a, const ChanShape& s, const ChanGrads& o, hip
     if (s.L > 0) {
         if (a.f.nseg > 1) {
             hipLaunchKernelGGL((k_chan_states<T, NR, CW, true>), grid, blk, 0, st, a);
-            const int64_t items = s.Bz * a.tiles * 256 * NR;
-            hipLaunchKernelGGL((k_chan_link<NR, CW>), dim3((unsigned)((items + 255) / 256)), blk, 0, st, a, items);
+            if (a.linked) {
+                const int64_t items = s.Bz * a.tiles * 256 * NR;
+                hipLaunchKernelGGL((k_chan_link<NR, CW>), dim3((unsigned)((items + 255) / 256)), blk, 0, st, a, items);
+            }
         } else {
             hipLaunchKernelGGL((k_chan_states<T, NR, CW, false>), grid, blk, 0, st, a);
         }
@@ -710,6 +750,7 @@ hipError_t launch_chan_bwd(const ChanShape& s, const ChanBwdPlan& p, const ChanI
     BwdArgs a = {};
     a.f = chan_args(s, in);
     a.f.seg = p.seg; a.f.nseg = p.nseg;
+    a.linked = p.nseg > kJoinMost;
     a.tiles = (int)chan_tiles(s, p.cw);
     a.f.tpg = (int)(a.tiles / s.G);
     a.nb = (int)p.nb;
