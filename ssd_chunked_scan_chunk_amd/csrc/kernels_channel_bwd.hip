@@ -13,8 +13,8 @@
 // then takes the eight steps in reverse, the adjoint staying in registers
 // throughout.  About 32 vector instructions per (step, channel, state), ten of them in
 // the first pass, against some 45 bytes per (step, channel): bound by vector issue
-// (4 x 2048 x 5120 x 16: 183 us the first pass, 453 us the main one, its vector units
-// active 97% of the time).
+// (4 x 2048 x 5120 x 16: 181 us the first pass, 463 us the main one, its vector units
+// active 95% of the time).
 //
 // The layout is the forward's: a workgroup owns CW channels of a group, a thread
 // NR of a channel's states; dt, dt u and d are formed once per (step, channel) and
