@@ -22,16 +22,18 @@ def lengths(seqlens, Bz, L):
     return [L] * Bz if seqlens is None else [min(max(int(n), 0), L) for n in seqlens]
 
 
-def conv(x, weight, bias, win, seqlens, silu, dy=None, dwin=None):
+def conv(x, weight, bias, win, seqlens, silu, dy=None, dwin=None, walk=32):
     """Everything of the convolution: y and the final window, and with dy the
     gradients.  Every entry of the result comes with its tolerance in fp32
-    roundings (times U), under the name with "~" before it."""
+    roundings (times U), under the name with "~" before it.  ``walk``: the most
+    steps that the backward sums in one chain."""
     Bz, L, C = x.shape
     W = weight.shape[1]
     out = {"y": np.zeros_like(x), "window": np.zeros((Bz, W - 1, C)), "dx": np.zeros_like(x),
            "dweight": np.zeros_like(weight), "dbias": np.zeros(C), "dinitial_window": np.zeros((Bz, W - 1, C))}
     out.update({"~" + k: np.zeros_like(v) for k, v in list(out.items())})
     aw = np.abs(weight)
+    chain = lambda n: walk + 16 + Bz * (1 + n / 128)
     for b, n in enumerate(lengths(seqlens, Bz, L)):
         xe = np.zeros((n + W - 1, C))
         if win is not None:
@@ -67,13 +69,16 @@ def conv(x, weight, bias, win, seqlens, silu, dy=None, dwin=None):
             dxe[k:k + n] += weight[:, k] * d
             ex[k:k + n] += aw[:, k] * (err + W * np.abs(d))
             out["dweight"][:, k] += (xe[k:k + n] * d).sum(0)
-            # sums of at most 32 + 3 terms in a chain, then one chain over parts
-            out["~dweight"][:, k] += (np.abs(xe[k:k + n]) * (err + (48 + Bz * (1 + n / 128)) * np.abs(d))).sum(0)
+            # a chain of `walk` terms, three additions over the wavefronts; then the parts, at
+            # least 16 steps each (four walks of four or more), every fourth of them in groups
+            # of four (a chain of a sixteenth of them, and the group's and the last ones' five),
+            # three more additions over the wavefronts
+            out["~dweight"][:, k] += (np.abs(xe[k:k + n]) * (err + chain(n) * np.abs(d))).sum(0)
         if dwin is not None:
             dxe[n:] += dwin[b]
             ex[n:] += np.abs(dxe[n:]) + np.abs(dwin[b])
         out["dbias"] += d.sum(0)
-        out["~dbias"] += (err + (48 + Bz * (1 + n / 128)) * np.abs(d)).sum(0)
+        out["~dbias"] += (err + chain(n) * np.abs(d)).sum(0)
         out["dx"][b, :n], out["~dx"][b, :n] = dxe[W - 1:], ex[W - 1:]
         out["dinitial_window"][b], out["~dinitial_window"][b] = dxe[:W - 1], ex[:W - 1]
     return out
