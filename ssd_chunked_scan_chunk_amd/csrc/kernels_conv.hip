@@ -253,6 +253,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvArgs a, const T* _
         for (int j = 0; j < W - 1; ++j) widen<V>(hist[j], xf[j]);
 
         const int64_t tlast = t1 + W - 1;
+        const int64_t te = t1 < n ? t1 : n;   // steps whose terms of dw and db are this walk's
         for (int64_t t = t0; t < tlast; t += U) {
             Row<T, V> in[U], gin[U];
 #pragma unroll
@@ -270,7 +271,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_conv_bwd(ConvArgs a, const T* _
                 float g[V], o[V];
                 widen<V>(in[j], xf[W - 1]);
                 widen<V>(gin[j], g);
-                const bool own = r < t1;
+                // of these alone: past the end d is 0, but the inputs may be infinite or NaN
+                const bool own = r < te;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     float d = g[v];

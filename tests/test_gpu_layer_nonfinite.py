@@ -1,0 +1,64 @@
+"""Infinities, NaN and the type's lowest values in the operators around the chunked
+scan: where the definition gives a finite result, so do the kernels, whatever the
+batch is padded with.  Each call is held to one whose inputs are finite and whose
+results are, by the definition, the same: the bits have to be."""
+import pytest
+import torch
+
+import ssd_chunked_scan_chunk_amd as ssd
+from gpu_util import log
+from test_gpu_channel_scan import DT, lens_of
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+
+
+# ---- convolution ------------------------------------------------------------------------
+
+def conv_inputs(Bz, L, C, W, dtype, seed):
+    gen = torch.Generator().manual_seed(seed)
+    r = lambda *s, dt=DT[dtype]: torch.randn(s, generator=gen).to(dt).cuda()
+    return r(Bz, L, C), r(C, W, dt=torch.float32), r(C, dt=torch.float32), r(Bz, W - 1, C), r(Bz, L, C)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("silu", [True, False])
+@pytest.mark.parametrize("L,W", [(9, 4), (1, 2), (0, 3), (200, 4)])
+def test_window_of_an_empty_sequence(dtype, silu, L, W):
+    # a slot of the batch without a sequence adds nothing to dweight, whatever its window holds
+    log("short conv window of an empty sequence %s" % ((dtype, silu, L, W),))
+    x, weight, bias, win, dy = conv_inputs(3, L, 20, W, dtype, L)
+    lens = lens_of([L, 0, L])
+    run = lambda: ssd.short_conv_bwd(x, weight, dy, bias, initial_window=win, seqlens=lens, silu=silu,
+                                     return_dinitial_window=True)
+    g0 = run()
+    win[1, :, 3], win[1, 0, 7], win[1, :, 11] = NAN, INF, -INF
+    if L == 0:
+        win[0, 0, 5] = INF
+    g1 = run()
+    torch.cuda.synchronize()
+    for k in g0:
+        assert bool(g1[k].isfinite().all()) and torch.equal(g0[k], g1[k]), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("W", [2, 3, 4])
+@pytest.mark.parametrize("n", [1, 3, 4, 6, 40])
+def test_infinity_among_the_last_inputs(dtype, W, n):
+    # without the nonlinearity tap k sums dy[t] x[t - (W-1) + k], t < n: an infinite x in
+    # the last step is in the last tap's sum alone, however long the batch
+    log("short conv infinity among the last inputs %s" % ((dtype, W, n),))
+    x, weight, bias, win, dy = conv_inputs(2, 41, 20, W, dtype, n)
+    dy = dy.abs() + 0.5
+    lens = lens_of([41, n])
+    run = lambda: ssd.short_conv_bwd(x, weight, dy, bias, initial_window=win, seqlens=lens, silu=False)
+    g0 = run()
+    x[1, n - 1, 3], x[1, n - 1, 8] = INF, NAN
+    g1 = run()
+    torch.cuda.synchronize()
+    assert torch.equal(g0["dweight"][:, :W - 1], g1["dweight"][:, :W - 1])
+    assert g1["dweight"][3, W - 1] == INF and bool(g1["dweight"][8, W - 1].isnan())
+    others = [c for c in range(20) if c not in (3, 8)]
+    assert torch.equal(g0["dweight"][others], g1["dweight"][others])
+    assert torch.equal(g0["dx"], g1["dx"]) and torch.equal(g0["dbias"], g1["dbias"])   # neither depends on x
