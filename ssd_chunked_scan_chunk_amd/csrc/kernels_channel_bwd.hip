@@ -417,13 +417,17 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
     // threads past the group repeat its last channel, store nothing and add nothing
     // to sums over channels
     const int cl = live ? cg : f.per - 1;
-    uint32_t col = (uint32_t)cl * ES;
+    const uint32_t col = (uint32_t)cl * ES;
     const int64_t gch = (int64_t)g * f.per, ch = gch + cl, b = blockIdx.z, seg = blockIdx.y;
     const int64_t ts = seg * f.seg, t1 = ts + f.seg < f.L ? ts + f.seg : f.L;
     const int64_t len = chan_length(f.in.lens, b, f.L);
     const int te = (int)(len < ts ? 0 : (len < t1 ? len : t1) - ts);
     const bool gated = f.in.gate != nullptr;
     const int nb = (te + TB - 1) / TB;                 // batches of this segment
+    // A last batch of fewer steps holds them at its end, behind `idle` ones of dt = 0: what
+    // these multiply by 0 for dA is the first step's own e g h, where past the end it would
+    // be the state after the last step, which may be infinite and is no part of dA.
+    const int idle = nb * TB - te;
 
     float A2[NR], dA[NR] = {}, carry[NR] = {}, hin[NR] = {};
     const float bias = f.in.dbias ? f.in.dbias[ch] : 0.f, skip = f.in.skip ? f.in.skip[ch] : 0.f;
@@ -439,15 +443,15 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
     const RowOut dup = row_out(a.du, dense), ddp = row_out(a.ddelta, dense), dzp = row_out(a.dgate, dense);
 
     // The share of batch j of this thread, as in the forward: the steps part + k
-    // NPART of channel c, elements e 256 + tid of B and C.  Steps past `last` (in the
-    // last batch of a segment only) repeat that one.
+    // NPART of channel c, elements e 256 + tid of B and C.  Idle steps, the first `ahead`
+    // (of the last batch of a segment only), repeat the first one's row.
     auto in_C = [&](int e) { return e * 256 + wave64 >= TB * NP; };   // else in B
     uint32_t ou[TP], od[TP], oz[TP], oy[TP], obc[NE], ock = tid * NR * 4, ocdt = c * 4;
-    auto offsets = [&](int last) {
+    auto offsets = [&](int ahead) {
 #pragma unroll
         for (int k = 0; k < TP; ++k) {
             const int s = part + k * NPART;
-            const uint32_t r = s < last ? s : last;
+            const uint32_t r = s > ahead ? s - ahead : 0;
             ou[k] = r * f.ur + col;
             od[k] = r * f.dr + col;
             oz[k] = r * f.zr + col;
@@ -456,7 +460,7 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             const int i = e * 256 + tid, s = i / NP & (TB - 1), n = i & (NP - 1);
-            const uint32_t r = s < last ? s : last;
+            const uint32_t r = s > ahead ? s - ahead : 0;
             obc[e] = r * (in_C(e) ? f.Cr : f.Br) + (uint32_t)(n < f.N ? n : f.N - 1) * ES;
         }
     };
@@ -481,11 +485,11 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
     };
     // of a pair: u, dt, d, softplus' and dy silu'(gate)
     float u[TP], dtv[TP], d[TP], sx[TP], dz[TP], h[NR], sskip = 0.f, sbias = 0.f;
-    auto prepare = [&](int j) {
+    auto prepare = [&](int ahead) {
 #pragma unroll
         for (int k = 0; k < TP; ++k) {
             const int s = part + k * NPART;
-            const bool on = live && j * TB + s < te;   // neither a step past the end nor a channel past
+            const bool on = live && s >= ahead;        // neither an idle step nor a channel past
             const float x = as_f32(rd[k]) + bias;      // the group may add to anything
             const float e = exp_neg_abs<EXACT>(x), r = __builtin_amdgcn_rcpf(1.f + e);
             const float sp = fmaxf(x, 0.f) + log1p_unit(e);
@@ -501,7 +505,7 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
 #pragma unroll
         for (int e = 0; e < NE; ++e) {
             const int i = e * 256 + tid;
-            const bool in = (i & (NP - 1)) < f.N && j * TB + (i / NP & (TB - 1)) < te;
+            const bool in = (i & (NP - 1)) < f.N && (i / NP & (TB - 1)) >= ahead;
             if (NBC % 256 == 0 || i < NBC) s_bc[i] = in ? as_f32(rbc[e]) : 0.f;
         }
         // the state entering the batch
@@ -511,7 +515,7 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
     };
 
     if (nb > 0) {
-        offsets(te - 1 - (nb - 1) * TB);
+        offsets(idle);
         fetch(nb - 1);
     }
     load_values<NR>(f.in.A + ch * f.N, n0, f.N, A2);
@@ -531,8 +535,8 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
         join_segments<NR>(a.hs + first, ss, a.sumdt + dfirst, ds, (int)seg, A2, hin);
         join_segments<NR>(a.gs + first + nth * ss, -ss, a.sumdt + dfirst + nth * ds, -ds, (int)(nth - seg), A2, carry);
     }
-    if (nb > 0) prepare(nb - 1);
-    offsets(TB - 1);   // of all other batches, and of the outputs
+    if (nb > 0) prepare(idle);
+    offsets(0);   // of all other batches, and of the outputs
     using Sum = LaneSum<RB * 2 * NR, CW>;
     // the values this lane is left with, vi .. : state (part's n0 +) i of B or C at step k
     const int vi = Sum::index(lane);
@@ -548,7 +552,8 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
     // what was loaded so far has arrived before the loop counts its own loads
 #pragma unroll
     for (int i = 0; i < NR; ++i) asm volatile("" : "+v"(carry[i]), "+v"(hin[i]));
-    for (int j = nb - 1; j >= 0; --j) {
+    for (int j = nb - 1, ahead = idle; j >= 0; --j, ahead = 0) {
+        const int row0 = j * TB - ahead;   // of the batch's first step, idle or not
         if (j > 0) fetch(j - 1);
         lds_barrier();
         // forward: states and decays of the batch
@@ -574,7 +579,7 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
         // empty asm keeps the compiler from holding them): kept, they would cost a
         // third of the registers and with them a wavefront per SIMD (876 against
         // 532 us for 4 x 2048 x 5120 x 16 in four segments).
-        const RowOut pbc = row_out(a.pbc, (((b * f.L + ts + (int64_t)j * TB) * a.tiles + tile) * 2 * NP) * 4);
+        const RowOut pbc = row_out(a.pbc, (((b * f.L + ts + row0) * a.tiles + tile) * 2 * NP) * 4);
 #pragma unroll
         for (int k0 = TB - RB; k0 >= 0; k0 -= RB) {
             asm volatile("" ::: "memory");
@@ -605,7 +610,7 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
             for (int e = 0; e < Sum::kLeft; ++e) {
                 asm volatile("" : "+v"(v[e]));   // the last addition stays ahead of the branch, in one instruction
                 // lanes that share a value store it more than once, the same bits
-                if (j * TB + k0 + vk[e] < te) store_at(pbc, ov[k0 / RB][e], v[e], 0.f);
+                if (k0 + vk[e] >= ahead) store_at(pbc, ov[k0 / RB][e], v[e], 0.f);
             }
         }
         lds_barrier();
@@ -622,29 +627,34 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
             }
             // A2 = A log2(e)
             const float dd = fmaf(fed, u[k], ma * 0.69314718f) * sx[k];
-            if (live && j * TB + s < te) {
+            if (live && s >= ahead) {
                 sskip = fmaf(d[k], u[k], sskip);
                 sbias += dd;
-                store_at(dup + (uint64_t)j * TB * yr, oy[k], fmaf(fed, dtv[k], skip * d[k]), T());
-                store_at(ddp + (uint64_t)j * TB * yr, oy[k], dd, T());
-                if (gated) store_at(dzp + (uint64_t)j * TB * yr, oy[k], dz[k] * fmaf(skip, u[k], y), T());
+                store_at(dup + (int64_t)row0 * yr, oy[k], fmaf(fed, dtv[k], skip * d[k]), T());
+                store_at(ddp + (int64_t)row0 * yr, oy[k], dd, T());
+                if (gated) store_at(dzp + (int64_t)row0 * yr, oy[k], dz[k] * fmaf(skip, u[k], y), T());
             }
         }
-        if (j > 0) prepare(j - 1);
+        if (j > 0) prepare(0);
     }
 
+    // the channel once more: kept over the loop, whose registers are full, it is spilled
+    int c1 = c;
+    asm volatile("" : "+v"(c1));
+    const int cl1 = (tile - g * f.tpg) * CW + c1;   // of live threads
+    const int64_t row = b * f.nseg + seg, ch1 = gch + cl1;
+    uint32_t col1 = (uint32_t)cl1 * ES;
     for (int64_t s = te + part; s < t1 - ts; s += NPART)
         if (live) {
-            store_at(dup + s * (uint64_t)yr, col, 0.f, T());
-            store_at(ddp + s * (uint64_t)yr, col, 0.f, T());
-            if (gated) store_at(dzp + s * (uint64_t)yr, col, 0.f, T());
+            store_at(dup + s * (uint64_t)yr, col1, 0.f, T());
+            store_at(ddp + s * (uint64_t)yr, col1, 0.f, T());
+            if (gated) store_at(dzp + s * (uint64_t)yr, col1, 0.f, T());
         }
-    const int64_t row = b * f.nseg + seg;
 #pragma unroll
     for (int i = 0; i < NR; ++i)
         if (live && n0 + i < f.N) {
-            a.pA[(row * f.D + ch) * f.N + n0 + i] = dA[i];
-            if (a.dh0 && seg == 0) a.dh0[(b * f.D + ch) * f.N + n0 + i] = carry[i];
+            a.pA[(row * f.D + ch1) * f.N + n0 + i] = dA[i];
+            if (a.dh0 && seg == 0) a.dh0[(b * f.D + ch1) * f.N + n0 + i] = carry[i];
         }
     __syncthreads();
     float* sum = &s_part[0][0][0][0];
@@ -658,8 +668,8 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
             sskip += sum[q * CW + c];
             sbias += sum[256 + q * CW + c];
         }
-        if (a.pskip) a.pskip[row * f.D + ch] = sskip;
-        if (a.pbias) a.pbias[row * f.D + ch] = sbias;
+        if (a.pskip) a.pskip[row * f.D + ch1] = sskip;
+        if (a.pbias) a.pbias[row * f.D + ch1] = sbias;
     }
 }
 

@@ -7,7 +7,7 @@ import torch
 
 import ssd_chunked_scan_chunk_amd as ssd
 from gpu_util import log
-from test_gpu_channel_scan import DT, lens_of
+from test_gpu_channel_scan import DT, inputs, lens_of, upstream
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +62,30 @@ def test_infinity_among_the_last_inputs(dtype, W, n):
     others = [c for c in range(20) if c not in (3, 8)]
     assert torch.equal(g0["dweight"][others], g1["dweight"][others])
     assert torch.equal(g0["dx"], g1["dx"]) and torch.equal(g0["dbias"], g1["dbias"])   # neither depends on x
+
+
+# ---- scan -------------------------------------------------------------------------------
+
+# in one segment and in several, sequences that end inside a batch of eight steps at every
+# place, at its end, and one segment early
+LENGTHS = [(n, n) for n in range(8, 17)] + [(40, n) for n in (1, 8, 13, 24, 31)] + [(300, 300), (300, 283), (300, 299)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [5, 16, 24, 40])
+@pytest.mark.parametrize("L,n", LENGTHS)
+def test_infinite_last_input_and_dA(dtype, N, L, n):
+    # dA sums e g[t] h[t-1] dt: the state after the last step is not in it
+    log("channel scan infinite last input %s" % ((dtype, N, L, n),))
+    d = inputs(2, L, 40, N, 1, dtype, n, carry=False)
+    dy, dh = upstream(d, dtype, 5)
+    run = lambda: ssd.channel_scan_bwd(**d, dy=dy, dfinal_state=dh, softplus=True, seqlens=lens_of([n, L]),
+                                       return_dinitial_state=True)
+    g0 = run()
+    d["u"][0, n - 1, 3] = INF
+    g1 = run()
+    torch.cuda.synchronize()
+    assert bool(g0["dA"].isfinite().all()) and torch.equal(g0["dA"], g1["dA"])
+    for k in ("ddelta", "dgate"):
+        assert torch.equal(g0[k][:, :n - 1], g1[k][:, :n - 1]), k
+    assert torch.equal(g0["du"], g1["du"]) and torch.equal(g0["dinitial_state"], g1["dinitial_state"])
