@@ -72,7 +72,9 @@ template <bool EXACT> __device__ __forceinline__ float exp_neg_abs(float x) {
     const float e = fast_exp2(p);
     if constexpr (EXACT) {
         const float lo = fmaf(a, kLog2e, -p) + a * 1.9259629911e-8f;   // log2(e) - float(log2(e))
-        return fmaf(e, lo * 0.69314718f, e);
+        // below 2e-5 in size wherever e is not 0; an infinity or NaN where p overflowed (x
+        // beyond 2.3e38: masks of the lowest value, infinities), which e = 0 has to win over
+        return fmaf(e, __builtin_amdgcn_fmed3f(lo, -1.f, 1.f) * 0.69314718f, e);
     }
     return e;
 }

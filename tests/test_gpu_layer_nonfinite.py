@@ -11,7 +11,7 @@ from test_gpu_channel_scan import DT, inputs, lens_of, upstream
 
 pytestmark = pytest.mark.gpu
 
-INF, NAN = float("inf"), float("nan")
+INF, NAN, LOWEST = float("inf"), float("nan"), torch.finfo(torch.float32).min
 
 
 # ---- convolution ------------------------------------------------------------------------
@@ -89,3 +89,65 @@ def test_infinite_last_input_and_dA(dtype, N, L, n):
     for k in ("ddelta", "dgate"):
         assert torch.equal(g0[k][:, :n - 1], g1[k][:, :n - 1]), k
     assert torch.equal(g0["du"], g1["du"]) and torch.equal(g0["dinitial_state"], g1["dinitial_state"])
+
+
+MASKS = [("bf16", -INF), ("bf16", torch.finfo(torch.bfloat16).min), ("f32", -INF), ("f32", LOWEST), ("f32", -2.5e38)]
+
+
+@pytest.mark.parametrize("dtype,value", MASKS)
+@pytest.mark.parametrize("L,N", [(13, 16), (77, 40), (300, 5)])
+def test_masked_steps(dtype, value, L, N):
+    # softplus of -infinity is 0, as it is of -150 in 32 bits: such a step leaves the
+    # state as it was
+    log("channel scan masked steps %s" % ((dtype, value, L, N),))
+    d = inputs(2, L, 40, N, 1, dtype, 3)
+    dy, dh = upstream(d, dtype, 5)
+
+    def run(v, bias):
+        d["delta"][0, 4, 3] = d["delta"][1, L - 1] = d["delta"][0, 7:9, 20:] = v
+        d["delta_bias"][17] = bias
+        y, h = ssd.channel_scan_fwd(**d, softplus=True, return_final_state=True)
+        g = ssd.channel_scan_bwd(**d, dy=dy, dfinal_state=dh, softplus=True, return_dinitial_state=True)
+        return dict(g, y=y, h=h)
+
+    want, got = run(-150.0, -150.0), run(value, -INF)
+    torch.cuda.synchronize()
+    assert torch.equal(want["h"][:, 17], d["initial_state"][:, 17])   # a channel that takes no step
+    for k in want:
+        assert bool(got[k].isfinite().all()) and torch.equal(want[k], got[k]), k
+
+
+@pytest.mark.parametrize("dtype,value", MASKS)
+def test_masked_token(dtype, value):
+    log("channel step masked %s" % ((dtype, value),))
+    d = inputs(3, 1, 40, 16, 1, dtype, 4)
+    one = {k: v if v is None or k in ("A", "skip", "delta_bias") else v[:, 0] for k, v in d.items()
+           if k != "initial_state"}
+    out = []
+    for v in (-150.0, value):
+        one["delta"][1] = one["delta"][2, 5] = v
+        state = d["initial_state"].clone()
+        out.append((ssd.channel_step(state, **one, softplus=True), state))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) and bool(b.isfinite().all()) for a, b in zip(*out))
+    assert torch.equal(out[1][1][1], d["initial_state"][1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [INF, NAN])
+def test_unbounded_steps_stay_in_their_channel(dtype, value):
+    # softplus of infinity is infinity, of NaN is NaN: everything of that channel from
+    # there on, nothing of the others
+    log("channel scan unbounded steps %s" % ((dtype, value),))
+    d = inputs(2, 29, 40, 16, 1, dtype, 6)
+    run = lambda: ssd.channel_scan_fwd(**d, softplus=True, return_final_state=True)
+    y0, h0 = run()
+    d["delta"][0, 9, 3] = value
+    y1, h1 = run()
+    torch.cuda.synchronize()
+    assert not h1[0, 3].isfinite().any() and not y1[0, 9:, 3].isfinite().any()
+    keep = torch.ones_like(y0, dtype=torch.bool)
+    keep[0, 9:, 3] = False
+    assert torch.equal(y0[keep], y1[keep])
+    others = [c for c in range(40) if c != 3]
+    assert torch.equal(h0[0, others], h1[0, others]) and torch.equal(h0[1], h1[1])
