@@ -64,6 +64,15 @@ template <int NR> __device__ __forceinline__ void load_values(const float* p, in
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(u16 v) { return bf_bits_to_f32(v); }
 
+// A log2(e), what dt is multiplied by in a decay's exponent.  Products that overflow, and
+// infinities, become the largest finite value: with dt = 0 (steps past the end, masked
+// steps, segments of neither) the exponent is then 0 and the state stays, and with any
+// other dt down to 1e-36 the decay is 0 (or infinite) as it was.
+__device__ __forceinline__ float log2_rate(float A) {
+    const float v = A * kLog2e, most = 3.402823466e38f;
+    return fabsf(v) > most ? copysignf(most, v) : v;
+}
+
 // e^-|x|.  EXACT carries the product with log2(e) in two parts, as its rounding
 // alone moves the result by |x| roundings; without it the error stays below
 // |x| 2^-24, which bf16 inputs do not need less than.

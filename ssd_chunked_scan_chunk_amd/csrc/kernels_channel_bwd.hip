@@ -312,7 +312,7 @@ __global__ __launch_bounds__(256, NR <= 4 ? 5 : 2) void k_chan_states(BwdArgs a)
         prepare(0, Int<0>());
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-            A2[i] *= kLog2e;
+            A2[i] = log2_rate(A2[i]);
             P[i] = 1.f;
         }
         for (int t = 0; t < te; t += 2 * TB) {
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(256) void k_chan_link(BwdArgs a, int64_t items)
     const int last = in ? 0 : n - f.N + 1;   // states past N read the last one's values
     const float A = f.in.A[ch * f.N + n - last];
     float h = f.in.h0 ? f.in.h0[at - last] : 0.f, gr = a.dh ? a.dh[at - last] : 0.f;
-    const float A2 = in ? A * kLog2e : 0.f;
+    const float A2 = in ? log2_rate(A) : 0.f;
     h = in ? h : 0.f;
     gr = in ? gr : 0.f;
     float* S = a.hs + b * f.nseg * per_b + k;
@@ -527,7 +527,7 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
         if (SEGS && f.in.h0) load_values<NR>(f.in.h0 + (b * f.D + ch) * f.N, n0, f.N, hin);
     }
 #pragma unroll
-    for (int i = 0; i < NR; ++i) A2[i] *= kLog2e;
+    for (int i = 0; i < NR; ++i) A2[i] = log2_rate(A2[i]);
     if (SEGS && !a.linked) {   // states from the segments before, adjoints from those behind
         const int64_t ss = (int64_t)a.tiles * 256 * NR, ds = (int64_t)a.tiles * CW, nth = f.nseg - 1;
         const int64_t first = b * f.nseg * ss + ((int64_t)tile * 256 + tid) * NR;

@@ -151,3 +151,45 @@ def test_unbounded_steps_stay_in_their_channel(dtype, value):
     assert torch.equal(y0[keep], y1[keep])
     others = [c for c in range(40) if c != 3]
     assert torch.equal(h0[0, others], h1[0, others]) and torch.equal(h0[1], h1[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [-INF, LOWEST, -2.4e38])
+@pytest.mark.parametrize("L,n", [(13, 13), (16, 16), (40, 21), (300, 300), (300, 150), (1000, 999)])
+def test_states_that_forget_at_once(dtype, value, L, n):
+    # e^{dt A} is 0 for A = -infinity and the lowest values as for -1e30, with every dt
+    # here; steps past the end have dt = 0 and leave the state as it is
+    log("channel scan forgetting states %s" % ((dtype, value, L, n),))
+    d = inputs(2, L, 40, 16, 1, dtype, 7)
+    dy, dh = upstream(d, dtype, 5)
+    lens = lens_of([n, L])
+
+    def run(v):
+        d["A"][3, 5] = d["A"][11] = v
+        y, h = ssd.channel_scan_fwd(**d, softplus=True, seqlens=lens, return_final_state=True)
+        g = ssd.channel_scan_bwd(**d, dy=dy, dfinal_state=dh, softplus=True, seqlens=lens, return_dinitial_state=True)
+        return dict(g, y=y, h=h)
+
+    want, got = run(-1e30), run(value)
+    torch.cuda.synchronize()
+    for k in want:
+        assert bool(got[k].isfinite().all()) and torch.equal(want[k], got[k]), k
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_token_of_states_that_forget_at_once(dtype):
+    # ... and with dt = 0 (delta of -150) such a state stays
+    log("channel step forgetting states %s" % dtype)
+    d = inputs(2, 1, 40, 16, 1, dtype, 8)
+    one = {k: v if v is None or k in ("A", "skip", "delta_bias") else v[:, 0] for k, v in d.items()
+           if k != "initial_state"}
+    one["delta"][1] = -150.0
+    out = []
+    for v in (-1e30, LOWEST, -INF):
+        one["A"][3, 5] = one["A"][11] = v
+        state = d["initial_state"].clone()
+        out.append((ssd.channel_step(state, **one, softplus=True), state))
+    torch.cuda.synchronize()
+    for y, state in out[1:]:
+        assert torch.equal(y, out[0][0]) and torch.equal(state, out[0][1])
+    assert torch.equal(out[0][1][1], d["initial_state"][1])
