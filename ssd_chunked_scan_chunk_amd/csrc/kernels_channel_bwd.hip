@@ -744,12 +744,15 @@ hipError_t run_bwd(const BwdArgs& a, const ChanShape& s, const ChanGrads& o, hip
                        s.Bz * a.f.nseg, o);
     return hipGetLastError();
 }
+// The plan's instance alone fits the regions of its workspace.
 template <typename T>
-hipError_t run_bwd_t(const BwdArgs& a, const ChanShape& s, const ChanGrads& o, hipStream_t st) {
-    if (s.N <= 8) return run_bwd<T, 2, 64>(a, s, o, st);
-    if (s.N <= 16) return run_bwd<T, 4, 64>(a, s, o, st);
-    if (s.N <= 32) return run_bwd<T, 4, 32>(a, s, o, st);
-    return run_bwd<T, 8, 32>(a, s, o, st);
+hipError_t run_bwd_t(const BwdArgs& a, const ChanShape& s, const ChanBwdPlan& p, const ChanGrads& o, hipStream_t st) {
+    if (256 / p.cw * p.nr < s.N) return hipErrorInvalidConfiguration;
+    if (p.cw == 64 && p.nr == 2) return run_bwd<T, 2, 64>(a, s, o, st);
+    if (p.cw == 64 && p.nr == 4) return run_bwd<T, 4, 64>(a, s, o, st);
+    if (p.cw == 32 && p.nr == 4) return run_bwd<T, 4, 32>(a, s, o, st);
+    if (p.cw == 32 && p.nr == 8) return run_bwd<T, 8, 32>(a, s, o, st);
+    return hipErrorInvalidConfiguration;
 }
 
 }  // namespace
@@ -770,7 +773,7 @@ hipError_t launch_chan_bwd(const ChanShape& s, const ChanBwdPlan& p, const ChanI
     a.ck = at(0); a.cdt = at(1); a.hs = at(2); a.gs = at(3); a.sumdt = at(4); a.pbc = at(5); a.pA = at(6);
     a.pskip = o.dskip ? at(7) : nullptr;
     a.pbias = o.ddbias ? at(8) : nullptr;
-    return s.bf16 ? run_bwd_t<u16>(a, s, o, st) : run_bwd_t<float>(a, s, o, st);
+    return s.bf16 ? run_bwd_t<u16>(a, s, p, o, st) : run_bwd_t<float>(a, s, p, o, st);
 }
 
 }  // namespace ssd

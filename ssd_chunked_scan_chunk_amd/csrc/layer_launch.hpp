@@ -54,12 +54,13 @@ int64_t chan_tiles(const ChanShape& s, int cw);   // workgroups over the channel
 size_t chan_fwd_bytes(const ChanShape& s, const ChanPlan& p);
 hipError_t launch_chan_fwd(const ChanShape& s, const ChanPlan& p, const ChanIn& in, void* y, float* hfin,
                            float* ws, hipStream_t st);
-// The backward's segments (64 or 32 channels per workgroup by the number of
-// states), batches of eight steps per segment, and the workspace's regions: states
+// The backward's instance (channels of a workgroup, 64 or 32, and states of a thread, by
+// the number of states; the launcher takes these, which the regions are laid out for),
+// segments, batches of eight steps per segment, and the workspace's regions: states
 // of the batches and their sums of dt, states, adjoints and sums of dt of the
 // segments, the workgroups' sums of dB and dC, the segments' of dA, dskip, dbias.
 struct ChanBwdPlan {
-    int cw;
+    int cw, nr;
     int64_t seg, nseg, nb;
     size_t off[10];          // off[9]: bytes in all
 };

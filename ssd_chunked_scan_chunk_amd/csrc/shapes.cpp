@@ -129,6 +129,7 @@ ChanBwdPlan chan_bwd_plan(const ChanShape& s) {
     p.cw = s.N <= 16 ? 64 : 32;
     const int64_t tiles = chan_tiles(s, p.cw), pieces = 256 / p.cw;
     const int64_t np = s.N <= 8 ? 8 : s.N <= 16 ? 16 : s.N <= 32 ? 32 : 64, nr = np / pieces;
+    p.nr = (int)nr;
     const int64_t groups = s.Bz * tiles > 0 ? s.Bz * tiles : 1, most = s.L > 16 ? (s.L + 15) / 16 : 1;
     int64_t want = groups >= 768 ? 1 : (768 + groups - 1) / groups;
     if (want > most) want = most;
