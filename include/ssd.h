@@ -265,9 +265,10 @@ ssd_status ssd_chunk_scan(const ssd_fwd_desc* desc, const void* X, const float* 
  *   y, dy    npieces (1 to 3) arrays of their own: piece i is
  *            [batch][seqlen][piece[i]], the piece widths adding up to
  *            `channels` in order (X, B and C for the chunked scan, say).
- * x, windows and pieces need the alignment of an element; wide accesses are
- * used where addresses, strides and widths allow them.  Outputs must not
- * overlap inputs or each other. */
+ * x, windows and pieces need the alignment of an element; accesses are wide at
+ * any alignment (with a piece of fewer than four channels, an element at a time).
+ * Rows past a sequence's end and the window of an empty sequence are in no sum,
+ * whatever they hold.  Outputs must not overlap inputs or each other. */
 typedef struct ssd_conv_desc {
     int64_t batch, seqlen, channels, width; /* width 2, 3 or 4 */
     int64_t x_bstride, x_rstride;           /* elements, >= 0 */
@@ -321,9 +322,12 @@ ssd_status ssd_short_conv_step(const ssd_conv_desc* desc, void* window, const vo
  * dstate is 1 to 64.  u, delta, gate, B, C, y and the gradients need the
  * alignment of an element.  Outputs must not overlap inputs, each other or
  * the workspace.  Values are not inspected; NaN and infinities stay within
- * their channel (and the sums over channels dB and dC).  Sequences may be
- * evaluated in segments joined through e^{A sum dt}: with growing states
- * (dt A > 0) results overflow where that factor does. */
+ * their channel (and the sums over channels dB and dC), where an infinity of the
+ * definition may come out as a NaN.  A masked step (delta = -infinity, or low enough
+ * for its softplus to vanish) leaves the state as it is; A = -infinity counts as the
+ * lowest finite value.  Sequences may be evaluated in segments joined through
+ * e^{A sum dt}: with growing states (dt A > 0) results overflow where that factor
+ * does. */
 typedef struct ssd_channel_desc {
     int64_t batch, seqlen, channels, dstate, ngroups;
     int64_t u_bstride, u_rstride, delta_bstride, delta_rstride, gate_bstride, gate_rstride;
@@ -348,7 +352,13 @@ ssd_status ssd_channel_scan_fwd(const ssd_channel_desc* desc, const void* u, con
  * call's dtype; dA, dskip, ddelta_bias (the latter two required exactly when
  * their input is given) and dinitial_state (may be NULL) float32.  dB and dC
  * are summed over their group's channels in float32 and rounded once.  The
- * sums' order is fixed: repeated calls give the same bits. */
+ * sums' order is fixed: repeated calls give the same bits.
+ * The workspace holds the states at every eighth step, sums of dt up to there and
+ * each workgroup's sums of dB and dC, per (batch, step, channel) n/2 + n/8 + 1/2
+ * bytes for n up to 16, n/2 + n/4 + 1/2 above, where n is dstate rounded up to 8, 16,
+ * 32 or 64 and the channels of a group to the next 64 (32 above 16); the segments'
+ * states add a few percent in long sequences, more in short ones.  8 x 2048 x 5120
+ * x 16: 914 MB.  batch*seqlen*ngroups is at most 2^24. */
 typedef struct ssd_channel_grads {
     void* du;
     void* ddelta;

@@ -230,8 +230,8 @@ __device__ __forceinline__ void chan_fwd(const ChanArgs& a, FwdLds<NR, CW, FULL>
 }
 
 // Five wavefronts per SIMD need two registers fewer than the compiler takes with up to
-// four states in a lane (16 x 1024 x 5120 x 16, five workgroups per CU: 348 us at four,
-// 335 at five; six would spill, 696 us).
+// four states in a lane (16 x 1024 x 5120 x 16, five workgroups per CU: 337 us at four,
+// 321 at five; six would spill, 696 us).
 template <typename T, int NR, int CW, bool FULL>
 __global__ __launch_bounds__(256, NR <= 4 ? 5 : FULL ? 4 : 2) void k_chan_fwd(ChanArgs a)
 {
@@ -285,8 +285,8 @@ __global__ __launch_bounds__(256) void k_chan_pass(ChanArgs a, int64_t items)
 }
 
 // Single token: LPC lanes per channel, four states each.  The states are read and
-// written once, 128 bytes a channel at 16 of them: bound by HBM (256 x 5120 x 16: 39 us,
-// 4.6 TB/s, a large copy's rate).
+// written once, 128 bytes a channel at 16 of them: bound by HBM (256 x 5120 x 16: 37 us,
+// 4.8 TB/s, above a large copy's median rate).
 template <typename T, int LPC>
 __global__ __launch_bounds__(256) void k_chan_step(ChanArgs a, float* __restrict__ state, int64_t items)
 {

@@ -11,10 +11,11 @@
 // inputs' own bytes per state), and the main pass walks the batches of eight steps
 // backwards, runs each forward again with its states and decays in registers and
 // then takes the eight steps in reverse, the adjoint staying in registers
-// throughout.  About 32 vector instructions per (step, channel, state), ten of them in
-// the first pass, against some 45 bytes per (step, channel): bound by vector issue
-// (4 x 2048 x 5120 x 16: 181 us the first pass, 463 us the main one, its vector units
-// active 95% of the time).
+// throughout.  About 31 vector instructions per (step, channel, state), nine of them in
+// the first pass, against some 45 bytes per (step, channel) in and out: the main pass is
+// bound by vector issue (4 x 2048 x 5120 x 16: 450 us, its vector units active 95% of the
+// time), the first by that and HBM at once (178 us, always active; the states it
+// writes are half of its 726 MB, 4.1 TB/s).
 //
 // The layout is the forward's: a workgroup owns CW channels of a group, a thread
 // NR of a channel's states; dt, dt u and d are formed once per (step, channel) and
@@ -57,9 +58,9 @@ struct BwdArgs {
 };
 
 // Up to this many segments every workgroup joins them by itself, above it a kernel of
-// its own does it once (kernels in us, joined by the workgroups and by the kernel: 4 x
-// 2048 x 5120 x 16, eight segments, 674 and 700; 3 x 301 x 770 x 12, 19, 38.1 and
-// 39.2; 1 x 2048 x 1536 x 16, 32, 84.1 and 83.6; 1 x 4096 x 256 x 16, 256, 74.8 and 68.1).
+// its own does it once (whole calls in us, joined by the workgroups and by the kernel: 4 x
+// 2048 x 5120 x 16, eight segments, 646 and 647; 3 x 301 x 770 x 12, 19, 37.5 and 38.1;
+// 1 x 2048 x 1536 x 16, 32, 70 and 72; 1 x 4096 x 256 x 16, 256, 113 and 80).
 constexpr int kJoinMost = 24;
 
 // A wavefront's reduction of NV values over W neighbouring lanes (64 or 32): lane l
@@ -180,7 +181,8 @@ template <int NR> __device__ __forceinline__ void store_states(RowOut row, uint3
 // The states at the start of every batch.  SEGS: from zero, with the segment's
 // adjoint, state and sum of dt; otherwise from the initial state.
 // Up to four states in a lane fit five wavefronts per SIMD, a few registers short of
-// what the compiler would take (4 x 2048 x 5120 x 16: 192 us at four, 184 at five).
+// what the compiler would take (4 x 2048 x 5120 x 16: the whole call 653 us at four, 647
+// at five).
 template <typename T, int NR, int CW, bool SEGS>
 __global__ __launch_bounds__(256, NR <= 4 ? 5 : 2) void k_chan_states(BwdArgs a)
 {
@@ -578,7 +580,7 @@ __global__ __launch_bounds__(256, NR <= 4 ? 3 : 2) void k_chan_bwd(BwdArgs a)
         // channels before the next.  The batch's values are read from LDS again (the
         // empty asm keeps the compiler from holding them): kept, they would cost a
         // third of the registers and with them a wavefront per SIMD (876 against
-        // 532 us for 4 x 2048 x 5120 x 16 in four segments).
+        // 532 us for 4 x 2048 x 5120 x 16 in four segments when both were built).
         const RowOut pbc = row_out(a.pbc, (((b * f.L + ts + row0) * a.tiles + tile) * 2 * NP) * 4);
 #pragma unroll
         for (int k0 = TB - RB; k0 >= 0; k0 -= RB) {

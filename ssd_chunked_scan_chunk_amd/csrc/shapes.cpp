@@ -46,9 +46,10 @@ int conv_vec(const ConvShape& s) {
 // The longest walk that leaves enough wavefronts: short walks read their filters
 // and the rows ahead of them more often (the backward also redoes W-1 steps and
 // writes more parts of dweight), long ones are too few to hide latency.  On MI355X,
-// bf16, four channels per thread: forward 8 x 4096 x 5376 at 4, 16 and 64 steps 204,
-// 143 and 148 us, 1 x 1024 x 1792 at 4, 16 and 64 5.1, 6.3 and 15 us; backward 4 x
-// 2048 x 5376 136, 81 and 73 us, 4 x 2048 x 1792 at 8, 32 and 64 39, 33 and 47 us.
+// bf16, four channels per thread: forward 8 x 4096 x 5376 at 4, 16 and 64 steps 223,
+// 139 and 145 us, 1 x 1024 x 1792 at 4, 16 and 64 5.1, 6.3 and 15 us (the kernel);
+// backward 4 x 2048 x 5376 at 4, 16 and 64 134, 73 and 63 us, 4 x 2048 x 1792 at 8, 32
+// and 64 37, 30 and 42 us.
 int64_t conv_rows(const ConvShape& s, bool bwd) {
     const int64_t wide = 64 * conv_vec(s), across = s.Bz * ((s.C + wide - 1) / wide);
     int64_t rows = bwd ? 64 : 16;
@@ -64,9 +65,11 @@ int64_t conv_bwd_parts(const ConvShape& s) { return s.Bz * conv_time_blocks(s, c
 int64_t chan_tiles(const ChanShape& s, int cw) { return s.G * ((s.D / s.G + cw - 1) / cw); }
 // Nanoseconds a CU takes for one step of the r workgroups it holds: the latency
 // of a step while few run, the rate of vector issue once they fill it.  Fitted on
-// MI355X to forwards of 1 x 1536 to 8 x 5120 channels and 8, 16, 32 and 64 states
-// (a step of one workgroup, 16 states: 118 ns at 64 channels, 88 ns at 32; filled:
-// 65 and 38 ns per workgroup; most shapes within 15%).
+// MI355X to forwards of 1 x 1536 to 8 x 5120 channels and 8, 16, 32 and 64 states at
+// four wavefronts per SIMD (a step of one workgroup, 16 states: 118 ns at 64 channels,
+// 88 ns at 32; filled: 65 and 38 ns per workgroup; most shapes within 15%).  At the five
+// that up to 16 states run now, a filled step takes 60 and 31 ns; the plans still come
+// within 4% of the best that was tried (1 x 32768 x 1536 x 16: 337 us, 328 in 96 segments).
 static double chan_step_ns(int cw, int64_t N, int64_t r) {
     const double lat = cw == 64 ? 62 + 3.6 * N : 64 + 1.75 * N, rate = cw == 64 ? 21.7 + 2.7 * N : 16 + 1.41 * N;
     const double few = lat + 0.6 * (double)(r - 1) * rate, many = (double)r * rate;
@@ -75,8 +78,8 @@ static double chan_step_ns(int cw, int64_t N, int64_t r) {
 // The cheapest of a few segment counts at 64 and at 32 channels per workgroup.
 // Segments pay a second pass (0.72 of the steps' time), the scan over them (one
 // read and one write of their states) and two launches: 2 x 2048 x 5120 x 16 takes
-// 295 us of kernels in one segment, 167 us in 16; 8 x 2048 x 5120 x 16, whose
-// channels fill the GPU, 442 us in one and 571 us in 16.
+// 265 us in one segment, 149 us in 16; 8 x 2048 x 5120 x 16, whose channels fill the
+// GPU, 414 us in one (64 channels wide throughout) and 524 us in 16.
 ChanPlan chan_fwd_plan(const ChanShape& s) {
     const int64_t all = s.L > 0 ? s.L : 1;
     ChanPlan best{64, all, 1, 0};
@@ -100,7 +103,7 @@ ChanPlan chan_fwd_plan(const ChanShape& s) {
     }
     // up to half a 64-wide workgroup per CU left over: as halves they add half a
     // workgroup's time to every CU, not a whole one's to some (8 x 2048 x 5120 x 16, 640
-    // workgroups: 382 us of kernels against 442)
+    // workgroups: 340 us against 414, and 385 if all are 32 channels wide)
     const int64_t flats = s.Bz * chan_tiles(s, 64), full = flats / 256, rest = flats % 256;
     if (full > 0 && rest > 0 && rest <= 128) {
         const double w = chan_step_ns(64, s.N, full), n = 16 + 1.41 * (double)s.N;
@@ -119,11 +122,10 @@ size_t chan_fwd_bytes(const ChanShape& s, const ChanPlan& p) {
 // Segments of the backward: three to eleven workgroups per CU in all, as evenly as
 // they come (the CU with one more sets the time), the fewer the better as each
 // costs some twelve steps' time of its own, and none shorter than 16 steps.  4 x
-// 2048 x 5120 x 16 (320 workgroups per segment) takes 1039 us of kernels in one
-// segment, 693 in four, 723 in five, 691 in eight, 754 in 32; 1 x 2048 x 1536 x 16
-// (24) 781 us in one, 99 in 16, 86 in 32, 89 in 43.  64 channels to a workgroup
-// measured 15% faster than 32 wherever a lane's states of a batch fit the registers
-// (dstate up to 16).
+// 2048 x 5120 x 16 (320 workgroups per segment) takes 1077 us in one segment, 657 in
+// four, 678 in five, 650 in eight, 713 in 32; 1 x 2048 x 1536 x 16 (24) 805 us in one,
+// 92 in 16, 74 in 32, 77 in 43.  64 channels to a workgroup measured 15% faster than
+// 32 wherever a lane's states of a batch fit the registers (dstate up to 16).
 ChanBwdPlan chan_bwd_plan(const ChanShape& s) {
     ChanBwdPlan p;
     p.cw = s.N <= 16 ? 64 : 32;

@@ -265,8 +265,9 @@ def channel_scan_fwd(u, delta, A, B, C, skip=None, gate=None, delta_bias=None, s
     64, channel c reads group c*G//D), A [D,N], skip, delta_bias [D] f32,
     initial_state [Bz,D,N] f32 (None: zero).  seqlens [Bz] int32 on the GPU:
     sequence b has that many steps; later rows are not read, y is 0 there and the
-    final state is the one after the last step.  Returns (y, final_state or
-    None); channel_step continues from the state."""
+    final state is the one after the last step.  With softplus a step of delta =
+    -inf leaves the state as it is.  Returns (y, final_state or None); channel_step
+    continues from the state."""
     d = _chan_check(u, delta, A, B, C, skip, gate, delta_bias, softplus, 2)
     dev, state = u.device, (u.shape[0], u.shape[2], A.shape[1])
     _same("initial_state", initial_state, state, torch.float32, dev)
