@@ -324,8 +324,8 @@ ssd_status ssd_short_conv_step(const ssd_conv_desc* desc, void* window, const vo
  * the workspace.  Values are not inspected; NaN and infinities stay within
  * their channel (and the sums over channels dB and dC), where an infinity of the
  * definition may come out as a NaN.  A masked step (delta = -infinity, or low enough
- * for its softplus to vanish) leaves the state as it is; A = -infinity counts as the
- * lowest finite value.  Sequences may be evaluated in segments joined through
+ * for its softplus to vanish) of finite u and B leaves the state as it is; A =
+ * -infinity counts as the lowest finite value.  Sequences may be evaluated in segments joined through
  * e^{A sum dt}: with growing states (dt A > 0) results overflow where that factor
  * does. */
 typedef struct ssd_channel_desc {
