@@ -386,6 +386,109 @@ ssd_status ssd_channel_step(const ssd_channel_desc* desc, float* state, const vo
                             const float* skip, const void* gate, const float* delta_bias, void* y,
                             void* stream);
 
+/* ---- Linear attention with a constant decay for each head ----
+ *
+ * With gamma_h = e^log_decay[h] and g = h * kv_heads / nheads, per (batch, head)
+ *     S[t] = gamma_h S[t-1] + v[t][g] k[t][g]^T,   y[t][h] = scale S[t] q[t][h]
+ * (ssd_chunk_scan_fwd's recurrence has a decay of its own for every step, dense
+ * inputs and X per head beside shared B and C).
+ *   q          rows of nheads*key_dim elements at b*bstride + t*rstride
+ *   k, v       rows of kv_heads*key_dim and kv_heads*value_dim elements, likewise
+ *              strided (rstride at most 2^24 when seqlen > 1), so that all three may be
+ *              parts of one projection's rows
+ *   log_decay  [nheads] float32, a constant of the head; -infinity: no memory
+ *   states     [batch][nheads][value_dim][key_dim] float32, as ssd_step's
+ *   seqlens    [batch] int32 on the device, or NULL: sequence b ends after seqlens[b]
+ *              steps (clamped to 0..seqlen).  Later rows are not read, y and the
+ *              gradients' rows there are set to 0, and the final state is the one
+ *              after the last step
+ *   y, dy      [batch][seqlen][nheads][value_dim] dense
+ * key_dim and value_dim are 1 to 256.  q, k, v, y and the gradients need the alignment of
+ * an element.  Outputs must not overlap inputs, each other or the workspace.  States and
+ * sums are float32 and y is rounded once; bf16 calls form decayed scores and
+ * states' products from two bf16 parts, the decayed values from three.  Values are not
+ * inspected: NaN and infinities stay within their (batch, head) and what is summed over
+ * it, but may reach the up to 63 steps before theirs that share a chunk.  With
+ * growing states (log_decay > 0) results overflow where e^(64 log_decay) does. */
+typedef struct ssd_linear_attn_desc {
+    int64_t batch, seqlen, nheads, kv_heads, key_dim, value_dim;
+    int64_t q_bstride, q_rstride, k_bstride, k_rstride, v_bstride, v_rstride; /* elements, >= 0 */
+    float scale;
+    int32_t dtype; /* ssd_dtype of q, k, v, y and their gradients */
+} ssd_linear_attn_desc;
+
+/* initial_state NULL = zero; final_state may be NULL.  Where few (batch, head)
+ * pairs leave the GPU idle the sequence is split into segments, whose end states
+ * the workspace holds (0 bytes for a single segment). */
+ssd_status ssd_linear_attn_fwd_workspace_bytes(const ssd_linear_attn_desc* desc, size_t* bytes);
+ssd_status ssd_linear_attn_fwd(const ssd_linear_attn_desc* desc, const void* q, const void* k,
+                               const void* v, const float* log_decay, const float* initial_state,
+                               const int32_t* seqlens, void* y, float* final_state, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* Gradients for the upstream dy and (NULL = zero) dfinal_state: dq [batch][seqlen]
+ * [nheads][key_dim], dk and dv [batch][seqlen][kv_heads][...] dense in the call's dtype,
+ * summed over the heads that share a key and value head in float32 and rounded once;
+ * dinitial_state float32 (may be NULL).  log_decay is a constant and has no gradient.  The sums'
+ * order is fixed: repeated calls give the same bits.  With kv_heads < nheads the
+ * workspace holds the heads' dk and dv, 4*(key_dim + value_dim) bytes per (batch, step,
+ * head). */
+ssd_status ssd_linear_attn_bwd_workspace_bytes(const ssd_linear_attn_desc* desc, size_t* bytes);
+ssd_status ssd_linear_attn_bwd(const ssd_linear_attn_desc* desc, const void* q, const void* k,
+                               const void* v, const float* log_decay, const float* initial_state,
+                               const int32_t* seqlens, const void* dy, const float* dfinal_state,
+                               void* dq, void* dk, void* dv, float* dinitial_state, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/* One token: state is updated in place and y [batch][nheads][value_dim] written; rows of
+ * q, k and v are at b*bstride (seqlen must be 1). */
+ssd_status ssd_linear_attn_step(const ssd_linear_attn_desc* desc, float* state, const void* q,
+                                const void* k, const void* v, const float* log_decay, void* y,
+                                void* stream);
+
+/* ---- Norm over groups of channels, with an activation or a gate ----
+ *
+ * For every row (b, t) and group of m = channels/groups consecutive channels, with
+ * act(z) = z sigmoid(z) if silu, else z:
+ *     u = x act(gate) if gate_first, else x
+ *     n = (u - mean(u)) / sqrt(mean((u - mean(u))^2) + eps), mean taken as 0 unless center
+ *     p = weight n + bias
+ *     y = act(p) without a gate, p act(gate) with one, p if gate_first
+ * (a group per head after linear attention; gate_first without center for the
+ * state space layer).  The statistics are each row's own, in float32, the mean before
+ * the squares about it; y is rounded once.
+ *   x, gate       rows of `channels` elements at b*bstride + t*rstride
+ *   weight, bias  [channels] float32 or NULL (1, 0); gate NULL: none
+ *   seqlens       as above: rows behind a sequence's end are not read and are in no sum; y
+ *                 and the gradients' rows there are 0
+ *   y, dy         [batch][seqlen][channels] dense
+ * A group has at most 16384 channels.  x, gate, y and the gradients need the alignment of
+ * an element.  Outputs must not overlap inputs, each other or the workspace.  Values are
+ * not inspected: NaN and infinities stay within their row and group and the sums dweight
+ * and dbias of their channels. */
+typedef struct ssd_group_norm_desc {
+    int64_t batch, seqlen, channels, groups;
+    int64_t x_bstride, x_rstride, gate_bstride, gate_rstride; /* elements, >= 0 */
+    float eps;                           /* finite, >= 0 */
+    int32_t dtype;                       /* ssd_dtype of x, gate, y and their gradients */
+    int32_t center, silu, gate_first;    /* 1 or 0; gate_first needs a gate */
+    int32_t reserved;                    /* must be 0 */
+} ssd_group_norm_desc;
+
+ssd_status ssd_group_norm_fwd(const ssd_group_norm_desc* desc, const void* x, const float* weight,
+                              const float* bias, const void* gate, const int32_t* seqlens, void* y,
+                              void* stream);
+
+/* Gradients for the upstream dy: dx and dgate [batch][seqlen][channels] dense in the
+ * call's dtype, dweight and dbias float32 (dgate, dweight and dbias required exactly
+ * when their input is given).  Sums over rows are formed in a fixed order (repeated calls
+ * give the same bits); the workspace holds their parts. */
+ssd_status ssd_group_norm_bwd_workspace_bytes(const ssd_group_norm_desc* desc, size_t* bytes);
+ssd_status ssd_group_norm_bwd(const ssd_group_norm_desc* desc, const void* x, const float* weight,
+                              const float* bias, const void* gate, const int32_t* seqlens,
+                              const void* dy, void* dx, void* dgate, float* dweight, float* dbias,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* ssd_status_str(ssd_status s);
 /* Detail of the calling thread's most recent error ("" if none). */

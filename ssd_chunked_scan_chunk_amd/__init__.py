@@ -1,6 +1,7 @@
 """MI355X (gfx950) SSD layer: chunked forward, its backward, the recurrent
-decode step, and the operators around them (the short causal convolution and the
-scan with one decay per channel and state).
+decode step, and the operators around them (the short causal convolution, the
+scan with one decay per channel and state, linear attention with one decay per head
+and the norm over groups of channels).
 
 A thin torch binding over libssd.so's C ABI (include/ssd.h).  This module
 only marshals arguments -- checks every tensor's shape, dtype, device and
@@ -29,7 +30,9 @@ __all__ = ["chunk_scan_fwd", "chunk_scan_fwd_noalloc", "chunk_scan_bwd", "bwd_wo
            "SSD_ALGO_MFMA", "SSD_ALGO_VALU", "library_path", "short_conv_fwd", "short_conv_bwd",
            "short_conv_bwd_workspace_bytes", "short_conv_step", "channel_scan_fwd",
            "channel_scan_fwd_workspace_bytes", "channel_scan_bwd", "channel_scan_bwd_workspace_bytes",
-           "channel_step"]
+           "channel_step", "linear_attn_fwd", "linear_attn_fwd_workspace_bytes", "linear_attn_bwd",
+           "linear_attn_bwd_workspace_bytes", "linear_attn_step", "group_norm_fwd", "group_norm_bwd",
+           "group_norm_bwd_workspace_bytes"]
 
 
 def library_path() -> str:
@@ -396,3 +399,6 @@ def chunk_scan(X, a, B, C, chunk, states_in=None, seg_chunks=1, Y=None, wg_units
 from .layer import (channel_scan_bwd, channel_scan_bwd_workspace_bytes,  # noqa: E402
                     channel_scan_fwd, channel_scan_fwd_workspace_bytes, channel_step, short_conv_bwd,
                     short_conv_bwd_workspace_bytes, short_conv_fwd, short_conv_step)
+from .attn import (linear_attn_bwd, linear_attn_bwd_workspace_bytes,  # noqa: E402
+                   linear_attn_fwd, linear_attn_fwd_workspace_bytes, linear_attn_step)
+from .norm import group_norm_bwd, group_norm_bwd_workspace_bytes, group_norm_fwd  # noqa: E402

@@ -34,6 +34,9 @@ EXPORTS = (
     "ssd_stream_rmw", "ssd_short_conv_fwd", "ssd_short_conv_bwd_workspace_bytes", "ssd_short_conv_bwd",
     "ssd_short_conv_step", "ssd_channel_scan_fwd_workspace_bytes", "ssd_channel_scan_fwd", "ssd_channel_step",
     "ssd_channel_scan_bwd_workspace_bytes", "ssd_channel_scan_bwd",
+    "ssd_linear_attn_fwd_workspace_bytes", "ssd_linear_attn_fwd", "ssd_linear_attn_bwd_workspace_bytes",
+    "ssd_linear_attn_bwd", "ssd_linear_attn_step", "ssd_group_norm_fwd", "ssd_group_norm_bwd_workspace_bytes",
+    "ssd_group_norm_bwd",
 )
 SSD_NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -72,6 +75,19 @@ class ChannelDesc(ctypes.Structure):
 class ChannelGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("du", "ddelta", "dgate", "dB", "dC", "dA", "dskip", "ddelta_bias",
                                                "dinitial_state")]
+
+
+class LinearAttnDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("batch", "seqlen", "nheads", "kv_heads", "key_dim", "value_dim", "q_bstride", "q_rstride", "k_bstride",
+                 "k_rstride", "v_bstride", "v_rstride")] + [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class GroupNormDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in
+                ("batch", "seqlen", "channels", "groups", "x_bstride", "x_rstride", "gate_bstride", "gate_rstride")] + \
+               [("eps", ctypes.c_float)] + [(n, ctypes.c_int32) for n in
+                                            ("dtype", "center", "silu", "gate_first", "reserved")]
 
 
 class SSDError(RuntimeError):
@@ -120,12 +136,23 @@ def load(path: str = LIB_PATH):
     lib.ssd_channel_scan_bwd_workspace_bytes.argtypes = [ph, ctypes.POINTER(sz)]
     lib.ssd_channel_scan_bwd.argtypes = [ph] + [vp] * 12 + [ctypes.POINTER(ChannelGrads), vp, sz, vp]
     lib.ssd_channel_step.argtypes = [ph] + [vp] * 11
+    pa, pn, psz = ctypes.POINTER(LinearAttnDesc), ctypes.POINTER(GroupNormDesc), ctypes.POINTER(sz)
+    lib.ssd_linear_attn_fwd_workspace_bytes.argtypes = [pa, psz]
+    lib.ssd_linear_attn_fwd.argtypes = [pa] + [vp] * 9 + [sz, vp]
+    lib.ssd_linear_attn_bwd_workspace_bytes.argtypes = [pa, psz]
+    lib.ssd_linear_attn_bwd.argtypes = [pa] + [vp] * 13 + [sz, vp]
+    lib.ssd_linear_attn_step.argtypes = [pa] + [vp] * 7
+    lib.ssd_group_norm_fwd.argtypes = [pn] + [vp] * 7
+    lib.ssd_group_norm_bwd_workspace_bytes.argtypes = [pn, psz]
+    lib.ssd_group_norm_bwd.argtypes = [pn] + [vp] * 11 + [sz, vp]
     for f in ("ssd_channel_scan_bwd_workspace_bytes", "ssd_channel_scan_bwd", "ssd_channel_scan_fwd_workspace_bytes", "ssd_channel_scan_fwd", "ssd_channel_step", "ssd_short_conv_fwd", "ssd_short_conv_bwd_workspace_bytes", "ssd_short_conv_bwd", "ssd_short_conv_step",
               "ssd_fwd_workspace_bytes", "ssd_fwd_plan", "ssd_chunk_scan_fwd", "ssd_chunk_scan_fwd_noalloc",
               "ssd_step",
               "ssd_chunk_cumsum", "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan",
               "ssd_bwd_workspace_bytes", "ssd_chunk_scan_bwd", "ssd_bwd_da_workspace_bytes", "ssd_bwd_da",
-              "ssd_stream_rmw"):
+              "ssd_stream_rmw", "ssd_linear_attn_fwd_workspace_bytes", "ssd_linear_attn_fwd",
+              "ssd_linear_attn_bwd_workspace_bytes", "ssd_linear_attn_bwd", "ssd_linear_attn_step",
+              "ssd_group_norm_fwd", "ssd_group_norm_bwd_workspace_bytes", "ssd_group_norm_bwd"):
         getattr(lib, f).restype = ctypes.c_int
     lib.ssd_status_str.argtypes = [ctypes.c_int]
     lib.ssd_status_str.restype = ctypes.c_char_p

@@ -949,3 +949,4 @@ ssd_status ssd_bwd_da(const ssd_fwd_desc* desc, const void* X, const float* a, c
 }  // extern "C"
 
 #include "api_layer.hpp"
+#include "api_attn.hpp"

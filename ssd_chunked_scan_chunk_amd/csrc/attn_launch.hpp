@@ -1,0 +1,91 @@
+// attn_launch.hpp -- host-side launchers of linear attention with a decay per head
+// and of the norm over groups of channels.  Arguments are already validated by
+// the C ABI layer (api_attn.hpp); these only enqueue.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ssd {
+
+// ---- linear attention (kernels_attn*.hip) ----------------------------------------
+struct AttnShape {
+    int64_t Bz, L, H, K;                 // K: heads of k and v
+    int64_t Dk, Dv;
+    int64_t qb, qr, kb, kr, vb, vr;      // batch and step strides in elements
+    bool bf16;
+    float scale;
+};
+// One walk over the sequences, in time or against it: with rows a, c of `cd`
+// elements and rows x of `xd`
+//     S[t] = gamma S[t-1] + scale_w x[t] c[t]^T,   y[t] = S[t] a[t],
+// the part of y from inside a chunk times scale_p, the rest times scale_in.  The
+// forward and each of the gradients is one such walk.
+struct AttnPass {
+    const void *a, *c, *x;
+    void* y;                             // dense [Bz][L][H][xd]; fp32 if y_f32
+    int64_t ab, cb, xb;                  // batch strides in elements
+    uint32_t ar, cr, xr;                 // step strides in elements
+    int ag, cg, xg;                      // heads that share a head of a, c, x
+    int cd, xd;
+    const float *first;                  // states [Bz][H][Dv][Dk] (or NULL)
+    float* last;
+    int sc, sx;                          // element (c, x) of a state is at c * sc + x * sx
+    float scale_p, scale_in, scale_w;
+    int rev, y_f32;
+};
+// Chunks of a segment, segments, and the workspace: the states at the segments'
+// ends [Bz][H][nseg - 1][Dv][Dk], forward and backward, and the heads' gradients
+// of shared keys and values (shapes.cpp).
+struct AttnPlan {
+    int64_t cps, nseg;
+    size_t states, adjoint, dk, dv, bytes;   // offsets; bytes in all
+};
+constexpr int kAttnChunkBf16 = 64, kAttnChunkF32 = 32;
+inline int attn_chunk(const AttnShape& s) { return s.bf16 ? kAttnChunkBf16 : kAttnChunkF32; }
+AttnPlan attn_plan(const AttnShape& s, bool bwd);
+// wavefronts of a workgroup, each 32 columns wide, for `xd` columns
+inline int attn_waves(int64_t xd) { return xd > 64 ? 4 : 2; }
+inline int64_t attn_slices(int64_t xd) { return (xd + 32 * attn_waves(xd) - 1) / (32 * attn_waves(xd)); }
+// contracted elements the kernels hold for `cd`
+inline int attn_width(int64_t cd) { return cd > 128 ? 256 : cd > 64 ? 128 : 64; }
+
+// the states at the ends of all segments but the last, each from nothing (the first
+// from p.first), to slots; then joined there
+hipError_t launch_attn_states(const AttnShape& s, const AttnPlan& pl, const AttnPass& p, const float* log_decay,
+                              const int32_t* lens, float* slots, hipStream_t st);
+hipError_t launch_attn_pass(const AttnShape& s, const AttnPlan& pl, const AttnPass& p, const float* log_decay,
+                            const int32_t* lens, const float* slots, hipStream_t st);
+// sums of each key and value head's heads: in [rows][H][D] fp32 -> out [rows][K][D]
+hipError_t launch_attn_share(const float* in, void* out, int64_t rows, int64_t H, int64_t K, int64_t D, bool bf16,
+                             hipStream_t st);
+hipError_t launch_attn_step(const AttnShape& s, float* state, const void* q, const void* k, const void* v,
+                            const float* log_decay, void* y, hipStream_t st);
+
+// ---- group norm (kernels_norm.hip) --------------------------------------------------
+struct NormShape {
+    int64_t Bz, L, C, G;
+    int64_t xb, xr, zb, zr;              // batch and row strides of x and the gate in elements
+    float eps;
+    bool bf16, center, silu, gate_first;
+};
+struct NormIn {
+    const void *x, *gate;
+    const float *weight, *bias;
+    const int32_t* lens;
+};
+// How rows lie over the GPU (shapes.cpp): channels of a thread's piece (16 bytes of them, or
+// 1 where a group is smaller), pieces of a thread, lanes of a group (block: the whole
+// workgroup), groups and rows of a workgroup, workgroups across a row and down the rows.
+struct NormLayout {
+    int vec, pieces, lanes, gw, rw, threads;
+    bool block;
+    int64_t across, down;
+};
+constexpr int64_t kNormMost = 16384;          // channels of a group
+NormLayout norm_layout(const NormShape& s, bool bwd);
+int64_t norm_bwd_parts(const NormShape& s);   // rows of the partial sums of dweight and dbias
+hipError_t launch_norm_fwd(const NormShape& s, const NormIn& in, void* y, hipStream_t st);
+hipError_t launch_norm_bwd(const NormShape& s, const NormIn& in, const void* dy, void* dx, void* dgate, float* dweight,
+                           float* dbias, float* parts, hipStream_t st);
+
+}  // namespace ssd

@@ -1,0 +1,117 @@
+// attn_util.hpp -- device-side pieces shared by the linear attention kernels: rows
+// loaded 16 bytes at a time at any alignment and length, the walk's bookkeeping,
+// and the states' places in memory.
+#pragma once
+#include "attn_launch.hpp"
+#include "mfma_util.hpp"
+
+namespace ssd {
+
+struct AttnArgs {
+    AttnPass p;
+    const float* log_decay;
+    const int32_t* lens;
+    float* slots;            // states at the segments' ends, [Bz][H][nseg - 1][Dv * Dk]
+    int64_t L, cps, nseg, walked, items;   // `walked`: segments of this launch
+    int H, slices;
+};
+
+__device__ __forceinline__ int64_t attn_length(const int32_t* lens, int64_t b, int64_t L) {
+    if (!lens) return L;
+    const int64_t n = lens[b];
+    return n < 0 ? 0 : n > L ? L : n;
+}
+
+// log_decay in powers of two, as the sum of two floats, bounded to finite values:
+// gamma^0 is then 1 whatever the decay, and a decay of -infinity forgets all at once.
+struct Decay {
+    float hi, lo;
+};
+__device__ __forceinline__ Decay log2_decay(float log_decay) {
+    const float v = log_decay * kLog2e, most = 3.402823466e38f;
+    if (!(fabsf(v) < 1e30f)) return Decay{fabsf(v) > most ? copysignf(most, v) : v, 0.f};
+    return Decay{v, fmaf(log_decay, kLog2e, -v) + log_decay * 1.9259629911e-8f};   // log2(e) - float(log2(e))
+}
+// gamma^n, n a whole number >= 0.  What the exponent's roundings lose is carried along:
+// alone they would move the result by |exponent| roundings.
+__device__ __forceinline__ float decay_pow(const Decay& g, int n) {
+    const float f = (float)n, e = g.hi * f, v = fast_exp2(e);
+    const float lo = fmaf(g.lo, f, fmaf(g.hi, f, -e));
+    return fabsf(e) < 200.f ? fmaf(v, lo * 0.69314718f, v) : v;
+}
+
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x4 u32x4_any4 __attribute__((aligned(4)));
+__device__ __forceinline__ u32x4 load16(const u16* p) { return *reinterpret_cast<const u32x4_any*>(p); }
+__device__ __forceinline__ u32x4 load16(const float* p) { return *reinterpret_cast<const u32x4_any4*>(p); }
+
+// A thread's 16-byte piece of every row of a tile: elements [col, col + E) of rows of
+// `d` elements.  It is read from where a whole piece of the row is left (at +
+// shifted(...) the elements then move down by `skip`), so that no read passes the
+// row's end; rows shorter than a piece are read an element at a time.
+template <typename T> struct Piece {
+    static constexpr int E = 16 / sizeof(T);
+    int at, skip;
+    bool shortrow;
+    __device__ __forceinline__ Piece(int col, int d) {
+        shortrow = d < E;
+        const int most = d - E;
+        at = shortrow ? 0 : col < most ? col : most;
+        skip = shortrow ? (col < d ? 0 : E) : col - at;
+        if (skip > E) skip = E;
+    }
+    __device__ __forceinline__ u32x4 load(const T* row, int d) const {
+        if (!shortrow) return load16(row + at);
+        u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const uint32_t bits = e < d ? (uint32_t)raw(row[e < d ? e : 0]) : 0u;
+            if constexpr (E == 8) v[e / 2] |= bits << (16 * (e & 1));
+            else v[e] = bits;
+        }
+        return v;
+    }
+    // what belongs at col.., zeros past the row's end
+    __device__ __forceinline__ u32x4 shifted(u32x4 v) const {
+        if constexpr (E == 8) {
+            if (skip & 4) v = u32x4{v[2], v[3], 0, 0};
+            if (skip & 2) v = u32x4{v[1], v[2], v[3], 0};
+            if (skip & 1)
+                v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+            if (skip & 8) v = u32x4{0, 0, 0, 0};
+        } else {
+            if (skip & 2) v = u32x4{v[2], v[3], 0, 0};
+            if (skip & 1) v = u32x4{v[1], v[2], v[3], 0};
+            if (skip & 4) v = u32x4{0, 0, 0, 0};
+        }
+        return v;
+    }
+    static __device__ __forceinline__ uint32_t raw(u16 v) { return v; }
+    static __device__ __forceinline__ uint32_t raw(float v) { return __float_as_uint(v); }
+};
+
+// A workgroup's place: batch, head, first column, segment.
+struct AttnPlace {
+    int64_t b, seg, len;
+    int h, x0;
+    int64_t state;           // the (batch, head)'s index
+};
+__device__ __forceinline__ bool attn_place(const AttnArgs& A, int width, AttnPlace* w) {
+    // workgroups alternate over the XCDs: those of one take neighbouring items, so that
+    // the slices of a head and the heads of a row meet in one L2
+    const int64_t per = (A.items + kXcds - 1) / kXcds;
+    const int64_t item = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+    if ((int64_t)(blockIdx.x / kXcds) >= per || item >= A.items) return false;
+    int64_t i = item;
+    w->x0 = (int)(i % A.slices) * width;
+    i /= A.slices;
+    w->h = (int)(i % A.H);
+    i /= A.H;
+    w->seg = i % A.walked;
+    w->b = i / A.walked;
+    w->len = attn_length(A.lens, w->b, A.L);
+    w->state = w->b * A.H + w->h;
+    return true;
+}
+
+}  // namespace ssd

@@ -2,6 +2,7 @@
 // shapes each kernel family takes and how the forward MFMA kernel groups
 // heads into workgroups.  Host code only (no kernels), so the C ABI's
 // planning can also be built and checked without a GPU toolchain.
+#include "attn_launch.hpp"
 #include "layer_launch.hpp"
 #include "ssd_launch.hpp"
 
@@ -161,6 +162,74 @@ ChanBwdPlan chan_bwd_plan(const ChanShape& s) {
     }
     p.off[9] = s.Bz > 0 ? o : 0;
     return p;
+}
+
+// Segments of the linear attention's walks: two workgroups per CU, segments of four
+// chunks or more.
+AttnPlan attn_plan(const AttnShape& s, bool bwd) {
+    AttnPlan p = {};
+    const int64_t chunk = attn_chunk(s), chunks = (s.L + chunk - 1) / chunk;
+    const int64_t fewer = bwd && attn_slices(s.Dk) < attn_slices(s.Dv) ? attn_slices(s.Dk) : attn_slices(s.Dv);
+    const int64_t items = s.Bz * s.H * fewer > 0 ? s.Bz * s.H * fewer : 1;
+    int64_t want = (512 + items - 1) / items;
+    if (want > chunks / 4) want = chunks / 4;
+    if (want < 1) want = 1;
+    p.cps = chunks > 0 ? (chunks + want - 1) / want : 1;
+    p.nseg = chunks > 0 ? (chunks + p.cps - 1) / p.cps : 1;
+    const size_t state = (size_t)(s.Bz * s.H * (p.nseg - 1) * s.Dk * s.Dv) * sizeof(float);
+    const size_t rows = bwd && s.K != s.H ? (size_t)(s.Bz * s.L * s.H) * sizeof(float) : 0;
+    auto take = [&](size_t n) {
+        const size_t at = p.bytes;
+        p.bytes += (n + 255) / 256 * 256;
+        return at;
+    };
+    p.states = take(state);
+    p.adjoint = take(bwd ? state : 0);
+    p.dk = take(rows * s.Dk);
+    p.dv = take(rows * s.Dv);
+    return p;
+}
+
+// A group's channels over lanes of a wavefront if 64 pieces hold them, else over a
+// workgroup of up to 16 wavefronts.  Rows are walked by as many workgroups as fill the
+// GPU, the same columns in every one (the backward leaves one part of dweight and dbias
+// for each).
+NormLayout norm_layout(const NormShape& s, bool bwd) {
+    NormLayout l = {};
+    const int64_t m = s.C / s.G, full = s.bf16 ? 8 : 4, rows = s.Bz * s.L;
+    l.vec = (int)(m < full ? 1 : full);
+    const int64_t pieces = (m + l.vec - 1) / l.vec;
+    l.pieces = 1;
+    l.rw = 1;
+    if (pieces <= 64) {
+        l.lanes = 1;
+        while (l.lanes < pieces) l.lanes *= 2;
+        const int64_t waves = (s.G * l.lanes + 63) / 64;
+        l.across = (waves + 7) / 8;
+        const int64_t each = (waves + l.across - 1) / l.across;
+        l.gw = (int)(each * 64 / l.lanes);
+        if (l.gw > s.G) l.gw = (int)s.G;
+        if (l.across == 1 && s.G * l.lanes <= 128) l.rw = (int)(256 / (s.G * l.lanes));
+        l.threads = (int)((l.gw * l.rw * l.lanes + 63) / 64 * 64);
+        l.across = (s.G + l.gw - 1) / l.gw;
+    } else {
+        l.block = true;
+        l.lanes = 64;
+        while ((pieces + 64 * l.pieces - 1) / (64 * l.pieces) > 16) l.pieces *= 2;   // 4 at most, as m is at most kNormMost
+        l.threads = (int)((pieces + 64 * l.pieces - 1) / (64 * l.pieces) * 64);
+        l.gw = 1;
+        l.across = s.G;
+    }
+    const int64_t want = (256 * 2048 / l.threads + l.across - 1) / l.across, most = (rows + l.rw - 1) / l.rw;
+    const int64_t cap = bwd ? 512 : 32768;
+    l.down = want < most ? want : most;
+    if (l.down > cap) l.down = cap;
+    if (l.down < 1) l.down = 1;
+    return l;
+}
+int64_t norm_bwd_parts(const NormShape& s) {
+    const NormLayout l = norm_layout(s, true);
+    return l.down * l.rw;
 }
 
 }  // namespace ssd

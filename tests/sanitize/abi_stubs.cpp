@@ -3,6 +3,7 @@
 // That build exercises argument validation and planning on the CPU; every
 // call it is given fails validation or is host-only, so none of these should
 // run.  If one does, it reports hipErrorNotSupported instead of launching.
+#include "attn_launch.hpp"
 #include "layer_launch.hpp"
 #include "ssd_launch.hpp"
 
@@ -76,5 +77,15 @@ hipError_t launch_chan_fwd(const ChanShape&, const ChanPlan&, const ChanIn&, voi
 hipError_t launch_chan_bwd(const ChanShape&, const ChanBwdPlan&, const ChanIn&, const void*, const float*,
                            const ChanGrads&, void*, hipStream_t) { SSD_STUB; }
 hipError_t launch_chan_step(const ChanShape&, float*, const ChanIn&, void*, hipStream_t) { SSD_STUB; }
+hipError_t launch_attn_states(const AttnShape&, const AttnPlan&, const AttnPass&, const float*, const int32_t*, float*,
+                              hipStream_t) { SSD_STUB; }
+hipError_t launch_attn_pass(const AttnShape&, const AttnPlan&, const AttnPass&, const float*, const int32_t*,
+                            const float*, hipStream_t) { SSD_STUB; }
+hipError_t launch_attn_share(const float*, void*, int64_t, int64_t, int64_t, int64_t, bool, hipStream_t) { SSD_STUB; }
+hipError_t launch_attn_step(const AttnShape&, float*, const void*, const void*, const void*, const float*, void*,
+                            hipStream_t) { SSD_STUB; }
+hipError_t launch_norm_fwd(const NormShape&, const NormIn&, void*, hipStream_t) { SSD_STUB; }
+hipError_t launch_norm_bwd(const NormShape&, const NormIn&, const void*, void*, void*, float*, float*, float*,
+                           hipStream_t) { SSD_STUB; }
 #undef SSD_STUB
 }  // namespace ssd
