@@ -12,8 +12,8 @@ struct AttnArgs {
     const float* log_decay;
     const int32_t* lens;
     float* slots;            // states at the segments' ends, [Bz][H][nseg - 1][Dv * Dk]
-    int64_t L, cps, nseg, walked, items;   // `walked`: segments of this launch
-    int H, slices;
+    int64_t L, cps, nseg;
+    unsigned items, walked, H, slices;     // `walked`: segments of this launch
 };
 
 __device__ __forceinline__ int64_t attn_length(const int32_t* lens, int64_t b, int64_t L) {
@@ -42,6 +42,7 @@ __device__ __forceinline__ float decay_pow(const Decay& g, int n) {
 
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef u32x4 u32x4_any4 __attribute__((aligned(4)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 __device__ __forceinline__ u32x4 load16(const u16* p) { return *reinterpret_cast<const u32x4_any*>(p); }
 __device__ __forceinline__ u32x4 load16(const float* p) { return *reinterpret_cast<const u32x4_any4*>(p); }
 
@@ -52,22 +53,20 @@ __device__ __forceinline__ u32x4 load16(const float* p) { return *reinterpret_ca
 template <typename T> struct Piece {
     static constexpr int E = 16 / sizeof(T);
     int at, skip;
-    bool shortrow;
     __device__ __forceinline__ Piece(int col, int d) {
-        shortrow = d < E;
+        const bool shortrow = d < E;
         const int most = d - E;
         at = shortrow ? 0 : col < most ? col : most;
         skip = shortrow ? (col < d ? 0 : E) : col - at;
         if (skip > E) skip = E;
     }
-    __device__ __forceinline__ u32x4 load(const T* row, int d) const {
-        if (!shortrow) return load16(row + at);
+    __device__ __forceinline__ u32x4 load_short(const T* row, int d) const {
         u32x4 v = {0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const uint32_t bits = e < d ? (uint32_t)raw(row[e < d ? e : 0]) : 0u;
-            if constexpr (E == 8) v[e / 2] |= bits << (16 * (e & 1));
-            else v[e] = bits;
+            const uint32_t bits = (uint32_t)raw(row[e < d ? e : 0]);
+            if constexpr (E == 8) v[e / 2] |= (e < d ? bits : 0u) << (16 * (e & 1));
+            else v[e] = e < d ? bits : 0u;
         }
         return v;
     }
@@ -90,26 +89,28 @@ template <typename T> struct Piece {
     static __device__ __forceinline__ uint32_t raw(float v) { return __float_as_uint(v); }
 };
 
-// A workgroup's place: batch, head, first column, segment.
+// A workgroup's place: batch, head, first column, segment; the sequence's length.  All of it the
+// same for the workgroup, and in scalar registers (the copies to LDS take their
+// base from there).
 struct AttnPlace {
     int64_t b, seg, len;
     int h, x0;
     int64_t state;           // the (batch, head)'s index
 };
+__device__ __forceinline__ unsigned uniform(unsigned v) { return (unsigned)__builtin_amdgcn_readfirstlane((int)v); }
 __device__ __forceinline__ bool attn_place(const AttnArgs& A, int width, AttnPlace* w) {
     // workgroups alternate over the XCDs: those of one take neighbouring items, so that
     // the slices of a head and the heads of a row meet in one L2
-    const int64_t per = (A.items + kXcds - 1) / kXcds;
-    const int64_t item = (int64_t)(blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-    if ((int64_t)(blockIdx.x / kXcds) >= per || item >= A.items) return false;
-    int64_t i = item;
-    w->x0 = (int)(i % A.slices) * width;
+    const unsigned per = (A.items + kXcds - 1) / kXcds;
+    unsigned i = blockIdx.x % kXcds * per + blockIdx.x / kXcds;
+    if (blockIdx.x / kXcds >= per || i >= A.items) return false;
+    w->x0 = (int)uniform(i % A.slices) * width;
     i /= A.slices;
-    w->h = (int)(i % A.H);
+    w->h = (int)uniform(i % A.H);
     i /= A.H;
-    w->seg = i % A.walked;
-    w->b = i / A.walked;
-    w->len = attn_length(A.lens, w->b, A.L);
+    w->seg = uniform(i % A.walked);
+    w->b = uniform(i / A.walked);
+    w->len = uniform((unsigned)attn_length(A.lens, w->b, A.L));
     w->state = w->b * A.H + w->h;
     return true;
 }

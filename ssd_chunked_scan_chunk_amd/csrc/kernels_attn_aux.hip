@@ -1,7 +1,6 @@
 // kernels_attn_aux.hip -- linear attention around its walks: the segments' states
 // joined, gradients of shared keys and values added up, the single-token step.
 #include "attn_util.hpp"
-#include "chan_util.hpp"
 
 namespace ssd {
 namespace {
@@ -80,9 +79,9 @@ static AttnArgs attn_args(const AttnShape& s, const AttnPlan& pl, const AttnPass
                           const int32_t* lens, float* slots, int64_t segs) {
     AttnArgs A;
     A.p = p; A.log_decay = log_decay; A.lens = lens; A.slots = slots;
-    A.L = s.L; A.cps = pl.cps; A.nseg = pl.nseg; A.walked = segs; A.H = (int)s.H;
-    A.slices = (int)attn_slices(p.xd);
-    A.items = s.Bz * s.H * A.slices * segs;
+    A.L = s.L; A.cps = pl.cps; A.nseg = pl.nseg; A.walked = (unsigned)segs; A.H = (unsigned)s.H;
+    A.slices = (unsigned)attn_slices(p.xd);
+    A.items = (unsigned)(s.Bz * s.H * A.slices * segs);
     return A;
 }
 

@@ -19,11 +19,14 @@ template <int W, int NTH> struct StageF {
         lds = row0 * (W + kPad) + tid % PR * 4;
     }
     __device__ __forceinline__ void get(const float* base, uint32_t rs, int rev, int r0, int d) {
+        const bool shortrow = d < 4;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             int r = row0 + k * RS;
             r = r < r0 ? r0 : r;
-            v[k] = piece.load(base + (uint32_t)(rev ? kC - 1 - r : r) * rs, d);
+            const float* row = base + (uint32_t)(rev ? kC - 1 - r : r) * rs;
+            if (!shortrow) v[k] = load16(row + piece.at);
+            else v[k] = piece.load_short(row, d);
         }
     }
     __device__ __forceinline__ void put(float* tile, int r0, bool whole) {
@@ -77,22 +80,29 @@ __global__ __launch_bounds__(64 * NW, KD > 128 ? 1 : 2) void k_attn_f32(const At
     const float* from = w.seg == 0 ? (P.first ? P.first + w.state * SE : nullptr)
                       : FULL ? A.slots + (w.state * (A.nseg - 1) + w.seg - 1) * SE : nullptr;
     if (from && (w.seg == 0 || c0 < chunks)) {
+        // read at a clamped place and dropped: a condition around each read would have it
+        // wait for its own value
+        const float* col = from + (int64_t)(mine ? xc : 0) * P.sx;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int c = element(nt, r);
-                if (mine && c < P.cd) S[nt][r] = from[c * P.sc + xc * P.sx];
+                S[nt][r] = col[(c < P.cd ? c : 0) * P.sc];
             }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[nt][r] = mine && element(nt, r) < P.cd ? S[nt][r] : 0.f;
+        }
     }
     auto save = [&](float* to, float f) {
+        float* col = to + (int64_t)xc * P.sx;
+        int cd = P.cd;
+        asm volatile("" : "+s"(cd));   // or the comparisons above stay in 128 scalar registers till here
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int c = element(nt, r);
-                if (mine && c < P.cd) to[c * P.sc + xc * P.sx] = f * S[nt][r];
-            }
+            for (int r = 0; r < 16; ++r)
+                if (mine && element(nt, r) < cd) col[element(nt, r) * P.sc] = f * S[nt][r];
     };
 
     const float* Ab = FULL ? static_cast<const float*>(P.a) + w.b * P.ab + (w.h / P.ag) * P.cd : nullptr;
