@@ -78,6 +78,7 @@ ssd::AttnPass attn_forward(const ssd::AttnShape& s, const void* q, const void* k
     p.sc = 1; p.sx = (int)s.Dk;
     p.scale_p = p.scale_in = s.scale;
     p.scale_w = 1.f;
+    p.exact = 1;
     return p;
 }
 
@@ -218,6 +219,7 @@ ssd_status ssd_linear_attn_bwd(const ssd_linear_attn_desc* desc, const void* q, 
     pq.x = k; pq.xb = f.cb; pq.xr = f.cr; pq.xg = f.cg;
     pq.cd = f.xd; pq.xd = f.cd; pq.sc = f.sx; pq.sx = f.sc;
     pq.y = dq;
+    pq.exact = 0;                    // its states are no results
     // against time, G[t] = scale dy[t] q[t]^T + gamma G[t+1]: dk = G^T v and dv = G k
     ssd::AttnPass pv = f;
     pv.rev = 1;
@@ -232,6 +234,7 @@ ssd_status ssd_linear_attn_bwd(const ssd_linear_attn_desc* desc, const void* q, 
     pk.c = dy; pk.cb = pq.ab; pk.cr = pq.ar; pk.cg = 1;
     pk.x = q; pk.xb = f.ab; pk.xr = f.ar; pk.xg = 1;
     pk.cd = f.xd; pk.xd = f.cd; pk.sc = f.sx; pk.sx = f.sc;
+    pk.exact = 0;
     pv.last = dinitial_state;
     pk.y = shared ? static_cast<void*>(ws + pl.dk) : dk;
     pv.y = shared ? static_cast<void*>(ws + pl.dv) : dv;

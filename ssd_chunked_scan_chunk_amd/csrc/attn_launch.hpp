@@ -32,22 +32,26 @@ struct AttnPass {
     int sc, sx;                          // element (c, x) of a state is at c * sc + x * sx
     float scale_p, scale_in, scale_w;
     int rev, y_f32;
+    int exact;                           // bf16: states to 25 bits, as they are results, not to 17 (y is
+                                         // rounded to 8; the same whether `last` is asked for)
 };
-// Chunks of a segment, segments, and the workspace: the states at the segments'
-// ends [Bz][H][nseg - 1][Dv][Dk], forward and backward, and the heads' gradients
-// of shared keys and values (shapes.cpp).
+// Steps of a segment (whole chunks of every walk's), segments, and the workspace: the
+// states at the segments' ends [Bz][H][nseg - 1][Dv][Dk], forward and backward, and the
+// heads' gradients of shared keys and values (shapes.cpp).
 struct AttnPlan {
-    int64_t cps, nseg;
+    int64_t steps, nseg;
     size_t states, adjoint, dk, dv, bytes;   // offsets; bytes in all
 };
-constexpr int kAttnChunkBf16 = 64, kAttnChunkF32 = 32;
-inline int attn_chunk(const AttnShape& s) { return s.bf16 ? kAttnChunkBf16 : kAttnChunkF32; }
 AttnPlan attn_plan(const AttnShape& s, bool bwd);
-// wavefronts of a workgroup, each 32 columns wide, for `xd` columns
-inline int attn_waves(int64_t xd) { return xd > 64 ? 4 : 2; }
-inline int64_t attn_slices(int64_t xd) { return (xd + 32 * attn_waves(xd) - 1) / (32 * attn_waves(xd)); }
+// columns of a workgroup, and workgroups across `xd` columns
+inline int attn_columns(int64_t xd) { return xd > 64 ? 128 : 64; }
+inline int64_t attn_slices(int64_t xd) { return (xd + attn_columns(xd) - 1) / attn_columns(xd); }
 // contracted elements the kernels hold for `cd`
 inline int attn_width(int64_t cd) { return cd > 128 ? 256 : cd > 64 ? 128 : 64; }
+// steps of a chunk
+inline int attn_chunk(bool bf16, int64_t cd, int64_t xd) {
+    return bf16 && attn_width(cd) == 128 && attn_columns(xd) == 128 ? 64 : 32;
+}
 
 // the states at the ends of all segments but the last, each from nothing (the first
 // from p.first), to slots; then joined there

@@ -12,7 +12,8 @@ struct AttnArgs {
     const float* log_decay;
     const int32_t* lens;
     float* slots;            // states at the segments' ends, [Bz][H][nseg - 1][Dv * Dk]
-    int64_t L, cps, nseg;
+    int64_t L;
+    int cps, nseg;
     unsigned items, walked, H, slices;     // `walked`: segments of this launch
 };
 
@@ -41,6 +42,7 @@ __device__ __forceinline__ float decay_pow(const Decay& g, int n) {
 }
 
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
 typedef u32x4 u32x4_any4 __attribute__((aligned(4)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 __device__ __forceinline__ u32x4 load16(const u16* p) { return *reinterpret_cast<const u32x4_any*>(p); }
@@ -93,8 +95,8 @@ template <typename T> struct Piece {
 // same for the workgroup, and in scalar registers (the copies to LDS take their
 // base from there).
 struct AttnPlace {
-    int64_t b, seg, len;
-    int h, x0;
+    int64_t b;
+    int seg, len, h, x0;
     int64_t state;           // the (batch, head)'s index
 };
 __device__ __forceinline__ unsigned uniform(unsigned v) { return (unsigned)__builtin_amdgcn_readfirstlane((int)v); }
@@ -108,9 +110,9 @@ __device__ __forceinline__ bool attn_place(const AttnArgs& A, int width, AttnPla
     i /= A.slices;
     w->h = (int)uniform(i % A.H);
     i /= A.H;
-    w->seg = uniform(i % A.walked);
+    w->seg = (int)uniform(i % A.walked);
     w->b = uniform(i / A.walked);
-    w->len = uniform((unsigned)attn_length(A.lens, w->b, A.L));
+    w->len = (int)uniform((unsigned)attn_length(A.lens, w->b, A.L));
     w->state = w->b * A.H + w->h;
     return true;
 }

@@ -79,7 +79,7 @@ static AttnArgs attn_args(const AttnShape& s, const AttnPlan& pl, const AttnPass
                           const int32_t* lens, float* slots, int64_t segs) {
     AttnArgs A;
     A.p = p; A.log_decay = log_decay; A.lens = lens; A.slots = slots;
-    A.L = s.L; A.cps = pl.cps; A.nseg = pl.nseg; A.walked = (unsigned)segs; A.H = (unsigned)s.H;
+    A.L = s.L; A.cps = (int)((pl.steps + attn_chunk(s.bf16, p.cd, p.xd) - 1) / attn_chunk(s.bf16, p.cd, p.xd)); A.nseg = (int)pl.nseg; A.walked = (unsigned)segs; A.H = (unsigned)s.H;
     A.slices = (unsigned)attn_slices(p.xd);
     A.items = (unsigned)(s.Bz * s.H * A.slices * segs);
     return A;
@@ -94,7 +94,7 @@ hipError_t launch_attn_states(const AttnShape& s, const AttnPlan& pl, const Attn
     const int64_t SE = s.Dk * s.Dv;
     const unsigned blocks = (unsigned)((SE + 255) / 256);
     k_attn_join<<<(unsigned)(s.Bz * s.H) * blocks, 256, 0, st>>>(slots, log_decay, lens, s.L, s.H, pl.nseg - 1,
-                                                                 pl.cps * attn_chunk(s), SE, blocks);
+                                                                 pl.steps, SE, blocks);
     return hipGetLastError();
 }
 

@@ -7,7 +7,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kC = kAttnChunkF32, kPad = 4;   // rows padded by 16 bytes: row reads of 16 bytes fall on different banks
+constexpr int kC = 32, kPad = 4;   // rows padded by 16 bytes: row reads of 16 bytes fall on different banks
 
 template <int W, int NTH> struct StageF {
     static constexpr int PR = W / 4, N = kC * PR / NTH, RS = NTH / PR;
@@ -60,8 +60,8 @@ __global__ __launch_bounds__(64 * NW, KD > 128 ? 1 : 2) void k_attn_f32(const At
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l32 = lane & 31, hi = lane >> 5;
     const int rev = P.rev;
-    const int64_t chunks = (w.len + kC - 1) / kC;
-    const int64_t c0 = w.seg * A.cps, c1 = c0 + A.cps < chunks ? c0 + A.cps : chunks;
+    const int chunks = (w.len + kC - 1) / kC;
+    const int c0 = w.seg * A.cps, c1 = c0 + A.cps < chunks ? c0 + A.cps : chunks;
     if (!FULL && c0 + A.cps >= chunks) return;   // no segment follows: its end is not asked for
     const Decay g = log2_decay(A.log_decay[w.h]);
 
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(64 * NW, KD > 128 ? 1 : 2) void k_attn_f32(const At
     const int64_t SE = (int64_t)P.cd * P.xd;
     auto element = [&](int nt, int r) { return 32 * nt + 16 * (r >> 3) + 8 * hi + (r & 7); };
     const float* from = w.seg == 0 ? (P.first ? P.first + w.state * SE : nullptr)
-                      : FULL ? A.slots + (w.state * (A.nseg - 1) + w.seg - 1) * SE : nullptr;
+                      : FULL ? A.slots + (w.state * (int64_t)(A.nseg - 1) + w.seg - 1) * SE : nullptr;
     if (from && (w.seg == 0 || c0 < chunks)) {
         // read at a clamped place and dropped: a condition around each read would have it
         // wait for its own value
@@ -112,8 +112,8 @@ __global__ __launch_bounds__(64 * NW, KD > 128 ? 1 : 2) void k_attn_f32(const At
 
     StageF<KD, NTH> ga(tid, 0, P.cd), gc(tid, 0, P.cd);
     StageF<XW, NTH> gx(tid, w.x0, P.xd);
-    auto first_row = [&](int64_t c) { return c == chunks - 1 ? (int)(chunks * kC - w.len) : 0; };
-    auto get = [&](int64_t c) {
+    auto first_row = [&](int c) { return c == chunks - 1 ? chunks * kC - w.len : 0; };
+    auto get = [&](int c) {
         const int r0 = first_row(c);
         const int64_t t0 = c * kC - r0, m0 = rev ? w.len - kC - t0 : t0;
         if constexpr (FULL) ga.get(Ab + m0 * (int64_t)P.ar, P.ar, rev, r0, P.cd);
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(64 * NW, KD > 128 ? 1 : 2) void k_attn_f32(const At
     for (int s = 0; s < 16; ++s) wt[s] = P.scale_w * decay_pow(g, kC - 1 - (8 * (s >> 2) + 4 * hi + (s & 3)));
 
     if (c0 < c1) get(c0);
-    for (int64_t c = c0; c < c1; ++c) {
+    for (int c = c0; c < c1; ++c) {
         const int r0 = first_row(c), lead = rev && c == 0 ? 0 : 1;
         sync_lds();
         const bool whole = wide && r0 == 0;
@@ -227,19 +227,19 @@ __global__ __launch_bounds__(64 * NW, KD > 128 ? 1 : 2) void k_attn_f32(const At
         if (P.last && (chunks > 0 ? c0 < chunks && c1 == chunks : w.seg == 0))
             save(P.last + w.state * SE, rev && chunks > 0 ? decay_pow(g, 1) : 1.f);
         const int64_t e0 = c0 * kC > w.len ? c0 * kC : w.len;
-        const int64_t e1 = w.seg + 1 == A.nseg || (c0 + A.cps) * kC > A.L ? A.L : (c0 + A.cps) * kC;
+        const int64_t e1 = w.seg + 1 == A.nseg ? A.L : (c0 + A.cps) * kC;
         for (int64_t t = e0 + tid / XW; t < e1; t += NTH / XW) {
             const int x = w.x0 + tid % XW;
             if (x < P.xd) static_cast<float*>(P.y)[((w.b * A.L + t) * A.H + w.h) * P.xd + x] = 0.f;
         }
     } else {
-        save(A.slots + (w.state * (A.nseg - 1) + w.seg) * SE, 1.f);
+        save(A.slots + (w.state * (int64_t)(A.nseg - 1) + w.seg) * SE, 1.f);
     }
 }
 
 template <bool FULL, int KD>
-hipError_t launch(const AttnArgs& A, int waves, unsigned grid, hipStream_t st) {
-    if (waves == 4) k_attn_f32<KD, 4, FULL><<<grid, 256, 0, st>>>(A);
+hipError_t launch(const AttnArgs& A, unsigned grid, hipStream_t st) {
+    if (attn_columns(A.p.xd) == 128) k_attn_f32<KD, 4, FULL><<<grid, 256, 0, st>>>(A);
     else k_attn_f32<KD, 2, FULL><<<grid, 128, 0, st>>>(A);
     return hipGetLastError();
 }
@@ -248,11 +248,10 @@ hipError_t launch(const AttnArgs& A, int waves, unsigned grid, hipStream_t st) {
 
 hipError_t launch_attn_f32(const AttnArgs& A, bool full, hipStream_t st) {
     const unsigned grid = (unsigned)((A.items + kXcds - 1) / kXcds * kXcds);
-    const int waves = attn_waves(A.p.xd);
     switch (attn_width(A.p.cd)) {
-        case 64: return full ? launch<true, 64>(A, waves, grid, st) : launch<false, 64>(A, waves, grid, st);
-        case 128: return full ? launch<true, 128>(A, waves, grid, st) : launch<false, 128>(A, waves, grid, st);
-        default: return full ? launch<true, 256>(A, waves, grid, st) : launch<false, 256>(A, waves, grid, st);
+        case 64: return full ? launch<true, 64>(A, grid, st) : launch<false, 64>(A, grid, st);
+        case 128: return full ? launch<true, 128>(A, grid, st) : launch<false, 128>(A, grid, st);
+        default: return full ? launch<true, 256>(A, grid, st) : launch<false, 256>(A, grid, st);
     }
 }
 

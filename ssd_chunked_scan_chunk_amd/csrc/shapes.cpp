@@ -168,14 +168,15 @@ ChanBwdPlan chan_bwd_plan(const ChanShape& s) {
 // chunks or more.
 AttnPlan attn_plan(const AttnShape& s, bool bwd) {
     AttnPlan p = {};
-    const int64_t chunk = attn_chunk(s), chunks = (s.L + chunk - 1) / chunk;
+    const int64_t chunks = (s.L + 63) / 64;
     const int64_t fewer = bwd && attn_slices(s.Dk) < attn_slices(s.Dv) ? attn_slices(s.Dk) : attn_slices(s.Dv);
     const int64_t items = s.Bz * s.H * fewer > 0 ? s.Bz * s.H * fewer : 1;
     int64_t want = (512 + items - 1) / items;
     if (want > chunks / 4) want = chunks / 4;
     if (want < 1) want = 1;
-    p.cps = chunks > 0 ? (chunks + want - 1) / want : 1;
-    p.nseg = chunks > 0 ? (chunks + p.cps - 1) / p.cps : 1;
+    const int64_t each = chunks > 0 ? (chunks + want - 1) / want : 1;
+    p.steps = 64 * each;
+    p.nseg = chunks > 0 ? (chunks + each - 1) / each : 1;
     const size_t state = (size_t)(s.Bz * s.H * (p.nseg - 1) * s.Dk * s.Dv) * sizeof(float);
     const size_t rows = bwd && s.K != s.H ? (size_t)(s.Bz * s.L * s.H) * sizeof(float) : 0;
     auto take = [&](size_t n) {
