@@ -361,10 +361,22 @@ __global__ __launch_bounds__(128 * NW, (waves_per_simd<KD, NW>())) void k_attn(c
         // read at a clamped place and dropped: a condition around each read would have it
         // wait for its own value
         const float* col = from + (int64_t)(mine ? xc : 0) * P.sx;
+        if (P.sc == 1 && P.cd % 8 == 0) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) S[t][r] = col[(element(t, r) < P.cd ? element(t, r) : 0) * P.sc];
+                for (int r = 0; r < 16; r += 4) {
+                    const int e = element(t, r & 8);
+                    const f32x4 v = *reinterpret_cast<const f32x4_any*>(col + (e < P.cd ? e + (r & 4) : 0));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) S[t][r + k] = v[k];
+                }
+        } else {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) S[t][r] = col[(element(t, r) < P.cd ? element(t, r) : 0) * P.sc];
+        }
         int cd = P.cd;
         asm volatile("" : "+s"(cd));   // or the comparisons above stay in scalar registers till here
 #pragma unroll
@@ -376,6 +388,18 @@ __global__ __launch_bounds__(128 * NW, (waves_per_simd<KD, NW>())) void k_attn(c
         float* col = to + (int64_t)xc * P.sx;
         int cd = P.cd;
         asm volatile("" : "+s"(cd));
+        if (P.sc == 1 && cd % 8 == 0) {
+            if (mine) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 16; r += 4)
+                        if (element(t, r & 8) < cd)
+                            *reinterpret_cast<f32x4_any*>(col + element(t, r)) =
+                                f32x4{f * S[t][r], f * S[t][r + 1], f * S[t][r + 2], f * S[t][r + 3]};
+            }
+            return;
+        }
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
