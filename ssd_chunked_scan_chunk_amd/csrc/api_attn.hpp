@@ -168,8 +168,8 @@ ssd_status ssd_linear_attn_fwd(const ssd_linear_attn_desc* desc, const void* q, 
     ssd::AttnPass p = attn_forward(s, q, k, v, initial_state);
     p.y = y;
     p.last = final_state;
-    hipError_t e = ssd::launch_attn_states(s, pl, p, log_decay, seqlens, states, hs);
-    if (e == hipSuccess) e = ssd::launch_attn_pass(s, pl, p, log_decay, seqlens, states, hs);
+    hipError_t e = ssd::launch_attn_states(s, pl, &p, &states, 1, log_decay, seqlens, hs);
+    if (e == hipSuccess) e = ssd::launch_attn_walks(s, pl, &p, &states, 1, log_decay, seqlens, hs);
     return e == hipSuccess ? ok() : hip_fail(e, "linear attention launch");
 }
 
@@ -240,11 +240,10 @@ ssd_status ssd_linear_attn_bwd(const ssd_linear_attn_desc* desc, const void* q, 
     pv.y = shared ? static_cast<void*>(ws + pl.dv) : dv;
     pk.y_f32 = pv.y_f32 = shared;
 
-    hipError_t e = ssd::launch_attn_states(s, pl, pq, log_decay, seqlens, states, hs);
-    if (e == hipSuccess) e = ssd::launch_attn_states(s, pl, pv, log_decay, seqlens, adjoint, hs);
-    if (e == hipSuccess) e = ssd::launch_attn_pass(s, pl, pq, log_decay, seqlens, states, hs);
-    if (e == hipSuccess) e = ssd::launch_attn_pass(s, pl, pk, log_decay, seqlens, adjoint, hs);
-    if (e == hipSuccess) e = ssd::launch_attn_pass(s, pl, pv, log_decay, seqlens, adjoint, hs);
+    const ssd::AttnPass ends[] = {pq, pv}, walks[] = {pq, pk, pv};
+    float* const slots[] = {states, adjoint, adjoint};
+    hipError_t e = ssd::launch_attn_states(s, pl, ends, slots, 2, log_decay, seqlens, hs);
+    if (e == hipSuccess) e = ssd::launch_attn_walks(s, pl, walks, slots, 3, log_decay, seqlens, hs);
     if (e == hipSuccess && shared && rows > 0) {
         e = ssd::launch_attn_share(static_cast<const float*>(pk.y), dk, rows, s.H, s.K, s.Dk, s.bf16, hs);
         if (e == hipSuccess)

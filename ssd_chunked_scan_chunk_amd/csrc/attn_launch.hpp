@@ -35,11 +35,12 @@ struct AttnPass {
     int exact;                           // bf16: states to 25 bits, as they are results, not to 17 (y is
                                          // rounded to 8; the same whether `last` is asked for)
 };
-// Steps of a segment (whole chunks of every walk's), segments, and the workspace: the
-// states at the segments' ends [Bz][H][nseg - 1][Dv][Dk], forward and backward, and the
-// heads' gradients of shared keys and values (shapes.cpp).
+// The first `whole` (batch, head) pairs are walked in one piece, the others in nseg segments
+// of `steps` steps (whole chunks of every walk's).  The workspace: the states at the
+// segments' ends [pairs - whole][nseg - 1][Dv][Dk], forward and backward, and the heads'
+// gradients of shared keys and values (shapes.cpp).
 struct AttnPlan {
-    int64_t steps, nseg;
+    int64_t whole, steps, nseg;
     size_t states, adjoint, dk, dv, bytes;   // offsets; bytes in all
 };
 AttnPlan attn_plan(const AttnShape& s, bool bwd);
@@ -53,12 +54,13 @@ inline int attn_chunk(bool bf16, int64_t cd, int64_t xd) {
     return bf16 && attn_width(cd) == 128 && attn_columns(xd) == 128 ? 64 : 32;
 }
 
-// the states at the ends of all segments but the last, each from nothing (the first
-// from p.first), to slots; then joined there
-hipError_t launch_attn_states(const AttnShape& s, const AttnPlan& pl, const AttnPass& p, const float* log_decay,
-                              const int32_t* lens, float* slots, hipStream_t st);
-hipError_t launch_attn_pass(const AttnShape& s, const AttnPlan& pl, const AttnPass& p, const float* log_decay,
-                            const int32_t* lens, const float* slots, hipStream_t st);
+// n walks (at most two, to slots[0] and [1]): the states at the ends of all segments but the last,
+// each from nothing (the first from p.first); then joined there
+hipError_t launch_attn_states(const AttnShape& s, const AttnPlan& pl, const AttnPass* p, float* const* slots, int n,
+                              const float* log_decay, const int32_t* lens, hipStream_t st);
+// n walks (at most three); those of the same sizes side by side share a launch
+hipError_t launch_attn_walks(const AttnShape& s, const AttnPlan& pl, const AttnPass* p, float* const* slots, int n,
+                             const float* log_decay, const int32_t* lens, hipStream_t st);
 // sums of each key and value head's heads: in [rows][H][D] fp32 -> out [rows][K][D]
 hipError_t launch_attn_share(const float* in, void* out, int64_t rows, int64_t H, int64_t K, int64_t D, bool bf16,
                              hipStream_t st);

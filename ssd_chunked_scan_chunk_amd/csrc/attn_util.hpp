@@ -7,15 +7,22 @@
 
 namespace ssd {
 
+// Up to three walks of one instance in a launch.  The first `whole` (batch, head) pairs are
+// walked by a workgroup each (and slice of columns), the others by `segs` of them.
 struct AttnArgs {
-    AttnPass p;
+    AttnPass p[3];
+    float* slots[3];         // states at the segments' ends, [pairs - whole][nseg - 1][Dv * Dk]
     const float* log_decay;
     const int32_t* lens;
-    float* slots;            // states at the segments' ends, [Bz][H][nseg - 1][Dv * Dk]
     int64_t L;
-    int cps, nseg;
-    unsigned items, walked, H, slices;     // `walked`: segments of this launch
+    int cps, nseg;           // chunks of a segment, segments of a pair
+    unsigned walks, H, slices, pairs, whole, segs;   // segs: those of this launch
+    unsigned skip_whole;     // 1 for the segments' ends, which whole pairs do not have
 };
+// items of a launch: of whole pairs, and of segments
+inline __host__ __device__ unsigned attn_first(const AttnArgs& A) { return A.skip_whole ? 0 : A.whole * A.slices * A.walks; }
+inline __host__ __device__ unsigned attn_rest(const AttnArgs& A) { return (A.pairs - A.whole) * A.segs * A.slices * A.walks; }
+inline unsigned attn_grid(const AttnArgs& A) { return (attn_first(A) + kXcds - 1) / kXcds * kXcds + (attn_rest(A) + kXcds - 1) / kXcds * kXcds; }
 
 __device__ __forceinline__ int64_t attn_length(const int32_t* lens, int64_t b, int64_t L) {
     if (!lens) return L;
@@ -91,29 +98,43 @@ template <typename T> struct Piece {
     static __device__ __forceinline__ uint32_t raw(float v) { return __float_as_uint(v); }
 };
 
-// A workgroup's place: batch, head, first column, segment; the sequence's length.  All of it the
-// same for the workgroup, and in scalar registers (the copies to LDS take their
-// base from there).
+// A workgroup's place: its walk, batch, head, first column, segment; the sequence's length.  All of
+// it the same for the workgroup, and in scalar registers (the copies to LDS take their base
+// from there).
 struct AttnPlace {
     int64_t b;
-    int seg, len, h, x0;
-    int64_t state;           // the (batch, head)'s index
+    int walk, seg, nseg, cps, len, h, x0;
+    int64_t state, slot;     // indices of the pair's state, and of its first segment's among the slots
 };
 __device__ __forceinline__ unsigned uniform(unsigned v) { return (unsigned)__builtin_amdgcn_readfirstlane((int)v); }
 __device__ __forceinline__ bool attn_place(const AttnArgs& A, int width, AttnPlace* w) {
-    // workgroups alternate over the XCDs: those of one take neighbouring items, so that
-    // the slices of a head and the heads of a row meet in one L2
-    const unsigned per = (A.items + kXcds - 1) / kXcds;
-    unsigned i = blockIdx.x % kXcds * per + blockIdx.x / kXcds;
-    if (blockIdx.x / kXcds >= per || i >= A.items) return false;
+    // Workgroups alternate over the XCDs: those of one take neighbouring items, so that the
+    // walks of a pair, the slices of a head and the heads of a row meet in one L2.
+    const unsigned first = attn_first(A), rest = attn_rest(A), xcd = blockIdx.x % kXcds;
+    const unsigned per = (first + kXcds - 1) / kXcds, more = (rest + kXcds - 1) / kXcds;
+    unsigned j = blockIdx.x / kXcds, i, segs = 1;
+    if (j < per) {
+        i = xcd * per + j;
+        if (i >= first) return false;
+    } else {
+        j -= per;
+        i = xcd * more + j;
+        if (j >= more || i >= rest) return false;
+        segs = 0;
+    }
+    w->walk = (int)uniform(i % A.walks);
+    i /= A.walks;
     w->x0 = (int)uniform(i % A.slices) * width;
     i /= A.slices;
-    w->h = (int)uniform(i % A.H);
-    i /= A.H;
-    w->seg = (int)uniform(i % A.walked);
-    w->b = uniform(i / A.walked);
+    const unsigned in = segs ? A.whole : A.pairs - A.whole, pair = uniform(i % in + (segs ? 0 : A.whole));
+    w->seg = (int)uniform(i / in);
+    w->nseg = segs ? 1 : A.nseg;
+    w->cps = segs ? 1 << 26 : A.cps;
+    w->b = uniform(pair / A.H);
+    w->h = (int)uniform(pair % A.H);
     w->len = (int)uniform((unsigned)attn_length(A.lens, w->b, A.L));
-    w->state = w->b * A.H + w->h;
+    w->state = pair;
+    w->slot = (int64_t)(pair - A.whole) * (A.nseg - 1);
     return true;
 }
 

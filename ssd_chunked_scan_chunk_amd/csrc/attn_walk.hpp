@@ -172,27 +172,33 @@ __device__ __forceinline__ void split3(const bf16x8& v, const float (&w)[8], con
 // (256 wide) one.
 template <int KD, int NW> constexpr int attn_steps() { return KD == 128 && NW == 4 ? 64 : 32; }
 template <int KD, int NW> constexpr int waves_per_simd() { return KD == 64 ? 4 : KD == 256 && NW == 2 ? 1 : 2; }
+template <int KD, int NW, bool FULL> struct Tiles {
+    static constexpr int C = attn_steps<KD, NW>(), XW = 32 * NW, NP = C / 32 * (C / 32 + 1) / 2;
+    __attribute__((aligned(16))) u16 sA[FULL ? 3 : 1][FULL ? C * KD : 8];
+    __attribute__((aligned(16))) u16 sK[3][C * KD];
+    __attribute__((aligned(16))) u16 sX[2][C * XW];
+    // decayed scores [i][j] in blocks of 32 x 32, (0,0), (1,1), (1,0), high parts, low parts
+    __attribute__((aligned(16))) u16 sP[FULL ? 2 : 1][FULL ? NP : 1][FULL ? 2 * 32 * 32 : 8];
+    // powers of gamma: plain, with the scale of the scores (32 zeros ahead), with that of x
+    __attribute__((aligned(16))) float sG[C + 4], sGp[32 + C], sGw[C];
+};
 template <int KD, int NW, bool FULL, bool FAST, bool EX, bool YF>
-__global__ __launch_bounds__(128 * NW, (waves_per_simd<KD, NW>())) void k_attn(const AttnArgs A) {
+__device__ __forceinline__ void walk(const AttnArgs& A, const AttnPass& P, const AttnPlace& w, Tiles<KD, NW, FULL>& T) {
     constexpr int C = attn_steps<KD, NW>(), CB = C / 32, CS = C / 16;   // steps; blocks of 32, products' steps of 16
     constexpr int NT = KD / 32, CPR = KD / 8, XW = 32 * NW, XPR = XW / 8, NP = CB * (CB + 1) / 2;
-    __shared__ __attribute__((aligned(16))) u16 sA[FULL ? 3 : 1][FULL ? C * KD : 8];
-    __shared__ __attribute__((aligned(16))) u16 sK[3][C * KD];
-    __shared__ __attribute__((aligned(16))) u16 sX[2][C * XW];
-    // decayed scores [i][j] in blocks of 32 x 32, (0,0), (1,1), (1,0), high parts, low parts
-    __shared__ __attribute__((aligned(16))) u16 sP[FULL ? 2 : 1][FULL ? NP : 1][FULL ? 2 * 32 * 32 : 8];
-    // powers of gamma: plain, with the scale of the scores (32 zeros ahead), with that of x
-    __shared__ __attribute__((aligned(16))) float sG[C + 4], sGp[32 + C], sGw[C];
-
-    AttnPlace w;
-    if (!attn_place(A, XW, &w)) return;
-    const AttnPass& P = A.p;
+    auto &sA = T.sA;
+    auto &sK = T.sK;
+    auto &sX = T.sX;
+    auto &sP = T.sP;
+    auto &sG = T.sG;
+    auto &sGp = T.sGp;
+    auto &sGw = T.sGw;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l32 = lane & 31, hi = lane >> 5;
     const int rev = P.rev;
     const int chunks = (w.len + C - 1) / C;
-    const int c0 = w.seg * A.cps, c1 = c0 + A.cps < chunks ? c0 + A.cps : chunks;
-    if (!FULL && c0 + A.cps >= chunks) return;   // no segment follows: its end is not asked for
+    const int c0 = w.seg * w.cps, c1 = c0 + w.cps < chunks ? c0 + w.cps : chunks;
+    if (!FULL && c0 + w.cps >= chunks) return;   // no segment follows: its end is not asked for
 
     // A partial chunk's steps are the last rows of its tile (rows before are zero), so
     // that what follows it by C - 1 - j steps does so there too.
@@ -356,7 +362,7 @@ __global__ __launch_bounds__(128 * NW, (waves_per_simd<KD, NW>())) void k_attn(c
     const int64_t SE = (int64_t)P.cd * P.xd;
     auto element = [&](int t, int r) { return 32 * t + 16 * (r >> 3) + 8 * hi + (r & 7); };
     const float* from = w.seg == 0 ? (P.first ? P.first + w.state * SE : nullptr)
-                      : FULL ? A.slots + (w.state * (int64_t)(A.nseg - 1) + w.seg - 1) * SE : nullptr;
+                      : FULL ? A.slots[w.walk] + (w.slot + w.seg - 1) * SE : nullptr;
     if (from && (w.seg == 0 || c0 < chunks)) {
         // read at a clamped place and dropped: a condition around each read would have it
         // wait for its own value
@@ -583,7 +589,7 @@ __global__ __launch_bounds__(128 * NW, (waves_per_simd<KD, NW>())) void k_attn(c
             save(P.last + w.state * SE, rev && chunks > 0 ? decay_pow(gamma, 1) : 1.f);
         // rows behind the sequence's end
         const int64_t e0 = c0 * C > w.len ? c0 * C : w.len;
-        const int64_t e1 = w.seg + 1 == A.nseg ? A.L : (c0 + A.cps) * C;
+        const int64_t e1 = w.seg + 1 == w.nseg ? A.L : (c0 + w.cps) * C;
         for (int64_t t = e0 + tid / XW; t < e1; t += 64 * NW / XW) {
             const int col = w.x0 + tid % XW;
             const int64_t at = ((w.b * A.L + t) * A.H + w.h) * P.xd + col;
@@ -593,30 +599,42 @@ __global__ __launch_bounds__(128 * NW, (waves_per_simd<KD, NW>())) void k_attn(c
             }
         }
     } else {
-        save(A.slots + (w.state * (int64_t)(A.nseg - 1) + w.seg) * SE, 1.f);
+        save(A.slots[w.walk] + (w.slot + w.seg) * SE, 1.f);
     }
 }
 
-template <bool FULL, bool FAST, bool EX, bool YF> hipError_t launch(const AttnArgs& A, hipStream_t st) {
-    const unsigned grid = (unsigned)((A.items + kXcds - 1) / kXcds * kXcds);
-    const int kd = attn_width(A.p.cd);   // attn_chunk() goes by it too
-    if (attn_columns(A.p.xd) == 128) {
-        if (kd == 64) k_attn<64, 4, FULL, FAST, EX, YF><<<grid, 512, 0, st>>>(A);
-        else if (kd == 128) k_attn<128, 4, FULL, FAST, EX, YF><<<grid, 512, 0, st>>>(A);
-        else k_attn<256, 4, FULL, FAST, EX, YF><<<grid, 512, 0, st>>>(A);
+// Each of a launch's walks has its own EX and YF.
+template <int KD, int NW, bool FULL, bool FAST>
+__global__ __launch_bounds__(128 * NW, (waves_per_simd<KD, NW>())) void k_attn(const AttnArgs A) {
+    __shared__ Tiles<KD, NW, FULL> T;
+    AttnPlace w;
+    if (!attn_place(A, 32 * NW, &w)) return;
+    const AttnPass& P = A.p[w.walk];
+    if (FULL && P.y_f32) {
+        if (P.exact) walk<KD, NW, FULL, FAST, true, true>(A, P, w, T);
+        else walk<KD, NW, FULL, FAST, false, true>(A, P, w, T);
     } else {
-        if (kd == 64) k_attn<64, 2, FULL, FAST, EX, YF><<<grid, 256, 0, st>>>(A);
-        else if (kd == 128) k_attn<128, 2, FULL, FAST, EX, YF><<<grid, 256, 0, st>>>(A);
-        else k_attn<256, 2, FULL, FAST, EX, YF><<<grid, 256, 0, st>>>(A);
+        if (P.exact) walk<KD, NW, FULL, FAST, true, false>(A, P, w, T);
+        else walk<KD, NW, FULL, FAST, false, false>(A, P, w, T);
+    }
+}
+
+template <bool FULL, bool FAST> hipError_t launch(const AttnArgs& A, hipStream_t st) {
+    const unsigned grid = attn_grid(A);
+    const int kd = attn_width(A.p[0].cd);   // attn_chunk() goes by it too
+    if (attn_columns(A.p[0].xd) == 128) {
+        if (kd == 64) k_attn<64, 4, FULL, FAST><<<grid, 512, 0, st>>>(A);
+        else if (kd == 128) k_attn<128, 4, FULL, FAST><<<grid, 512, 0, st>>>(A);
+        else k_attn<256, 4, FULL, FAST><<<grid, 512, 0, st>>>(A);
+    } else {
+        if (kd == 64) k_attn<64, 2, FULL, FAST><<<grid, 256, 0, st>>>(A);
+        else if (kd == 128) k_attn<128, 2, FULL, FAST><<<grid, 256, 0, st>>>(A);
+        else k_attn<256, 2, FULL, FAST><<<grid, 256, 0, st>>>(A);
     }
     return hipGetLastError();
 }
-template <bool FAST, bool EX> hipError_t launch(const AttnArgs& A, bool full, hipStream_t st) {
-    if (!full) return launch<false, FAST, EX, false>(A, st);
-    return A.p.y_f32 ? launch<true, FAST, EX, true>(A, st) : launch<true, FAST, EX, false>(A, st);
-}
 template <bool FAST> hipError_t launch(const AttnArgs& A, bool full, hipStream_t st) {
-    return A.p.exact ? launch<FAST, true>(A, full, st) : launch<FAST, false>(A, full, st);
+    return full ? launch<true, FAST>(A, st) : launch<false, FAST>(A, st);
 }
 
 }  // namespace

@@ -12,9 +12,12 @@ static bool whole_pieces(const void* p, int64_t bs, uint32_t rs, int d) {
 hipError_t launch_attn_any(const AttnArgs& A, bool full, hipStream_t st);
 
 hipError_t launch_attn_bf16(const AttnArgs& A, bool full, hipStream_t st) {
-    const AttnPass& p = A.p;
-    const bool whole = (!full || (whole_pieces(p.a, p.ab, p.ar, p.cd) && reinterpret_cast<uintptr_t>(p.y) % 16 == 0)) &&
-                       whole_pieces(p.c, p.cb, p.cr, p.cd) && whole_pieces(p.x, p.xb, p.xr, p.xd);
+    bool whole = true;
+    for (unsigned i = 0; i < A.walks; ++i) {
+        const AttnPass& p = A.p[i];
+        whole = whole && whole_pieces(p.c, p.cb, p.cr, p.cd) && whole_pieces(p.x, p.xb, p.xr, p.xd);
+        if (full) whole = whole && whole_pieces(p.a, p.ab, p.ar, p.cd) && reinterpret_cast<uintptr_t>(p.y) % 16 == 0;
+    }
     return whole ? launch<true>(A, full, st) : launch_attn_any(A, full, st);
 }
 

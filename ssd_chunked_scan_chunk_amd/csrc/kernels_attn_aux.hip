@@ -7,17 +7,29 @@ namespace {
 
 // The states at the segments' ends, each from nothing but the first, to the states that
 // the next segments start from: one thread walks an element over the segments.
-__global__ __launch_bounds__(256) void k_attn_join(float* slots, const float* log_decay, const int32_t* lens, int64_t L,
-                                                   int64_t H, int64_t nslots, int64_t steps, int64_t SE, unsigned blocks) {
-    const int64_t s = blockIdx.x / blocks, e = (int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x;
+__global__ __launch_bounds__(256) void k_attn_join(float* slots0, float* slots1, const float* log_decay,
+                                                   const int32_t* lens, int64_t L, int64_t H, int64_t whole,
+                                                   int64_t nslots, int64_t steps, int64_t SE, unsigned blocks) {
+    float* slots = blockIdx.y ? slots1 : slots0;
+    const int64_t i = blockIdx.x / blocks, s = whole + i, e = (int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x;
     if (e >= SE) return;
     const int64_t len = attn_length(lens, s / H, L);
     const float f = decay_pow(log2_decay(log_decay[s % H]), (int)steps);   // every segment that another follows is whole
-    float* p = slots + s * nslots * SE + e;
+    float* p = slots + i * nslots * SE + e;
+    // as many as have steps after them; eight reads in flight
+    int64_t n = len > 0 ? (len - 1) / steps : 0;
+    if (n > nslots) n = nslots;
     float carry = 0.f;
-    for (int64_t k = 0; k < nslots && (k + 1) * steps < len; ++k) {
-        carry = k == 0 ? p[0] : fmaf(f, carry, p[k * SE]);
-        p[k * SE] = carry;
+    for (int64_t k = 0; k < n; k += 8) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = p[(k + j < n ? k + j : n - 1) * SE];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (k + j >= n) break;
+            carry = k + j == 0 ? v[0] : fmaf(f, carry, v[j]);
+            p[(k + j) * SE] = carry;
+        }
     }
 }
 
@@ -103,33 +115,59 @@ __global__ __launch_bounds__(256) void k_attn_step(float* state, const T* q, con
 hipError_t launch_attn_bf16(const AttnArgs& A, bool full, hipStream_t st);
 hipError_t launch_attn_f32(const AttnArgs& A, bool full, hipStream_t st);
 
-static AttnArgs attn_args(const AttnShape& s, const AttnPlan& pl, const AttnPass& p, const float* log_decay,
-                          const int32_t* lens, float* slots, int64_t segs) {
-    AttnArgs A;
-    A.p = p; A.log_decay = log_decay; A.lens = lens; A.slots = slots;
-    A.L = s.L; A.cps = (int)((pl.steps + attn_chunk(s.bf16, p.cd, p.xd) - 1) / attn_chunk(s.bf16, p.cd, p.xd)); A.nseg = (int)pl.nseg; A.walked = (unsigned)segs; A.H = (unsigned)s.H;
-    A.slices = (unsigned)attn_slices(p.xd);
-    A.items = (unsigned)(s.Bz * s.H * A.slices * segs);
-    return A;
+static hipError_t launch_walks(const AttnShape& s, const AttnPlan& pl, const AttnPass* p, float* const* slots, int n,
+                               const float* log_decay, const int32_t* lens, bool full, hipStream_t st) {
+    AttnArgs A = {};
+    const int64_t chunk = attn_chunk(s.bf16, p[0].cd, p[0].xd);
+    for (int i = 0; i < n; ++i) {
+        A.p[i] = p[i];
+        A.slots[i] = slots[i];
+    }
+    A.log_decay = log_decay; A.lens = lens; A.L = s.L;
+    A.cps = (int)((pl.steps + chunk - 1) / chunk);
+    A.nseg = (int)pl.nseg;
+    A.walks = (unsigned)n; A.H = (unsigned)s.H;
+    A.slices = (unsigned)attn_slices(p[0].xd);
+    A.pairs = (unsigned)(s.Bz * s.H);
+    A.whole = (unsigned)pl.whole;
+    A.segs = (unsigned)(full ? pl.nseg : pl.nseg - 1);
+    if (!full) A.skip_whole = 1;
+    return s.bf16 ? launch_attn_bf16(A, full, st) : launch_attn_f32(A, full, st);
 }
 
-hipError_t launch_attn_states(const AttnShape& s, const AttnPlan& pl, const AttnPass& p, const float* log_decay,
-                              const int32_t* lens, float* slots, hipStream_t st) {
-    if (pl.nseg < 2) return hipSuccess;
-    AttnArgs A = attn_args(s, pl, p, log_decay, lens, slots, pl.nseg - 1);
-    const hipError_t e = s.bf16 ? launch_attn_bf16(A, false, st) : launch_attn_f32(A, false, st);
+// walks whose rows have the same sizes share a launch
+static bool same_instance(const AttnPass& p, const AttnPass& q) {
+    return attn_width(p.cd) == attn_width(q.cd) && attn_columns(p.xd) == attn_columns(q.xd) &&
+           attn_slices(p.xd) == attn_slices(q.xd);
+}
+static hipError_t launch_grouped(const AttnShape& s, const AttnPlan& pl, const AttnPass* p, float* const* slots, int n,
+                                 const float* log_decay, const int32_t* lens, bool full, hipStream_t st) {
+    for (int i = 0; i < n;) {
+        int k = i + 1;
+        while (k < n && same_instance(p[i], p[k])) ++k;
+        const hipError_t e = launch_walks(s, pl, p + i, slots + i, k - i, log_decay, lens, full, st);
+        if (e != hipSuccess) return e;
+        i = k;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_attn_states(const AttnShape& s, const AttnPlan& pl, const AttnPass* p, float* const* slots, int n,
+                              const float* log_decay, const int32_t* lens, hipStream_t st) {
+    const int64_t cut = s.Bz * s.H - pl.whole;
+    if (pl.nseg < 2 || cut < 1) return hipSuccess;
+    const hipError_t e = launch_grouped(s, pl, p, slots, n, log_decay, lens, false, st);
     if (e != hipSuccess) return e;
     const int64_t SE = s.Dk * s.Dv;
     const unsigned blocks = (unsigned)((SE + 255) / 256);
-    k_attn_join<<<(unsigned)(s.Bz * s.H) * blocks, 256, 0, st>>>(slots, log_decay, lens, s.L, s.H, pl.nseg - 1,
-                                                                 pl.steps, SE, blocks);
+    k_attn_join<<<dim3((unsigned)cut * blocks, (unsigned)n), 256, 0, st>>>(
+        slots[0], n > 1 ? slots[1] : nullptr, log_decay, lens, s.L, s.H, pl.whole, pl.nseg - 1, pl.steps, SE, blocks);
     return hipGetLastError();
 }
 
-hipError_t launch_attn_pass(const AttnShape& s, const AttnPlan& pl, const AttnPass& p, const float* log_decay,
-                            const int32_t* lens, const float* slots, hipStream_t st) {
-    const AttnArgs A = attn_args(s, pl, p, log_decay, lens, const_cast<float*>(slots), pl.nseg);
-    return s.bf16 ? launch_attn_bf16(A, true, st) : launch_attn_f32(A, true, st);
+hipError_t launch_attn_walks(const AttnShape& s, const AttnPlan& pl, const AttnPass* p, float* const* slots, int n,
+                             const float* log_decay, const int32_t* lens, hipStream_t st) {
+    return launch_grouped(s, pl, p, slots, n, log_decay, lens, true, st);
 }
 
 hipError_t launch_attn_share(const float* in, void* out, int64_t rows, int64_t H, int64_t K, int64_t D, bool bf16,

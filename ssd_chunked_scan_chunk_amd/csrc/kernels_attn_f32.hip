@@ -56,13 +56,13 @@ __global__ __launch_bounds__(64 * NW, KD > 128 ? 1 : 2) void k_attn_f32(const At
 
     AttnPlace w;
     if (!attn_place(A, XW, &w)) return;
-    const AttnPass& P = A.p;
+    const AttnPass& P = A.p[w.walk];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int l32 = lane & 31, hi = lane >> 5;
     const int rev = P.rev;
     const int chunks = (w.len + kC - 1) / kC;
-    const int c0 = w.seg * A.cps, c1 = c0 + A.cps < chunks ? c0 + A.cps : chunks;
-    if (!FULL && c0 + A.cps >= chunks) return;   // no segment follows: its end is not asked for
+    const int c0 = w.seg * w.cps, c1 = c0 + w.cps < chunks ? c0 + w.cps : chunks;
+    if (!FULL && c0 + w.cps >= chunks) return;   // no segment follows: its end is not asked for
     const Decay g = log2_decay(A.log_decay[w.h]);
 
     // columns and state rows in the order of kernels_attn.hip: a lane's registers 8h .. 8h+7
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(64 * NW, KD > 128 ? 1 : 2) void k_attn_f32(const At
     const int64_t SE = (int64_t)P.cd * P.xd;
     auto element = [&](int nt, int r) { return 32 * nt + 16 * (r >> 3) + 8 * hi + (r & 7); };
     const float* from = w.seg == 0 ? (P.first ? P.first + w.state * SE : nullptr)
-                      : FULL ? A.slots + (w.state * (int64_t)(A.nseg - 1) + w.seg - 1) * SE : nullptr;
+                      : FULL ? A.slots[w.walk] + (w.slot + w.seg - 1) * SE : nullptr;
     if (from && (w.seg == 0 || c0 < chunks)) {
         // read at a clamped place and dropped: a condition around each read would have it
         // wait for its own value
@@ -227,19 +227,19 @@ __global__ __launch_bounds__(64 * NW, KD > 128 ? 1 : 2) void k_attn_f32(const At
         if (P.last && (chunks > 0 ? c0 < chunks && c1 == chunks : w.seg == 0))
             save(P.last + w.state * SE, rev && chunks > 0 ? decay_pow(g, 1) : 1.f);
         const int64_t e0 = c0 * kC > w.len ? c0 * kC : w.len;
-        const int64_t e1 = w.seg + 1 == A.nseg ? A.L : (c0 + A.cps) * kC;
+        const int64_t e1 = w.seg + 1 == w.nseg ? A.L : (c0 + w.cps) * kC;
         for (int64_t t = e0 + tid / XW; t < e1; t += NTH / XW) {
             const int x = w.x0 + tid % XW;
             if (x < P.xd) static_cast<float*>(P.y)[((w.b * A.L + t) * A.H + w.h) * P.xd + x] = 0.f;
         }
     } else {
-        save(A.slots + (w.state * (int64_t)(A.nseg - 1) + w.seg) * SE, 1.f);
+        save(A.slots[w.walk] + (w.slot + w.seg) * SE, 1.f);
     }
 }
 
 template <bool FULL, int KD>
 hipError_t launch(const AttnArgs& A, unsigned grid, hipStream_t st) {
-    if (attn_columns(A.p.xd) == 128) k_attn_f32<KD, 4, FULL><<<grid, 256, 0, st>>>(A);
+    if (attn_columns(A.p[0].xd) == 128) k_attn_f32<KD, 4, FULL><<<grid, 256, 0, st>>>(A);
     else k_attn_f32<KD, 2, FULL><<<grid, 128, 0, st>>>(A);
     return hipGetLastError();
 }
@@ -247,8 +247,8 @@ hipError_t launch(const AttnArgs& A, unsigned grid, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_attn_f32(const AttnArgs& A, bool full, hipStream_t st) {
-    const unsigned grid = (unsigned)((A.items + kXcds - 1) / kXcds * kXcds);
-    switch (attn_width(A.p.cd)) {
+    const unsigned grid = attn_grid(A);
+    switch (attn_width(A.p[0].cd)) {
         case 64: return full ? launch<true, 64>(A, grid, st) : launch<false, 64>(A, grid, st);
         case 128: return full ? launch<true, 128>(A, grid, st) : launch<false, 128>(A, grid, st);
         default: return full ? launch<true, 256>(A, grid, st) : launch<false, 256>(A, grid, st);

@@ -164,20 +164,54 @@ ChanBwdPlan chan_bwd_plan(const ChanShape& s) {
     return p;
 }
 
-// Segments of the linear attention's walks: two workgroups per CU, segments of four
-// chunks or more.
+// Segments of the linear attention's walks.  A walk of an instance takes `few` us for 64 steps
+// where its workgroups have the GPU nearly to themselves, `few` + `more` where `slots` of them
+// fill it, and `ends` where it only makes the segments' end states.  Fitted on MI355X to the
+// forward and the backward of 1 x 32768 to 8 x 2048 steps and 12 to 64 heads (bf16,
+// 128 x 128: 8 x 2048 x 32 heads 139 us, 1 x 32768 x 12 in 16, 21 and 40 segments 173, 160 and
+// 183 us, its backward in 7 and 21 390 and 404 us; within 8%).  What a last round that does
+// not fill the GPU would hold may be cut into segments while the rest stays whole: 8 x 2048 x 40
+// heads 223 us whole, 203 us with 64 pairs in four.
 AttnPlan attn_plan(const AttnShape& s, bool bwd) {
+    struct Rate { double few, more, ends; int64_t slots; };
+    const int kd = attn_width(s.Dk > s.Dv && bwd ? s.Dk : bwd ? s.Dv : s.Dk);
+    const bool narrow = attn_columns(bwd && s.Dk > s.Dv ? s.Dk : s.Dv) == 64;
+    const Rate bf16 = kd == 256             ? Rate{5.0, 2.6, 3.0, 256}
+                      : kd == 128 && !narrow ? Rate{3.0, 1.2, 1.6, 256}
+                      : kd == 64 && narrow   ? Rate{2.5, 2.8, 1.5, 768}
+                                             : Rate{3.0, 3.0, 1.8, 512};
+    const Rate f32 = kd == 256 ? Rate{30, 5, 15, 256} : kd == 128 ? Rate{12, 6, 6, 512} : Rate{6, 5, 3, 768};
+    const Rate& t = s.bf16 ? bf16 : f32;
     AttnPlan p = {};
-    const int64_t chunks = (s.L + 63) / 64;
-    const int64_t fewer = bwd && attn_slices(s.Dk) < attn_slices(s.Dv) ? attn_slices(s.Dk) : attn_slices(s.Dv);
-    const int64_t items = s.Bz * s.H * fewer > 0 ? s.Bz * s.H * fewer : 1;
-    int64_t want = (512 + items - 1) / items;
-    if (want > chunks / 4) want = chunks / 4;
-    if (want < 1) want = 1;
-    const int64_t each = chunks > 0 ? (chunks + want - 1) / want : 1;
+    const int64_t chunks = (s.L + 63) / 64, pairs = s.Bz * s.H, walks = bwd ? 3 : 1;
+    const int64_t slices = attn_slices(s.Dk) > attn_slices(s.Dv) && bwd ? attn_slices(s.Dk) : attn_slices(s.Dv);
+    const int64_t per = slices * walks;                       // workgroups of a whole pair
+    auto time = [&](int64_t groups, int64_t steps64, double few, double more) {
+        const int64_t rounds = groups / t.slots, left = groups % t.slots;
+        return (double)steps64 * ((double)rounds * (few + more) +
+                                  (left ? few + more * (double)left / (double)t.slots : 0.0));
+    };
+    double least = 1e300;
+    int64_t each = chunks > 0 ? chunks : 1;
+    for (int64_t n = 1; n <= 512 && pairs > 0 && chunks > 0 && (n == 1 || 2 * n <= chunks); ++n) {
+        const int64_t e = (chunks + n - 1) / n, segs = (chunks + e - 1) / e;
+        for (int64_t whole : {(int64_t)0, pairs * per / t.slots * t.slots / per}) {
+            const int64_t cut = pairs - whole;
+            double us = time(whole * per, chunks, t.few, t.more) + time(cut * segs * per, e, t.few, t.more);
+            if (segs > 1 && cut > 0)
+                us += time(cut * (segs - 1) * slices * (bwd ? 2 : 1), e, t.ends, 0.2 * t.ends) + 11 + 0.15 * (double)segs +
+                      (double)(cut * (segs - 1) * s.Dk * s.Dv * (bwd ? 2 : 1)) * 8 / 4.5e6;
+            if (us < least * (n > 1 ? 0.97 : 1.0)) {
+                least = us;
+                each = e;
+                p.whole = segs > 1 ? whole : 0;
+            }
+        }
+    }
     p.steps = 64 * each;
     p.nseg = chunks > 0 ? (chunks + each - 1) / each : 1;
-    const size_t state = (size_t)(s.Bz * s.H * (p.nseg - 1) * s.Dk * s.Dv) * sizeof(float);
+    if (p.nseg == 1) p.whole = pairs;
+    const size_t state = (size_t)((pairs - p.whole) * (p.nseg - 1) * s.Dk * s.Dv) * sizeof(float);
     const size_t rows = bwd && s.K != s.H ? (size_t)(s.Bz * s.L * s.H) * sizeof(float) : 0;
     auto take = [&](size_t n) {
         const size_t at = p.bytes;

@@ -77,10 +77,10 @@ hipError_t launch_chan_fwd(const ChanShape&, const ChanPlan&, const ChanIn&, voi
 hipError_t launch_chan_bwd(const ChanShape&, const ChanBwdPlan&, const ChanIn&, const void*, const float*,
                            const ChanGrads&, void*, hipStream_t) { SSD_STUB; }
 hipError_t launch_chan_step(const ChanShape&, float*, const ChanIn&, void*, hipStream_t) { SSD_STUB; }
-hipError_t launch_attn_states(const AttnShape&, const AttnPlan&, const AttnPass&, const float*, const int32_t*, float*,
-                              hipStream_t) { SSD_STUB; }
-hipError_t launch_attn_pass(const AttnShape&, const AttnPlan&, const AttnPass&, const float*, const int32_t*,
-                            const float*, hipStream_t) { SSD_STUB; }
+hipError_t launch_attn_states(const AttnShape&, const AttnPlan&, const AttnPass*, float* const*, int, const float*,
+                              const int32_t*, hipStream_t) { SSD_STUB; }
+hipError_t launch_attn_walks(const AttnShape&, const AttnPlan&, const AttnPass*, float* const*, int, const float*,
+                             const int32_t*, hipStream_t) { SSD_STUB; }
 hipError_t launch_attn_share(const float*, void*, int64_t, int64_t, int64_t, int64_t, bool, hipStream_t) { SSD_STUB; }
 hipError_t launch_attn_step(const AttnShape&, float*, const void*, const void*, const void*, const float*, void*,
                             hipStream_t) { SSD_STUB; }
