@@ -68,6 +68,7 @@ template <bool BLOCK> struct Sums {
     }
 };
 
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 template <typename T, int V> struct Vec;
 template <> struct Vec<u16, 8> {
     typedef u16 raw __attribute__((ext_vector_type(8), aligned(2)));
@@ -87,9 +88,11 @@ template <typename T> __device__ __forceinline__ float sigmoid_as(float x) {
     return x >= 0.f ? d : e * d;
 }
 
-// GATE: 0 none, 1 after the norm, 2 before it.
-template <typename T, int V, int NP, bool BLOCK, int GATE, bool BWD>
-__global__ __launch_bounds__(BLOCK ? 1024 : 512) void k_norm(const NormArgs A) {
+// GATE: 0 none, 1 after the norm, 2 before it.  WHOLE: a group is a whole number of pieces;
+// otherwise its last one starts early and its first `skip` elements are another thread's
+// (with that test at every element the bf16 backward needs 121 registers and 10% longer).
+template <typename T, int V, int NP, bool BLOCK, int GATE, bool BWD, bool WHOLE>
+__global__ __launch_bounds__(BLOCK ? 1024 : 512, BWD ? 4 : 1) void k_norm(const NormArgs A) {
     using R = typename Vec<T, V>::raw;
     __shared__ float lds[BLOCK ? 64 : 1];
     const int tid = threadIdx.x;
@@ -99,7 +102,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 512) void k_norm(const NormArgs A) {
     const int group = blockIdx.x * A.gw + slot % A.gw, rowat = slot / A.gw;
     const bool on = group < A.G && rowat < A.rw;
     const int64_t ch = (int64_t)(on ? group : 0) * A.m;
-    int at[NP], skip[NP];          // elements skip .. V-1 of a piece are the thread's own
+    int at[NP], skip[NP];          // elements skip .. V-1 of a piece are the thread's own; WHOLE: all or none
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
         const int col = (first + k * stride) * V, most = A.m - V;
@@ -119,28 +122,45 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 512) void k_norm(const NormArgs A) {
     const int64_t step = (int64_t)gridDim.y * A.rw;
     R xr[NP], zr[NP], dr[NP];
     bool live = false;
+    auto own = [&](int k, int e) { return WHOLE ? skip[k] == 0 : e >= skip[k]; };
+    auto read = [&](const T* p, R (&to)[NP]) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) to[k] = *reinterpret_cast<const R*>(p + at[k]);
+    };
+    // in fp32; rows that are not there, and pieces of no group, are zeros
+    auto values = [&](const R (&from)[NP], bool here, float (&v)[NP][V]) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            if constexpr (WHOLE && V > 1) {
+                u32x4 w = __builtin_bit_cast(u32x4, from[k]);
+                const uint32_t mask = here && skip[k] == 0 ? 0xffffffffu : 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    w[j] &= mask;
+                    if constexpr (V == 8) {
+                        v[k][2 * j] = __uint_as_float(w[j] << 16);
+                        v[k][2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                    } else {
+                        v[k][j] = __uint_as_float(w[j]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[k][e] = here && own(k, e) ? as_f32(from[k][e]) : 0.f;
+            }
+        }
+    };
     auto fetch = [&](int64_t row) {
-        if (row >= A.rows) { live = false; return; }
         int64_t b = 0, t = row;
         if (!A.flat) {
             b = (uint32_t)row / (uint32_t)A.L;
             t = row - b * A.L;
         }
-        live = !A.lens || t < A.lens[b];
+        live = row < A.rows && (!A.lens || t < A.lens[b]);
         if (!live) return;
-        const T* x = static_cast<const T*>(A.x) + b * A.xb + t * A.xr + ch;
-#pragma unroll
-        for (int k = 0; k < NP; ++k) xr[k] = *reinterpret_cast<const R*>(x + at[k]);
-        if constexpr (GATE != 0) {
-            const T* z = static_cast<const T*>(A.gate) + b * A.zb + t * A.zr + ch;
-#pragma unroll
-            for (int k = 0; k < NP; ++k) zr[k] = *reinterpret_cast<const R*>(z + at[k]);
-        }
-        if constexpr (BWD) {
-            const T* d = static_cast<const T*>(A.dy) + row * A.C + ch;
-#pragma unroll
-            for (int k = 0; k < NP; ++k) dr[k] = *reinterpret_cast<const R*>(d + at[k]);
-        }
+        read(static_cast<const T*>(A.x) + b * A.xb + t * A.xr + ch, xr);
+        if constexpr (GATE != 0) read(static_cast<const T*>(A.gate) + b * A.zb + t * A.zr + ch, zr);
+        if constexpr (BWD) read(static_cast<const T*>(A.dy) + row * A.C + ch, dr);
     };
     auto put = [&](void* to, int64_t row, const float (&v)[NP][V]) {
         T* p = static_cast<T*>(to) + row * A.C + ch;
@@ -150,7 +170,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 512) void k_norm(const NormArgs A) {
 #pragma unroll
             for (int e = 0; e < V; ++e) o[e] = to_elem(v[k][e], T{});
             if (skip[k] == 0) *reinterpret_cast<R*>(p + at[k]) = o;
-            else if (skip[k] < V) {
+            else if (!WHOLE && skip[k] < V) {
 #pragma unroll
                 for (int e = 1; e < V; ++e)
                     if (e >= skip[k]) p[at[k] + e] = o[e];
@@ -165,14 +185,9 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 512) void k_norm(const NormArgs A) {
     for (int64_t i = 0; i < turns; ++i, row += step) {
         const bool here = live, in = row < A.rows;
         float x[NP][V], z[NP][V], d[NP][V];
-#pragma unroll
-        for (int k = 0; k < NP; ++k)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                x[k][e] = here && e >= skip[k] ? as_f32(xr[k][e]) : 0.f;
-                z[k][e] = GATE != 0 && here && e >= skip[k] ? as_f32(zr[k][e]) : 0.f;
-                d[k][e] = BWD && here && e >= skip[k] ? as_f32(dr[k][e]) : 0.f;
-            }
+        values(xr, here, x);
+        if constexpr (GATE != 0) values(zr, here, z);
+        if constexpr (BWD) values(dr, here, d);
         if (i + 1 < turns) fetch(row + step);
 
         // ---- the normalised row ----
@@ -195,7 +210,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 512) void k_norm(const NormArgs A) {
 #pragma unroll
             for (int k = 0; k < NP; ++k)
 #pragma unroll
-                for (int e = 0; e < V; ++e) n[k][e] = e >= skip[k] ? n[k][e] - mean : 0.f;
+                for (int e = 0; e < V; ++e) n[k][e] = own(k, e) ? n[k][e] - mean : 0.f;
         }
         float sq = 0.f;
 #pragma unroll
@@ -203,7 +218,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 512) void k_norm(const NormArgs A) {
 #pragma unroll
             for (int e = 0; e < V; ++e) sq = fmaf(n[k][e], n[k][e], sq);
         sums(sq, other, false);
-        const float r = rsqrtf(fmaf(sq, inv, A.eps));
+        const float r = here ? rsqrtf(fmaf(sq, inv, A.eps)) : 0.f;   // zeros of eps 0 have none
 #pragma unroll
         for (int k = 0; k < NP; ++k)
 #pragma unroll
@@ -271,7 +286,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 512) void k_norm(const NormArgs A) {
         for (int k = 0; k < NP; ++k)
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                if (e >= skip[k]) {
+                if (own(k, e)) {
                     p[at[k] + e] = dw[k][e];
                     p[A.C + at[k] + e] = db[k][e];
                 }
@@ -306,11 +321,16 @@ __global__ __launch_bounds__(256) void k_norm_params(const float* parts, int64_t
     }
 }
 
+template <typename T, int V, int NP, bool BLOCK, bool BWD, bool WHOLE>
+void go(const NormArgs& A, int gate, dim3 grid, int threads, hipStream_t st) {
+    if (gate == 0) k_norm<T, V, NP, BLOCK, 0, BWD, WHOLE><<<grid, threads, 0, st>>>(A);
+    else if (gate == 1) k_norm<T, V, NP, BLOCK, 1, BWD, WHOLE><<<grid, threads, 0, st>>>(A);
+    else k_norm<T, V, NP, BLOCK, 2, BWD, WHOLE><<<grid, threads, 0, st>>>(A);
+}
 template <typename T, int V, int NP, bool BLOCK, bool BWD>
 void go(const NormArgs& A, int gate, dim3 grid, int threads, hipStream_t st) {
-    if (gate == 0) k_norm<T, V, NP, BLOCK, 0, BWD><<<grid, threads, 0, st>>>(A);
-    else if (gate == 1) k_norm<T, V, NP, BLOCK, 1, BWD><<<grid, threads, 0, st>>>(A);
-    else k_norm<T, V, NP, BLOCK, 2, BWD><<<grid, threads, 0, st>>>(A);
+    if (A.m % V == 0) go<T, V, NP, BLOCK, BWD, true>(A, gate, grid, threads, st);
+    else if constexpr (V > 1) go<T, V, NP, BLOCK, BWD, false>(A, gate, grid, threads, st);
 }
 
 template <typename T, bool BWD> hipError_t run(const NormShape& s, const NormLayout& l, const NormArgs& A, hipStream_t st) {
