@@ -38,9 +38,9 @@ ssd_status attn_shape(const ssd_linear_attn_desc* d, ssd::AttnShape* s) {
         if (*r > kMaxRow) return fail(SSD_ERR_UNSUPPORTED, "step strides must be at most 2^24 elements");
     }
     if (s->H * 256 > kMaxRow) return fail(SSD_ERR_UNSUPPORTED, "nheads too large");
-    // grids: 256 threads for every (batch, head) and up to four slices of columns; segments
-    // are made only where these are few
-    if (s->Bz * s->H * 4 * 256 >= ((int64_t)1 << 32))
+    // grids: up to 512 threads for each of two slices of columns of the backward's three walks
+    // of every (batch, head); a plan keeps what it cuts into segments below this as well
+    if (s->Bz * s->H > ssd::kAttnGroups / 6)
         return fail(SSD_ERR_UNSUPPORTED, "batch*nheads too large for one launch");
     return SSD_OK;
 }

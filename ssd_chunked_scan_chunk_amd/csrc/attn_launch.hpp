@@ -7,6 +7,9 @@
 
 namespace ssd {
 
+// The most workgroups of a launch: 512 threads each, 2^32 items at most.
+constexpr int64_t kAttnGroups = ((int64_t)1 << 23) - 1;
+
 // ---- linear attention (kernels_attn*.hip) ----------------------------------------
 struct AttnShape {
     int64_t Bz, L, H, K;                 // K: heads of k and v

@@ -197,6 +197,8 @@ AttnPlan attn_plan(const AttnShape& s, bool bwd) {
         const int64_t e = (chunks + n - 1) / n, segs = (chunks + e - 1) / e;
         for (int64_t whole : {(int64_t)0, pairs * per / t.slots * t.slots / per}) {
             const int64_t cut = pairs - whole;
+            // the walks' workgroups, and the join's: 256 threads for 256 numbers of a state
+            if (segs > 1 && (cut > kAttnGroups / (segs * per) || cut > kAttnGroups / 256)) continue;
             double us = time(whole * per, chunks, t.few, t.more) + time(cut * segs * per, e, t.few, t.more);
             if (segs > 1 && cut > 0)
                 us += time(cut * (segs - 1) * slices * (bwd ? 2 : 1), e, t.ends, 0.2 * t.ends) + 11 + 0.15 * (double)segs +
@@ -263,8 +265,7 @@ NormLayout norm_layout(const NormShape& s, bool bwd) {
     return l;
 }
 int64_t norm_bwd_parts(const NormShape& s) {
-    const NormLayout l = norm_layout(s, true);
-    return l.down * l.rw;
+    return norm_layout(s, true).down;
 }
 
 }  // namespace ssd

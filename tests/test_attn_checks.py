@@ -276,3 +276,12 @@ def test_norm_pointers(lib):
     assert norm_bwd(lib, d, dgate=F[5]) == X and norm_bwd(lib, d, dw=F[9]) == X
     assert norm_fwd(lib, None) == N and lib.ssd_group_norm_bwd_workspace_bytes(d, None) == N
     assert norm_fwd(lib, norm_desc(batch=0), x=None, gate=None, y=None) == _lib.SSD_OK
+
+
+@pytest.mark.parametrize("batch,nheads,fits", [(1, 1000, True), (65535, 21, True), (65535, 22, False), (22, 65535, False)])
+def test_attn_launch_size(lib, batch, nheads, fits):
+    # 512 threads for each of two slices and three walks of a pair: at most 2^32 items of a launch
+    d, size = attn_desc(batch=batch, seqlen=1, nheads=nheads, kv_heads=1, key_dim=1, value_dim=1), ctypes.c_size_t()
+    for name in ("fwd", "bwd"):
+        code = getattr(lib, "ssd_linear_attn_%s_workspace_bytes" % name)(ctypes.byref(d), ctypes.byref(size))
+        assert code == (0 if fits else _lib.SSD_ERR_UNSUPPORTED)

@@ -279,3 +279,30 @@ def test_a_layer_of_them():
     h = 1e-6
     num = (loss(base + h * u) - loss(base - h * u)) / (2 * h)
     assert abs(num - (ours * u).sum()) <= 1e-4 * np.abs(ours * u).sum()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("L,C,groups", [(3000, 2, 2), (2500, 64, 8), (1500, 120, 1), (700, 24, 3), (257, 3, 1)])
+def test_many_rows_of_few_channels(dtype, L, C, groups):
+    # rows beside each other in a workgroup, whose parameters' gradients it adds up itself
+    log("group norm many rows %s" % ((dtype, L, C, groups),))
+    for form in ("gate", "plain"):
+        d = inputs(2, L, C, dtype, seed=C, gate=form == "gate")
+        both(d, groups, dtype, [L, L // 2 + 1])
+
+
+@pytest.mark.parametrize("gate_first", [False, True])
+@pytest.mark.parametrize("gate", [False, True])
+def test_padding_is_zero_whatever_the_parameters(gate, gate_first):
+    # eps 0, and parameters that are not finite: rows behind the end are zeros all the same
+    if gate_first and not gate:
+        return
+    log("group norm padding")
+    for C, groups in ((96, 3), (1200, 1), (6, 3)):
+        d = inputs(2, 9, C, "bf16", seed=1, gate=gate)
+        d["weight"][:2] = float("inf")
+        d["bias"][1:3] = float("nan")
+        got = calls(d, groups, [9, 4], eps=0.0, gate_first=gate_first)
+        torch.cuda.synchronize()
+        for name in ("y", "dx") + (("dgate",) if gate else ()):
+            assert not got[name][1, 4:].any(), name
