@@ -1,6 +1,6 @@
 // attn_util.hpp -- device-side pieces shared by the linear attention kernels: rows
-// loaded 16 bytes at a time at any alignment and length, the walk's bookkeeping,
-// and the states' places in memory.
+// loaded 16 bytes at a time at any alignment and length, the walk's bookkeeping, the
+// states' places in memory, tiles in LDS, and values as sums of bf16 parts.
 #pragma once
 #include "attn_launch.hpp"
 #include "mfma_util.hpp"
@@ -136,6 +136,75 @@ __device__ __forceinline__ bool attn_place(const AttnArgs& A, int width, AttnPla
     w->state = pair;
     w->slot = (int64_t)(pair - A.whole) * (A.nseg - 1);
     return true;
+}
+
+// Places in a tile of rows of PR 16-byte pieces, swizzled.
+template <int PR> __device__ __forceinline__ int tile_bits(int r) { return swzbits<(PR > 16 ? 16 : PR)>(r); }
+template <int PR> __device__ __forceinline__ int tile_at(int row, int col) {
+    return row * (PR * 8) + ((((col >> 3) ^ tile_bits<PR>(row)) << 3) | (col & 7));
+}
+
+// LDS by byte address
+__device__ __forceinline__ bf16x8 lds_piece(uint32_t at) {
+    return as_bf16x8(*reinterpret_cast<__attribute__((address_space(3))) const u32x4*>(at));
+}
+__device__ __forceinline__ bf16x8 lds_transposed(uint32_t first, uint32_t second) {
+    return join8(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(first)),
+                 __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(second)));
+}
+__device__ __forceinline__ void lds_store4(uint32_t at, u32x4 v) {
+    *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(at) = v;
+}
+__device__ __forceinline__ void lds_store2(uint32_t at, u32x2 v) {
+    *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(at) = v;
+}
+// The compiler would keep every address that a loop derives from `at` in a register of its
+// own; after this it derives them where they are used.
+__device__ __forceinline__ uint32_t fresh(uint32_t at) {
+    asm volatile("" : "+v"(at));
+    return at;
+}
+
+// What a rounding to bf16 left of the low and the high value of `pair`, exact: one
+// v_dot2_f32_bf16 each, with (-1, 0) or (0, -1), in place of a shift or mask and a
+// subtraction.  The factors come in registers: as a literal the low one is taken for the
+// inline constant -1.0, whose one is in the high half.
+struct Minus {
+    uint32_t low, high;
+    __device__ __forceinline__ Minus() : low(0x0000bf80u), high(0xbf800000u) { asm volatile("" : "+s"(low), "+s"(high)); }
+    static __device__ __forceinline__ float dot(uint32_t pair, uint32_t one, float v) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, one), v, false);
+    }
+    __device__ __forceinline__ uint32_t rest(float v, float w, uint32_t pair) const {   // rounded in turn
+        return pack2(dot(pair, low, v), dot(pair, high, w));
+    }
+};
+
+// v as a sum of bf16 parts: three, or two and no third
+__device__ __forceinline__ void split3(const float (&v)[8], const Minus& minus, bool three, bf16x8 (&o)[3]) {
+    u32x4 part[3] = {};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        part[0][e] = pack2(v[2 * e], v[2 * e + 1]);
+        const float lo = minus.dot(part[0][e], minus.low, v[2 * e]), hi = minus.dot(part[0][e], minus.high, v[2 * e + 1]);
+        part[1][e] = pack2(lo, hi);
+        if (three) part[2][e] = minus.rest(lo, hi, part[1][e]);
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) o[p] = as_bf16x8(part[p]);
+}
+// eight bf16 times w, split
+__device__ __forceinline__ void split3(const bf16x8& v, const float (&w)[8], const Minus& minus, bool three,
+                                       bf16x8 (&o)[3]) {
+    const u32x4 u = as_u32x4(v);
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f[2 * e] = w[2 * e] * __uint_as_float(u[e] << 16);
+        f[2 * e + 1] = w[2 * e + 1] * __uint_as_float(u[e] & 0xffff0000u);
+    }
+    split3(f, minus, three, o);
 }
 
 }  // namespace ssd

@@ -26,32 +26,6 @@
 namespace ssd {
 namespace {
 
-template <int PR> __device__ __forceinline__ int tile_bits(int r) { return swzbits<(PR > 16 ? 16 : PR)>(r); }
-template <int PR> __device__ __forceinline__ int tile_at(int row, int col) {
-    return row * (PR * 8) + ((((col >> 3) ^ tile_bits<PR>(row)) << 3) | (col & 7));
-}
-
-// LDS by byte address
-__device__ __forceinline__ bf16x8 lds_piece(uint32_t at) {
-    return as_bf16x8(*reinterpret_cast<__attribute__((address_space(3))) const u32x4*>(at));
-}
-__device__ __forceinline__ bf16x8 lds_transposed(uint32_t first, uint32_t second) {
-    return join8(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(first)),
-                 __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(second)));
-}
-__device__ __forceinline__ void lds_store4(uint32_t at, u32x4 v) {
-    *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(at) = v;
-}
-__device__ __forceinline__ void lds_store2(uint32_t at, u32x2 v) {
-    *reinterpret_cast<__attribute__((address_space(3))) u32x2*>(at) = v;
-}
-// The compiler would keep every address that a loop derives from `at` in a register of its
-// own; after this it derives them where they are used.
-__device__ __forceinline__ uint32_t fresh(uint32_t at) {
-    asm volatile("" : "+v"(at));
-    return at;
-}
-
 // A tile of C rows with PR pieces of 16 bytes each, brought from memory to LDS by W
 // wavefronts.  Its first row is memory row 0 of `base` (C - 1 against time), rows are rs
 // elements apart; rows before r0 are no part of the sequence.
@@ -126,39 +100,6 @@ template <int C, int PR, int W> struct Stage {
         }
     }
 };
-
-// What a rounding to bf16 left of the low and the high value of `pair`, exact: one
-// v_dot2_f32_bf16 each, with (-1, 0) or (0, -1), in place of a shift or mask and a
-// subtraction.  The factors come in registers: as a literal the low one is taken for the
-// inline constant -1.0, whose one is in the high half.
-struct Minus {
-    uint32_t low, high;
-    __device__ __forceinline__ Minus() : low(0x0000bf80u), high(0xbf800000u) { asm volatile("" : "+s"(low), "+s"(high)); }
-    static __device__ __forceinline__ float dot(uint32_t pair, uint32_t one, float v) {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, one), v, false);
-    }
-    __device__ __forceinline__ uint32_t rest(float v, float w, uint32_t pair) const {   // rounded in turn
-        return pack2(dot(pair, low, v), dot(pair, high, w));
-    }
-};
-
-// v (eight bf16) times w, as a sum of bf16 parts: three, or two and no third
-__device__ __forceinline__ void split3(const bf16x8& v, const float (&w)[8], const Minus& minus, bool three,
-                                       bf16x8 (&o)[3]) {
-    const u32x4 u = as_u32x4(v);
-    u32x4 part[3] = {};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float lo = w[2 * e] * __uint_as_float(u[e] << 16), hi = w[2 * e + 1] * __uint_as_float(u[e] & 0xffff0000u);
-        part[0][e] = pack2(lo, hi);
-        const float lo1 = minus.dot(part[0][e], minus.low, lo), hi1 = minus.dot(part[0][e], minus.high, hi);
-        part[1][e] = pack2(lo1, hi1);
-        if (three) part[2][e] = minus.rest(lo1, hi1, part[1][e]);
-    }
-#pragma unroll
-    for (int p = 0; p < 3; ++p) o[p] = as_bf16x8(part[p]);
-}
 
 // KD: contracted elements held (64, 128 or 256); NW state wavefronts, and as many others; C
 // steps to a chunk.  FULL: y and the last state; else the states at the segments' ends.

@@ -166,12 +166,14 @@ ChanBwdPlan chan_bwd_plan(const ChanShape& s) {
 
 // Segments of the linear attention's walks.  A walk of an instance takes `few` us for 64 steps
 // where its workgroups have the GPU nearly to themselves, `few` + `more` where `slots` of them
-// fill it, and `ends` where it only makes the segments' end states.  Fitted on MI355X to the
-// forward and the backward of 1 x 32768 to 8 x 2048 steps and 12 to 64 heads (bf16,
-// 128 x 128: 8 x 2048 x 32 heads 139 us, 1 x 32768 x 12 in 16, 21 and 40 segments 173, 160 and
-// 183 us, its backward in 7 and 21 390 and 404 us; within 8%).  What a last round that does
-// not fill the GPU would hold may be cut into segments while the rest stays whole: 8 x 2048 x 40
-// heads 223 us whole, 203 us with 64 pairs in four.
+// fill it, and `ends` where it only makes the segments' end states.  Fitted on MI355X to
+// the forward and the backward of 1 x 32768 to 8 x 2048 steps and 1 to 64 heads of all widths
+// (bf16, 128 x 128: 8 x 2048 x 32 heads 139 us, 1 x 32768 x 12 in 16, 21 and 40 segments 173, 160
+// and 183 us, its backward in 7 and 21 390 and 404 us; fp32: 2 x 2048 x 40 whole 261, in 3 and
+// 6 segments 161 and 190 us, 3 x 517 x 6 in 1, 5 and 9 62, 34 and 26 us; the chosen number is
+// within 10% of the best of those tried).  What a last round that does not fill the GPU would
+// hold may be cut into segments while the rest stays whole: 8 x 2048 x 40 heads 223 us whole,
+// 203 us with 64 pairs in four.
 AttnPlan attn_plan(const AttnShape& s, bool bwd) {
     struct Rate { double few, more, ends; int64_t slots; };
     const int kd = attn_width(s.Dk > s.Dv && bwd ? s.Dk : bwd ? s.Dv : s.Dk);
@@ -180,7 +182,11 @@ AttnPlan attn_plan(const AttnShape& s, bool bwd) {
                       : kd == 128 && !narrow ? Rate{3.0, 1.2, 1.6, 256}
                       : kd == 64 && narrow   ? Rate{2.5, 2.8, 1.5, 768}
                                              : Rate{3.0, 3.0, 1.8, 512};
-    const Rate f32 = kd == 256 ? Rate{30, 5, 15, 256} : kd == 128 ? Rate{12, 6, 6, 512} : Rate{6, 5, 3, 768};
+    const Rate f32 = kd == 256             ? Rate{narrow ? 19.0 : 16.5, 2.0, 9.0, 256}
+                     : kd == 128 && !narrow ? Rate{7.6, 2.4, 4.0, 256}
+                     : kd == 128            ? Rate{8.2, 1.2, 4.0, 256}
+                     : narrow               ? Rate{5.3, 3.0, 2.7, 512}
+                                            : Rate{5.5, 1.3, 2.7, 256};
     const Rate& t = s.bf16 ? bf16 : f32;
     AttnPlan p = {};
     const int64_t chunks = (s.L + 63) / 64, pairs = s.Bz * s.H, walks = bwd ? 3 : 1;
@@ -193,7 +199,7 @@ AttnPlan attn_plan(const AttnShape& s, bool bwd) {
     };
     double least = 1e300;
     int64_t each = chunks > 0 ? chunks : 1;
-    for (int64_t n = 1; n <= 512 && pairs > 0 && chunks > 0 && (n == 1 || 2 * n <= chunks); ++n) {
+    for (int64_t n = 1; n <= 512 && pairs > 0 && n <= chunks; ++n) {
         const int64_t e = (chunks + n - 1) / n, segs = (chunks + e - 1) / e;
         for (int64_t whole : {(int64_t)0, pairs * per / t.slots * t.slots / per}) {
             const int64_t cut = pairs - whole;

@@ -8,7 +8,10 @@ ulp, its exponent's corrected parts, the product), at most an addition per step 
 per contracted element (counted as an ulp, twice a rounding, as the matrix
 instructions' order and intermediate rounding are theirs), and a few products.
 In bf16 the decayed scores and the state are split into two bf16 parts (what is
-left out is below 2^-17 of the value), decayed rows into three (2^-26)."""
+left out is below 2^-17 of the value), decayed rows into three (2^-26).  In fp32 every
+factor is three bf16 parts and six of the nine products are formed: each part is at most
+2^-9 of the one before, so the three left out are below 2^-26 + 2^-26 + 2^-36 of the product,
+half a rounding, within the several that are counted for it."""
 import numpy as np
 
 from layer_ref import HALF, U, check, lengths, sigmoid  # noqa: F401

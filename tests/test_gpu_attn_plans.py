@@ -81,7 +81,7 @@ def test_plans(Bz, L, H, K, Dk, Dv, dtype, bwd, plan, ragged):
     log("linear attention plan %s" % ((Bz, L, H, K, Dk, Dv, dtype, bwd, plan, ragged),))
     d = inputs(Bz, L, H, K, Dk, Dv, dtype, seed=H, wide=8, lo=20.0, hi=2000.0)
     # ends inside a segment: the sequences' last and, in pairs that are cut, the second
-    lens = [L - 3, plan[1] + 37] if ragged else [L, L]
+    lens = [L - 3, plan[1] + 37][:Bz] if ragged else [L] * Bz
     seqlens = torch.tensor(lens, dtype=torch.int32, device="cuda") if ragged else None
     args = [d[n] for n in ("q", "k", "v", "decay")]
     if bwd:
