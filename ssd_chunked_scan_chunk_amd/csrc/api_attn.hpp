@@ -244,11 +244,8 @@ ssd_status ssd_linear_attn_bwd(const ssd_linear_attn_desc* desc, const void* q, 
     float* const slots[] = {states, adjoint, adjoint};
     hipError_t e = ssd::launch_attn_states(s, pl, ends, slots, 2, log_decay, seqlens, hs);
     if (e == hipSuccess) e = ssd::launch_attn_walks(s, pl, walks, slots, 3, log_decay, seqlens, hs);
-    if (e == hipSuccess && shared && rows > 0) {
-        e = ssd::launch_attn_share(static_cast<const float*>(pk.y), dk, rows, s.H, s.K, s.Dk, s.bf16, hs);
-        if (e == hipSuccess)
-            e = ssd::launch_attn_share(static_cast<const float*>(pv.y), dv, rows, s.H, s.K, s.Dv, s.bf16, hs);
-    }
+    if (e == hipSuccess && shared && rows > 0)
+        e = ssd::launch_attn_share(s, static_cast<const float*>(pk.y), static_cast<const float*>(pv.y), dk, dv, hs);
     return e == hipSuccess ? ok() : hip_fail(e, "linear attention backward launch");
 }
 

@@ -64,8 +64,8 @@ hipError_t launch_attn_states(const AttnShape& s, const AttnPlan& pl, const Attn
 // n walks (at most three); those of the same sizes side by side share a launch
 hipError_t launch_attn_walks(const AttnShape& s, const AttnPlan& pl, const AttnPass* p, float* const* slots, int n,
                              const float* log_decay, const int32_t* lens, hipStream_t st);
-// sums of each key and value head's heads: in [rows][H][D] fp32 -> out [rows][K][D]
-hipError_t launch_attn_share(const float* in, void* out, int64_t rows, int64_t H, int64_t K, int64_t D, bool bf16,
+// sums over each key and value head's heads: [Bz][L][H][..] fp32 -> dk, dv [Bz][L][K][..]
+hipError_t launch_attn_share(const AttnShape& s, const float* dk_heads, const float* dv_heads, void* dk, void* dv,
                              hipStream_t st);
 hipError_t launch_attn_step(const AttnShape& s, float* state, const void* q, const void* k, const void* v,
                             const float* log_decay, void* y, hipStream_t st);

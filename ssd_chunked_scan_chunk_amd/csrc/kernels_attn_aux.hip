@@ -33,9 +33,14 @@ __global__ __launch_bounds__(256) void k_attn_join(float* slots0, float* slots1,
     }
 }
 
+// Gradients of shared keys (blockIdx.y 0) and values (1): sums over the heads that share.
 template <typename T>
-__global__ __launch_bounds__(256) void k_attn_share(const float* in, T* out, int64_t n, int each, int D) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+__global__ __launch_bounds__(256) void k_attn_share(const float* in0, const float* in1, T* out0, T* out1, int64_t heads,
+                                                    int each, int D0, int D1) {
+    const float* in = blockIdx.y ? in1 : in0;
+    T* out = blockIdx.y ? out1 : out0;
+    const int D = blockIdx.y ? D1 : D0;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < heads * D; i += (int64_t)gridDim.x * 256) {
         const int64_t head = i / D;               // i: (row, shared head, element)
         const float* p = in + head * each * D + i % D;
         float v = 0.f;
@@ -170,12 +175,15 @@ hipError_t launch_attn_walks(const AttnShape& s, const AttnPlan& pl, const AttnP
     return launch_grouped(s, pl, p, slots, n, log_decay, lens, true, st);
 }
 
-hipError_t launch_attn_share(const float* in, void* out, int64_t rows, int64_t H, int64_t K, int64_t D, bool bf16,
+hipError_t launch_attn_share(const AttnShape& s, const float* dk_heads, const float* dv_heads, void* dk, void* dv,
                              hipStream_t st) {
-    const int64_t n = rows * K * D;
-    const unsigned grid = (unsigned)(n < (int64_t)65536 * 256 ? (n + 255) / 256 : 65536);
-    if (bf16) k_attn_share<<<grid, 256, 0, st>>>(in, static_cast<u16*>(out), n, (int)(H / K), (int)D);
-    else k_attn_share<<<grid, 256, 0, st>>>(in, static_cast<float*>(out), n, (int)(H / K), (int)D);
+    const int64_t heads = s.Bz * s.L * s.K, n = heads * (s.Dk > s.Dv ? s.Dk : s.Dv);
+    const dim3 grid((unsigned)(n < (int64_t)65536 * 256 ? (n + 255) / 256 : 65536), 2);
+    const int each = (int)(s.H / s.K), Dk = (int)s.Dk, Dv = (int)s.Dv;
+    if (s.bf16)
+        k_attn_share<<<grid, 256, 0, st>>>(dk_heads, dv_heads, static_cast<u16*>(dk), static_cast<u16*>(dv), heads, each, Dk, Dv);
+    else
+        k_attn_share<<<grid, 256, 0, st>>>(dk_heads, dv_heads, static_cast<float*>(dk), static_cast<float*>(dv), heads, each, Dk, Dv);
     return hipGetLastError();
 }
 

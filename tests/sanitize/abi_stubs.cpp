@@ -81,7 +81,7 @@ hipError_t launch_attn_states(const AttnShape&, const AttnPlan&, const AttnPass*
                               const int32_t*, hipStream_t) { SSD_STUB; }
 hipError_t launch_attn_walks(const AttnShape&, const AttnPlan&, const AttnPass*, float* const*, int, const float*,
                              const int32_t*, hipStream_t) { SSD_STUB; }
-hipError_t launch_attn_share(const float*, void*, int64_t, int64_t, int64_t, int64_t, bool, hipStream_t) { SSD_STUB; }
+hipError_t launch_attn_share(const AttnShape&, const float*, const float*, void*, void*, hipStream_t) { SSD_STUB; }
 hipError_t launch_attn_step(const AttnShape&, float*, const void*, const void*, const void*, const float*, void*,
                             hipStream_t) { SSD_STUB; }
 hipError_t launch_norm_fwd(const NormShape&, const NormIn&, void*, hipStream_t) { SSD_STUB; }
