@@ -405,11 +405,14 @@ ssd_status ssd_channel_step(const ssd_channel_desc* desc, float* state, const vo
  *   y, dy      [batch][seqlen][nheads][value_dim] dense
  * key_dim and value_dim are 1 to 256.  q, k, v, y and the gradients need the alignment of
  * an element.  Outputs must not overlap inputs, each other or the workspace.  States and
- * sums are float32 and y is rounded once; bf16 calls form decayed scores and
- * states' products from two bf16 parts, the decayed values from three.  Values are not
- * inspected: NaN and infinities stay within their (batch, head) and what is summed over
- * it, but may reach the up to 63 steps before theirs that share a chunk.  With
- * growing states (log_decay > 0) results overflow where e^(64 log_decay) does. */
+ * sums are float32 and y is rounded once.  Factors that are not bf16 are multiplied as sums of
+ * bf16 parts: in bf16 calls the decayed scores and the states' products with q, dy, v and k
+ * of two (17 bits), the decayed values that make final_state and dinitial_state of three (25
+ * bits), the other gradients' of two; in float32 calls every factor of three, which hold its 24 bits.
+ * Values are not inspected: NaN and infinities (which give NaN, in float32 calls as
+ * magnitudes above 3.38e38 do) stay within their (batch, head) and what is summed over it, but
+ * may reach the up to 63 steps before theirs that share a chunk (in dk and dv, after).  With
+ * growing states (log_decay > 0) results may be lost where e^(seqlen log_decay) overflows. */
 typedef struct ssd_linear_attn_desc {
     int64_t batch, seqlen, nheads, kv_heads, key_dim, value_dim;
     int64_t q_bstride, q_rstride, k_bstride, k_rstride, v_bstride, v_rstride; /* elements, >= 0 */

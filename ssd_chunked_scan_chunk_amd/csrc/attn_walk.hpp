@@ -18,6 +18,10 @@
 // y's error is the rounding of y itself; the decayed x, whose errors stay in the
 // states (an fp32 output), into three parts (25 bits).  One part each would put y
 // 1.7 roundings off in place of one and the states at 2e-3 in place of 1e-7.
+//
+// Bound by HBM where every CU has a workgroup (8 x 2048 x 32 heads of 128 x 128: 137 us, 4.0 of the
+// 4.5 TB/s of a large copy), else by the state wavefronts' chain, 6000 cycles to a chunk of 64 steps:
+// 2270 the product with the state, 760 that with the scores, 2800 the state's step.
 #pragma once
 #include <type_traits>
 
