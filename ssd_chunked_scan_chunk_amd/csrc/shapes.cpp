@@ -199,8 +199,10 @@ AttnPlan attn_plan(const AttnShape& s, bool bwd) {
     };
     double least = 1e300;
     int64_t each = chunks > 0 ? chunks : 1;
-    for (int64_t n = 1; n <= 512 && pairs > 0 && n <= chunks; ++n) {
+    // every length e of a segment once: 2 sqrt(chunks) of them
+    for (int64_t n = 1, next; n <= 512 && pairs > 0 && n <= chunks; n = next) {
         const int64_t e = (chunks + n - 1) / n, segs = (chunks + e - 1) / e;
+        next = e > 1 ? (chunks + e - 2) / (e - 1) : chunks + 1;
         for (int64_t whole : {(int64_t)0, pairs * per / t.slots * t.slots / per}) {
             const int64_t cut = pairs - whole;
             // the walks' workgroups, and the join's: 256 threads for 256 numbers of a state
