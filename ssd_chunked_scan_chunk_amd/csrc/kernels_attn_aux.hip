@@ -5,13 +5,20 @@
 namespace ssd {
 namespace {
 
+template <int V> struct StepVec;
+template <> struct StepVec<4> { typedef f32x4_any type; };
+template <> struct StepVec<1> { typedef float type __attribute__((ext_vector_type(1))); };
+
 // The states at the segments' ends, each from nothing but the first, to the states that
-// the next segments start from: one thread walks an element over the segments.
+// the next segments start from: one thread walks V elements over the segments, four where a
+// state holds whole fours (64 pairs of 128 x 128 in four segments: 6.4 us, one by one 15).
+template <int V>
 __global__ __launch_bounds__(256) void k_attn_join(float* slots0, float* slots1, const float* log_decay,
                                                    const int32_t* lens, int64_t L, int64_t H, int64_t whole,
                                                    int64_t nslots, int64_t steps, int64_t SE, unsigned blocks) {
+    using F = typename StepVec<V>::type;
     float* slots = blockIdx.y ? slots1 : slots0;
-    const int64_t i = blockIdx.x / blocks, s = whole + i, e = (int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x;
+    const int64_t i = blockIdx.x / blocks, s = whole + i, e = ((int64_t)(blockIdx.x % blocks) * 256 + threadIdx.x) * V;
     if (e >= SE) return;
     const int64_t len = attn_length(lens, s / H, L);
     const float f = decay_pow(log2_decay(log_decay[s % H]), (int)steps);   // every segment that another follows is whole
@@ -19,33 +26,38 @@ __global__ __launch_bounds__(256) void k_attn_join(float* slots0, float* slots1,
     // as many as have steps after them; eight reads in flight
     int64_t n = len > 0 ? (len - 1) / steps : 0;
     if (n > nslots) n = nslots;
-    float carry = 0.f;
+    F carry = {};
     for (int64_t k = 0; k < n; k += 8) {
-        float v[8];
+        F v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = p[(k + j < n ? k + j : n - 1) * SE];
+        for (int j = 0; j < 8; ++j) v[j] = *reinterpret_cast<const F*>(p + (k + j < n ? k + j : n - 1) * SE);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if (k + j >= n) break;
-            carry = k + j == 0 ? v[0] : fmaf(f, carry, v[j]);
-            p[(k + j) * SE] = carry;
+#pragma unroll
+            for (int x = 0; x < V; ++x) carry[x] = k + j == 0 ? v[0][x] : fmaf(f, carry[x], v[j][x]);
+            *reinterpret_cast<F*>(p + (k + j) * SE) = carry;
         }
     }
 }
 
-// Gradients of shared keys (blockIdx.y 0) and values (1): sums over the heads that share.
-template <typename T>
+// Gradients of shared keys (blockIdx.y 0) and values (1): sums over the heads that share, V
+// elements to a thread (3 x 1301 steps of 16 heads on 4 of 64 x 64: 6.2 us, one by one 9.3).
+template <typename T, int V>
 __global__ __launch_bounds__(256) void k_attn_share(const float* in0, const float* in1, T* out0, T* out1, int64_t heads,
                                                     int each, int D0, int D1) {
+    using F = typename StepVec<V>::type;
     const float* in = blockIdx.y ? in1 : in0;
     T* out = blockIdx.y ? out1 : out0;
     const int D = blockIdx.y ? D1 : D0;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < heads * D; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; i < heads * D; i += (int64_t)gridDim.x * 256 * V) {
         const int64_t head = i / D;               // i: (row, shared head, element)
         const float* p = in + head * each * D + i % D;
-        float v = 0.f;
-        for (int k = 0; k < each; ++k) v += p[(int64_t)k * D];
-        Elem<T>::store(out + i, v);
+        F v = {};
+        for (int k = 0; k < each; ++k) v += *reinterpret_cast<const F*>(p + (int64_t)k * D);
+        if constexpr (V == 1) Elem<T>::store(out + i, v[0]);
+        else if constexpr (sizeof(T) == 4) *reinterpret_cast<F*>(out + i) = v;
+        else *reinterpret_cast<u32x2_any*>(out + i) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
     }
 }
 
@@ -53,10 +65,6 @@ __global__ __launch_bounds__(256) void k_attn_share(const float* in0, const floa
 // once: 16 bytes to a lane, `lanes` of them (a power of two) to a row of keys, so that a
 // wavefront has 64 / lanes rows at a time and kUnroll such groups in flight.  256 requests of 40
 // heads of 128 x 128: 4.7 TB/s, 4 bytes to a lane 2.6.
-template <int V> struct StepVec;
-template <> struct StepVec<4> { typedef f32x4_any type; };
-template <> struct StepVec<1> { typedef float type __attribute__((ext_vector_type(1))); };
-
 __device__ __forceinline__ float row_sum(float v, int lanes) {
     for (int d = 1; d < lanes; d *= 2) v += __shfl_xor(v, d, 64);
     return v;
@@ -164,8 +172,10 @@ hipError_t launch_attn_states(const AttnShape& s, const AttnPlan& pl, const Attn
     const hipError_t e = launch_grouped(s, pl, p, slots, n, log_decay, lens, false, st);
     if (e != hipSuccess) return e;
     const int64_t SE = s.Dk * s.Dv;
-    const unsigned blocks = (unsigned)((SE + 255) / 256);
-    k_attn_join<<<dim3((unsigned)cut * blocks, (unsigned)n), 256, 0, st>>>(
+    const bool four = SE % 4 == 0;
+    const unsigned blocks = (unsigned)((SE + (four ? 1023 : 255)) / (four ? 1024 : 256));
+    auto join = four ? k_attn_join<4> : k_attn_join<1>;
+    join<<<dim3((unsigned)cut * blocks, (unsigned)n), 256, 0, st>>>(
         slots[0], n > 1 ? slots[1] : nullptr, log_decay, lens, s.L, s.H, pl.whole, pl.nseg - 1, pl.steps, SE, blocks);
     return hipGetLastError();
 }
@@ -177,13 +187,14 @@ hipError_t launch_attn_walks(const AttnShape& s, const AttnPlan& pl, const AttnP
 
 hipError_t launch_attn_share(const AttnShape& s, const float* dk_heads, const float* dv_heads, void* dk, void* dv,
                              hipStream_t st) {
-    const int64_t heads = s.Bz * s.L * s.K, n = heads * (s.Dk > s.Dv ? s.Dk : s.Dv);
-    const dim3 grid((unsigned)(n < (int64_t)65536 * 256 ? (n + 255) / 256 : 65536), 2);
-    const int each = (int)(s.H / s.K), Dk = (int)s.Dk, Dv = (int)s.Dv;
-    if (s.bf16)
-        k_attn_share<<<grid, 256, 0, st>>>(dk_heads, dv_heads, static_cast<u16*>(dk), static_cast<u16*>(dv), heads, each, Dk, Dv);
-    else
-        k_attn_share<<<grid, 256, 0, st>>>(dk_heads, dv_heads, static_cast<float*>(dk), static_cast<float*>(dv), heads, each, Dk, Dv);
+    const int V = s.Dk % 4 == 0 && s.Dv % 4 == 0 ? 4 : 1;
+    const int64_t heads = s.Bz * s.L * s.K, n = (heads * (s.Dk > s.Dv ? s.Dk : s.Dv) + 256 * V - 1) / (256 * V);
+    const dim3 grid((unsigned)(n < 65536 ? n : 65536), 2);
+    auto run = [&](auto kernel, auto* k, auto* v) {
+        kernel<<<grid, 256, 0, st>>>(dk_heads, dv_heads, k, v, heads, (int)(s.H / s.K), (int)s.Dk, (int)s.Dv);
+    };
+    if (s.bf16) run(V == 4 ? k_attn_share<u16, 4> : k_attn_share<u16, 1>, static_cast<u16*>(dk), static_cast<u16*>(dv));
+    else run(V == 4 ? k_attn_share<float, 4> : k_attn_share<float, 1>, static_cast<float*>(dk), static_cast<float*>(dv));
     return hipGetLastError();
 }
 
