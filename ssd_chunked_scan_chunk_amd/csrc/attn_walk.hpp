@@ -72,36 +72,58 @@ template <int C, int PR, int W> struct Copy {
     }
 };
 
-// Otherwise: read to registers at any alignment and length, put into the tile later.
+// Otherwise: read to registers at any alignment and length, put into the tile later.  A row's
+// last piece, if it is not whole, is read from where a whole one is left and shifted (Piece),
+// by lanes of its own, a row each: were all lanes to shift as one of a row needs to, 4 x 2048 x 32
+// heads of 109 x 99 would take 170 us, so they take 147 (104 x 104, aligned: 97).  Pieces past
+// it are cleared once.
 template <int C, int PR, int W> struct Stage {
     static constexpr int NTH = 64 * W, N = C * PR / NTH, RS = NTH / PR;   // pieces of a thread, rows between them
-    Piece<u16> piece;
-    int row0, col;
-    u32x4 v[N];
+    static constexpr int TR = C / W;                                      // rows whose last piece a wavefront takes
+    static_assert(TR <= 64, "one to a lane");
+    Piece<u16> last;
+    int row0, at, col, full, tail, trow;   // whole pieces of the tile's rows; 1 if a last one follows; its row, or -1: none for this lane
+    u32x4 v[N], t;
     __device__ __forceinline__ Stage(int wave, int lane, uint32_t, int, int col0, int d)
-        : piece(col0 + lane % PR * 8, d) {
+        : last(col0 + (d - col0) / 8 * 8, d) {
+        full = (d - col0) / 8 < PR ? (d - col0) / 8 : PR;
         row0 = (64 * wave + lane) / PR;
         col = lane % PR * 8;
+        at = full > 0 ? col0 + (col < 8 * full ? col : 0) : 0;   // read and dropped past them
+        tail = full < PR && d % 8 != 0 ? 1 : 0;
+        trow = tail && lane < TR ? wave * TR + lane : -1;
     }
     __device__ __forceinline__ void get(const u16* base, uint32_t rs, int rev, int r0, int d) {
-        const bool shortrow = d < 8;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            int r = row0 + k * RS;
+        auto row = [&](int r) {
             r = r < r0 ? r0 : r;
-            const u16* row = base + (uint32_t)(rev ? C - 1 - r : r) * rs;
-            if (!shortrow) v[k] = load16(row + piece.at);
-            else v[k] = piece.load_short(row, d);
+            return base + (uint32_t)(rev ? C - 1 - r : r) * rs;
+        };
+        const int tr = trow < 0 ? 0 : trow;    // read and dropped: a condition would have the read wait
+        if (d >= 8) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = load16(row(row0 + k * RS) + at);
+            t = load16(row(tr) + last.at);
+        } else {
+            t = last.load_short(row(tr), d);
         }
     }
-    __device__ __forceinline__ void clear(u16*, int) {}
-    __device__ __forceinline__ void put(const u16*, u16* tile, int r0, int) {
+    __device__ __forceinline__ void clear(u16* tile, int) const {
+        if (col >= 8 * (full + tail)) {    // not the last pieces: other wavefronts may have put them already
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int r = row0 + k * RS;
-            const u32x4 w = r < r0 ? u32x4{0, 0, 0, 0} : piece.shifted(v[k]);
-            *reinterpret_cast<u32x4*>(tile + tile_at<PR>(r, col)) = w;
+            for (int k = 0; k < N; ++k)
+                lds_store4(lds_addr(tile) + 2 * tile_at<PR>(row0 + k * RS, col), u32x4{0, 0, 0, 0});
         }
+    }
+    __device__ __forceinline__ void put(const u16*, u16* tile, int r0, int) {
+        if (col < 8 * full) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int r = row0 + k * RS;
+                lds_store4(lds_addr(tile) + 2 * tile_at<PR>(r, col), r < r0 ? u32x4{0, 0, 0, 0} : v[k]);
+            }
+        }
+        if (trow >= 0)
+            lds_store4(lds_addr(tile) + 2 * tile_at<PR>(trow, 8 * full), trow < r0 ? u32x4{0, 0, 0, 0} : last.shifted(t));
     }
 };
 
@@ -168,6 +190,9 @@ __device__ __forceinline__ void walk(const AttnArgs& A, const AttnPass& P, const
         const u16* Ab = FULL ? static_cast<const u16*>(P.a) + w.b * P.ab + (w.h / P.ag) * P.cd : nullptr;
         const u16* Cb = static_cast<const u16*>(P.c) + w.b * P.cb + (w.h / P.cg) * P.cd;
         const u16* Xb = static_cast<const u16*>(P.x) + w.b * P.xb + (w.h / P.xg) * P.xd;
+        // through registers: a chunk ahead of their place in LDS (backward of 2 x 1024 x 20 heads of 109 x 99
+        // 82 us, else 92; 256 wide it costs more spills than it hides: 301 us at 250 x 222, else 295)
+        constexpr bool AHEAD = !FAST && KD < 256;
         using RowsC = typename std::conditional<FAST, Copy<C, CPR, W>, Stage<C, CPR, W>>::type;
         using RowsX = typename std::conditional<FAST, Copy<C, XPR, W>, Stage<C, XPR, W>>::type;
         RowsC ga(at, lane, P.ar, rev, 0, P.cd), gc(at, lane, P.cr, rev, 0, P.cd);
@@ -201,18 +226,22 @@ __device__ __forceinline__ void walk(const AttnArgs& A, const AttnPass& P, const
                 get_ac(c0 + 1);
                 put_ac(c0 + 1, 1);
             }
+            if (AHEAD && c0 + 1 < c1) get_x(c0 + 1);
+            if (AHEAD && c0 + 2 < c1) get_ac(c0 + 2);
         }
-        vm_wait_all();
+        if constexpr (FAST) vm_wait_all();
         sync_lds();                    // the first two chunks' a and c, the first's x
         sync_lds();                    // the first chunk's scores
         int b3 = 2;                    // chunk c + 2's tiles
         for (int c = c0; c < c1; ++c) {
-            if (c + 1 < c1) get_x(c + 1);
-            if (c + 2 < c1) get_ac(c + 2);
+            if (!AHEAD && c + 1 < c1) get_x(c + 1);
+            if (!AHEAD && c + 2 < c1) get_ac(c + 2);
             if (c + 1 < c1) put_x(c + 1, (c + 1 - c0) & 1);
             if (c + 2 < c1) put_ac(c + 2, b3);
+            if (AHEAD && c + 2 < c1) get_x(c + 2);
+            if (AHEAD && c + 3 < c1) get_ac(c + 3);
             b3 = b3 == 2 ? 0 : b3 + 1;
-            vm_wait_all();             // they have landed
+            if constexpr (FAST) vm_wait_all();  // they have landed
             sync_lds();
         }
         return;
@@ -452,12 +481,23 @@ __device__ __forceinline__ void walk(const AttnArgs& A, const AttnPass& P, const
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const u32x4 v = as_u32x4(acc_half(Y[I], h));
+                    if (x + 16 * h + 8 <= P.xd) {
+                        if constexpr (YF) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (x + 16 * h + e < P.xd) {
-                            if constexpr (YF) reinterpret_cast<float*>(y)[16 * h + e] = Y[I][8 * h + e];
-                            else reinterpret_cast<u16*>(y)[16 * h + e] = (u16)(v[e / 2] >> (16 * (e & 1)));
+                            for (int e = 0; e < 8; e += 4)
+                                *reinterpret_cast<f32x4_any*>(y + 4 * (16 * h + e)) =
+                                    f32x4{Y[I][8 * h + e], Y[I][8 * h + e + 1], Y[I][8 * h + e + 2], Y[I][8 * h + e + 3]};
+                        } else {
+                            *reinterpret_cast<u32x4_any*>(y + 2 * 16 * h) = v;
                         }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (x + 16 * h + e < P.xd) {
+                                if constexpr (YF) reinterpret_cast<float*>(y)[16 * h + e] = Y[I][8 * h + e];
+                                else reinterpret_cast<u16*>(y)[16 * h + e] = (u16)(v[e / 2] >> (16 * (e & 1)));
+                            }
+                    }
                 }
             }
         }
