@@ -96,6 +96,21 @@ def test_plans(Bz, L, H, K, Dk, Dv, dtype, bwd, plan, ragged):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Bz,L,H,K,Dk,Dv", [(2, 330, 2, 1, 203, 131), (2, 330, 3, 3, 109, 99), (2, 200, 2, 2, 5, 250),
+                                            (2, 330, 2, 2, 134, 64), (2, 200, 4, 2, 63, 9), (2, 330, 1, 1, 250, 222)])
+def test_rows_of_any_length(dtype, Bz, L, H, K, Dk, Dv):
+    # last pieces that are not whole, in both slices of columns, over many chunks
+    log("linear attention rows %s" % ((dtype, Bz, L, H, K, Dk, Dv),))
+    d = inputs(Bz, L, H, K, Dk, Dv, dtype, seed=Dk, wide=3, lo=20.0, hi=2000.0)
+    lens = [L - 1, 97]
+    got = calls(d, lens)
+    torch.cuda.synchronize()
+    for bwd in (False, True):
+        for name, (want, err) in expected(d, lens, dtype, bwd).items():
+            check(name, got[name], want, err, "f32" if "state" in name else dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_far_apart(dtype):
     # batches more than 2^32 bytes apart, and steps of the longest stride: offsets beyond 32 bits
     log("linear attention far apart %s" % dtype)
