@@ -165,3 +165,29 @@ def test_threads_and_graphs_side_by_side():
         for i in order:
             for n in wants[i]:
                 assert torch.equal(helds[i][n], wants[i][n]), (i, n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_what_a_workspace_held_before_does_not_matter(dtype):
+    # of NaN: segments that end early, shared heads, sequences of nothing; the norm's parts
+    log("linear attention and group norm, workspaces of NaN %s" % dtype)
+    d = inputs(3, 900, 4, 2, 64, 40, dtype, seed=4, wide=8)
+    args = [d[n] for n in ("q", "k", "v", "decay")]
+    lens = torch.tensor([900, 0, 333], dtype=torch.int32, device="cuda")
+    nans = lambda n: torch.full((n,), 255, dtype=torch.uint8, device="cuda")   # noqa: E731
+    kw = dict(initial_state=d["first"], seqlens=lens)
+    fwd, bwd = ssd.linear_attn_fwd_workspace_bytes(*args), ssd.linear_attn_bwd_workspace_bytes(*args)
+    assert fwd > 0 and bwd > 0
+    y, s = ssd.linear_attn_fwd(*args, return_final_state=True, **kw)
+    y2, s2 = ssd.linear_attn_fwd(*args, return_final_state=True, workspace=nans(fwd), **kw)
+    kw.update(dfinal_state=d["dlast"], return_dinitial_state=True)
+    g, g2 = ssd.linear_attn_bwd(*args, d["dy"], **kw), ssd.linear_attn_bwd(*args, d["dy"], workspace=nans(bwd), **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(s, s2) and all(torch.equal(g[n], g2[n]) for n in g)
+    x, w = d["dy"].flatten(2), torch.ones(160, device="cuda")
+    for groups in (1, 4, 40):
+        kw = dict(weight=w, bias=w, seqlens=lens)
+        ws = nans(ssd.group_norm_bwd_workspace_bytes(x, groups))
+        g, g2 = ssd.group_norm_bwd(x, groups, y.flatten(2), **kw), ssd.group_norm_bwd(x, groups, y.flatten(2), workspace=ws, **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(g[n], g2[n]) for n in ("dx", "dweight", "dbias"))
