@@ -250,8 +250,10 @@ __device__ __forceinline__ void walk(const AttnArgs& A, const AttnPass& P, const
         // ================= scores =================
         const int at = tid - 64 * NW;
         if (at < 64) {
+            // powers past the sequence's length meet nothing but its missing rows' zeros: 0, as growth
+            // may make infinities of them that the sequence itself does not reach
             for (int n = at; n <= C; n += 64) {
-                const float p = decay_pow(gamma, n);
+                const float p = n <= w.len ? decay_pow(gamma, n) : 0.f;
                 sG[n] = p;
                 if (n < C) {
                     sGp[32 + n] = P.scale_p * p;

@@ -118,7 +118,7 @@ __global__ __launch_bounds__(128 * NW, (f32_waves<KD, NW>())) void k_attn_f32(co
         // ================= rows and scores =================
         const int at = tid - NTH;
         if (at <= kC) {
-            const float p = decay_pow(g, at);
+            const float p = at <= w.len ? decay_pow(g, at) : 0.f;   // see attn_walk.hpp
             sG[at] = p;
             if (at < kC) {
                 sGp[at] = P.scale_p * p;
