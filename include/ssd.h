@@ -486,7 +486,8 @@ ssd_status ssd_group_norm_fwd(const ssd_group_norm_desc* desc, const void* x, co
 /* Gradients for the upstream dy: dx and dgate [batch][seqlen][channels] dense in the
  * call's dtype, dweight and dbias float32 (dgate, dweight and dbias required exactly
  * when their input is given).  Sums over rows are formed in a fixed order (repeated calls
- * give the same bits); the workspace holds their parts. */
+ * give the same bits); the workspace holds their parts, and may be NULL without weight and
+ * bias. */
 ssd_status ssd_group_norm_bwd_workspace_bytes(const ssd_group_norm_desc* desc, size_t* bytes);
 ssd_status ssd_group_norm_bwd(const ssd_group_norm_desc* desc, const void* x, const float* weight,
                               const float* bias, const void* gate, const int32_t* seqlens,

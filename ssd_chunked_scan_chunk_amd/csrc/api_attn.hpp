@@ -310,7 +310,7 @@ ssd_status ssd_group_norm_bwd(const ssd_group_norm_desc* desc, const void* x, co
     SSD_CHECK(check_aligned("dgate", dgate, es));
     SSD_CHECK(check_aligned("dweight", dweight, 4));
     SSD_CHECK(check_aligned("dbias", dbias, 4));
-    const size_t need = norm_bwd_bytes(s);
+    const size_t need = dweight || dbias ? norm_bwd_bytes(s) : 0;
     SSD_CHECK(check_workspace(workspace, workspace_bytes, need));
     r[kNormIn] = rng("dy", dy, n);
     const Range out[] = {rng("dx", dx, n), rng("dgate", dgate, n), rng("dweight", dweight, s.C * 4),

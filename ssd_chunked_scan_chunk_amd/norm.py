@@ -68,12 +68,16 @@ def group_norm_bwd(x, groups, dy, weight=None, bias=None, gate=None, eps=1e-5, c
     """Gradients of group_norm_fwd for upstream dy (x's shape, contiguous).
 
     Returns a dict with dx and dgate (x's dtype), dweight and dbias (f32); dgate,
-    dweight and dbias are None without their input."""
+    dweight and dbias are None without their input, and without weight and bias no
+    workspace is used."""
     d = _norm_check(x, groups, weight, bias, gate, eps, center, silu, gate_first)
     _need("dy", dy)
     _same("dy", dy, x.shape, x.dtype, x.device)
     _norm_lens(seqlens, x)
-    workspace, wsz = _workspace(workspace, _norm_bytes(d), x.device)
+    if workspace is None and weight is None and bias is None:
+        wsz = 0
+    else:
+        workspace, wsz = _workspace(workspace, _norm_bytes(d), x.device)
     g = {"dx": x.new_empty(x.shape), "dgate": x.new_empty(x.shape) if gate is not None else None,
          "dweight": torch.empty_like(weight) if weight is not None else None,
          "dbias": torch.empty_like(bias) if bias is not None else None}
