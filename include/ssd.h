@@ -409,7 +409,8 @@ ssd_status ssd_channel_step(const ssd_channel_desc* desc, float* state, const vo
  * bf16 parts: in bf16 calls the decayed scores and the states' products with q, dy, v and k
  * of two (17 bits), the decayed values that make final_state and dinitial_state of three (25
  * bits), the other gradients' of two; in float32 calls every factor of three, which hold its 24 bits
- * (fewer of magnitudes below 2^-110).
+ * (fewer of magnitudes below 2^-110), in six of their nine products (the others are below 2^-24 of
+ * the whole).
  * Values are not inspected: NaN and infinities (which give NaN, in float32 calls as
  * magnitudes above 3.38e38 do) stay within their (batch, head) and what is summed over it, but
  * may reach the up to 63 steps before theirs that share a chunk (in dk and dv, after).  With
