@@ -412,7 +412,7 @@ ssd_status ssd_channel_step(const ssd_channel_desc* desc, float* state, const vo
  * (fewer of magnitudes below 2^-110), in six of their nine products (the others are below 2^-24 of
  * the whole).
  * Values are not inspected: NaN and infinities (which give NaN, in float32 calls as
- * magnitudes above 3.38e38 do) stay within their (batch, head) and what is summed over it, but
+ * factors above 3.38e38 do) stay within their (batch, head) and what is summed over it, but
  * may reach the up to 63 steps before theirs that share a chunk (in dk and dv, after).  With
  * growing states (log_decay > 0) results may be lost where e^(seqlen log_decay) overflows. */
 typedef struct ssd_linear_attn_desc {
