@@ -461,7 +461,9 @@ ssd_status ssd_linear_attn_step(const ssd_linear_attn_desc* desc, float* state, 
  *     y = act(p) without a gate, p act(gate) with one, p if gate_first
  * (a group per head after linear attention; gate_first without center for the
  * state space layer).  The statistics are each row's own, in float32, the mean before
- * the squares about it; y is rounded once.
+ * the squares about it; y is rounded once.  Squares beyond float32's range are lost: where their
+ * sum overflows (values about the mean above 1.8e19 / sqrt(m)) n is 0, and those below 1e-19 count
+ * for nothing beside eps.
  *   x, gate       rows of `channels` elements at b*bstride + t*rstride
  *   weight, bias  [channels] float32 or NULL (1, 0); gate NULL: none
  *   seqlens       as above: rows behind a sequence's end are not read and are in no sum; y

@@ -74,3 +74,20 @@ def test_infinities_stay_in_their_group(dtype, C, groups, gate_first, name, valu
     # where the definition has no finite value, none is made up
     bad = {"x": "y", "gate": "y", "dy": "dx"}[name]
     assert not bool(got[bad][1, 3, 1].isfinite())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("C,groups", SIZES)
+def test_squares_beyond_the_range(dtype, C, groups):
+    # sums of squares that overflow leave n = 0, the row's bias; in that group alone
+    log("group norm squares %s" % ((dtype, C, groups),))
+    d = inputs(2, 5, C, dtype, seed=C, gate=False)
+    m = C // groups
+    clean = calls(d, groups, silu=False)
+    d["x"][1, 3, 0] = 1e25
+    got = calls(d, groups, silu=False)
+    torch.cuda.synchronize()
+    assert torch.equal(got["y"][1, 3, :m], d["bias"][:m].to(DT[dtype]))
+    a, b = got["y"].clone(), clean["y"].clone()
+    a[1, 3, :m], b[1, 3, :m] = 0, 0
+    assert torch.equal(a, b) and all(bool(t.isfinite().all()) for t in got.values() if t is not None)
