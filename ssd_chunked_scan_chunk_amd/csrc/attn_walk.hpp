@@ -1,10 +1,11 @@
 // attn_walk.hpp -- linear attention with a decay per head, bf16: one walk over the
-// sequences in chunks of 64 steps (AttnPass in attn_launch.hpp has the recurrence).
+// sequences in chunks of C steps, 64 where 128 x 128 elements are held and 32 otherwise
+// (AttnPass in attn_launch.hpp has the recurrence).
 //
 // With gamma the head's decay and S the state before the chunk,
 //     y_i = sum_{j<=i} gamma^(i-j) (a_i . c_j) x_j + gamma^(i+1) S a_i
-//     S'  = gamma^64 S + sum_j gamma^(63-j) x_j c_j^T
-// (in chunks of 32 or 64 steps) on v_mfma_f32_32x32x16_bf16.  A workgroup owns a (batch,
+//     S'  = gamma^C S + sum_j gamma^(C-1-j) x_j c_j^T
+// on v_mfma_f32_32x32x16_bf16.  A workgroup owns a (batch,
 // head), 64 or 128 columns x and a segment of the chunks.  Each of its state wavefronts keeps 32
 // columns of the state in accumulators.  As many more wavefronts bring the rows to LDS, two
 // chunks ahead, and form the decayed scores, one chunk ahead: neither the copies, which hold
@@ -14,14 +15,17 @@
 //
 // Precision.  The rows are bf16 and their products exact, but three factors are made
 // here and have to be rounded to multiply on: the decayed scores and the state in
-// the product with a are split into a high and a low bf16 part (17 bits), so that
-// y's error is the rounding of y itself; the decayed x, whose errors stay in the
-// states (an fp32 output), into three parts (25 bits).  One part each would put y
+// the product with a are split into a high and a low bf16 part (17 bits); the decayed x,
+// whose errors stay in the states (an fp32 output), into three parts (25 bits), or two
+// where no state is asked for (dq, dk).  y is off by its own rounding, 2^-8 of it, and by 2^-17
+// of the sum of its terms' magnitudes, of which the rounding is the larger unless they cancel
+// to less than 2^-9 of that sum (32-bit factors would leave 2^-24 of it).  One part each would put y
 // 1.7 roundings off in place of one and the states at 2e-3 in place of 1e-7.
 //
 // Bound by HBM where every CU has a workgroup (8 x 2048 x 32 heads of 128 x 128: 137 us, 4.0 of the
 // 4.5 TB/s of a large copy), else by the state wavefronts' chain, 6000 cycles to a chunk of 64 steps:
-// 2270 the product with the state, 760 that with the scores, 2800 the state's step.
+// 2270 the product with the state, 760 that with the scores, 2800 the state's step.  256 wide, a
+// lane holds 128 numbers of the state, and four wavefronts of it spill, 44 to 52 bytes a lane.
 #pragma once
 #include <type_traits>
 

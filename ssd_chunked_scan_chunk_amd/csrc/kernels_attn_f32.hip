@@ -3,12 +3,14 @@
 //
 // Every factor of its products is the sum of three bf16 parts, which hold its 24 bits (their
 // rests are exact), and six of the nine products of parts are formed, on
-// v_mfma_f32_32x32x16_bf16 (the scores on 16x16x32): the second part is up to 2^-8 of a value and the
-// third up to 2^-17, so what the other three leave out is below 2^-24 of a product, one rounding.  Six of these take 3/8 of the time of the fp32
-// instructions for the same elements; a forward of 8 x 2048 x 32 heads of 128 x 128 took 595 us
-// with those, 440 with the parts, and takes 322 with wavefronts of their own for the rows and
-// the scores (floor 240: what is left is the state wavefronts' chain, at 40% of the matrix
-// units' time and a third of the vector units').  What is infinite, or would round to it in
+// v_mfma_f32_32x32x16_bf16 (the scores on 16x16x32): the second part is up to 2^-8 of a
+// value and the third up to 2^-17, so what the other three leave out is below 2^-24 of a
+// product, one rounding.  Six of these take 3/8 of the time of the fp32 instructions for the
+// same elements; a forward of 8 x 2048 x 32 heads of 128 x 128 took 595 us with those, 440
+// with the parts, and takes 322 with wavefronts of their own for the rows and the scores
+// (floor 240: what is left is the state wavefronts' chain, at 40% of the matrix units' time
+// and a third of the vector units').  256 wide, a lane holds 128 numbers of the state and
+// four wavefronts of it spill, 52 to 64 bytes a lane.  What is infinite, or would round to it in
 // bf16, has no such parts and gives NaN.
 #include "attn_util.hpp"
 

@@ -82,6 +82,8 @@ template <typename T> struct Vec<T, 1> {
 __device__ __forceinline__ u16 to_elem(float v, u16) { return f32_to_bf_bits(v); }
 __device__ __forceinline__ float to_elem(float v, float) { return v; }
 
+// The exponential and the reciprocal are the hardware's, an ulp each; in fp32 the exponential's
+// argument is in two parts, as its rounding alone would move a sigmoid by |x| roundings.
 template <typename T> __device__ __forceinline__ float sigmoid_as(float x) {
     if constexpr (sizeof(T) == 2) return sigmoid_of(x);
     const float e = exp_neg_abs<true>(x), d = __builtin_amdgcn_rcpf(1.f + e);
@@ -91,6 +93,10 @@ template <typename T> __device__ __forceinline__ float sigmoid_as(float x) {
 // GATE: 0 none, 1 after the norm, 2 before it.  WHOLE: a group is a whole number of pieces;
 // otherwise its last one starts early and its first `skip` elements are another thread's
 // (with that test at every element the bf16 backward needs 121 registers and 10% longer).
+// 16 channels a lane (groups above 8192) do not fit the backward's 128 registers: 396 to 484 bytes
+// of scratch with a gate, 120 to 208 without (2 x 2048 x 16384 gated bf16 742 us, floor 148; fp32
+// 2 x 1024 x 16384 530, floor 148), and up to 60 in the gated fp32 forward (104 us, floor 89).  8 of
+// them in fp32 (groups above 4096) spill 20 to 28 bytes: 4 x 2048 x 5120, gate first, 177 us.
 template <typename T, int V, int NP, bool BLOCK, int GATE, bool BWD, bool WHOLE>
 __global__ __launch_bounds__(BLOCK ? 1024 : 512, BWD ? 4 : 1) void k_norm(const NormArgs A) {
     using R = typename Vec<T, V>::raw;
@@ -290,7 +296,7 @@ __global__ __launch_bounds__(BLOCK ? 1024 : 512, BWD ? 4 : 1) void k_norm(const 
         bool mine = on;
         if constexpr (!BLOCK) {
             // Rows beside each other in a workgroup add their columns up here.  With a part for each
-            // of them (up to 128) the sum over the parts read more than the rows hold: 4 x 2048
+            // of them (up to 256) the sum over the parts read more than the rows hold: 4 x 2048
             // rows of 64 channels took 211 us, now 22, 100000 fp32 rows of 8 channels 1637, now 35.
             if (A.rw > 1) {
                 __shared__ float part[2][512];
