@@ -36,7 +36,10 @@ struct AttnPass {
     float scale_p, scale_in, scale_w;
     int rev, y_f32;
     int exact;                           // bf16: states to 25 bits, as they are results, not to 17 (y is
-                                         // rounded to 8; the same whether `last` is asked for)
+                                         // rounded to 8; the same whether `last` is asked for).  A
+                                         // backward of 4 x 2048 x 40 heads of 128 x 128 with it for
+                                         // dq and dk too: 245 us, else 238; the error of each against
+                                         // 64 bits is the same, its rounding's
 };
 // The first `whole` (batch, head) pairs are walked in one piece, the others in nseg segments
 // of `steps` steps (whole chunks of every walk's).  The workspace: the states at the
